@@ -32,7 +32,7 @@ STATUS_NAMES = {0: "KDA_OK", 1: "KDA_ERR_NULL", 2: "KDA_ERR_SHAPE", 3: "KDA_ERR_
                 7: "KDA_ERR_CKPT_RANGE", 8: "KDA_ERR_SEQ", 9: "KDA_ERR_WORKSPACE",
                 10: "KDA_ERR_HIP", 11: "KDA_ERR_POOL", 12: "KDA_ERR_PINNED",
                 13: "KDA_ERR_NOT_FOUND"}
-KDA_F32, KDA_BF16 = 0, 1
+KDA_F32, KDA_BF16, KDA_INT8 = 0, 1, 2  # KDA_INT8: stored type of a kv pool only
 HASH_BLOCK = 512
 CHUNK = 64
 
@@ -42,6 +42,9 @@ EXPORTS = ("kda_version", "kda_last_error", "kda_pool_check", "kda_state_offset"
            "kda_checkpoint_write", "kda_checkpoint_restore", "kda_ckpt_int8_head_bytes",
            "kda_checkpoint_write_int8", "kda_checkpoint_restore_int8",
            "kda_conv_workspace_bytes", "kda_short_conv", "kda_short_conv_update", "kda_profile_enable", "kda_profile_read",
+           "kda_kv_pool_check", "kda_kv_head_bytes", "kda_kv_workspace_bytes", "kda_kv_append",
+           "kda_kv_append_step", "kda_kv_read", "kda_attn_prefill_workspace_bytes", "kda_attn_prefill",
+           "kda_attn_decode_workspace_bytes", "kda_attn_decode",
            "kda_xxh64", "kda_chain_hashes", "kda_ckpt_plan", "kda_index_create",
            "kda_index_destroy", "kda_index_register_pages", "kda_index_register_ckpt",
            "kda_index_mark_ready", "kda_index_lookup", "kda_index_release", "kda_index_evict_page",
@@ -66,6 +69,18 @@ class kda_conv_pool(ctypes.Structure):
                 ("width", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class kda_kv_pool(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64),
+                ("num_pages", ctypes.c_int32), ("num_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
+class kda_rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("num_pos", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 class kda_hit(ctypes.Structure):
     _fields_ = [("boundary", ctypes.c_int64), ("mla_tokens", ctypes.c_int64),
                 ("num_pages", ctypes.c_int32), ("pad", ctypes.c_int32),
@@ -84,6 +99,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 
 _P, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _PP = ctypes.POINTER(kda_pool)
+_PKV, _PR = ctypes.POINTER(kda_kv_pool), ctypes.POINTER(kda_rope)
 _sig = {
     "kda_version": (_i32, []),
     "kda_last_error": (ctypes.c_char_p, []),
@@ -111,6 +127,20 @@ _sig = {
                                       _P, _P, _P, _P, _P, _P, _P, _i32, _P, _sz, _P]),
     "kda_short_conv_update": (ctypes.c_int, [ctypes.POINTER(kda_conv_pool), _P, _P, _P, ctypes.c_int,
                                              _i32, _P, _P, _P]),
+    "kda_kv_pool_check": (ctypes.c_int, [_PKV]),
+    "kda_kv_head_bytes": (_i64, [_i32, _i32, ctypes.c_int]),
+    "kda_kv_workspace_bytes": (_i64, [_i32]),
+    "kda_kv_append": (ctypes.c_int, [_PKV, _PR, _P, _P, _P, ctypes.c_int, _i64, _i64, _i64, _P, _i32, _i32,
+                                     _P, _P, _P, _i32, _P, _sz, _P]),
+    "kda_kv_append_step": (ctypes.c_int, [_PKV, _PR, _P, _P, _P, ctypes.c_int, _i64, _i64, _i64, _P, _i32,
+                                          _i32, _i32, _P, _P, _i32, _P]),
+    "kda_kv_read": (ctypes.c_int, [_PKV, _P, _P, ctypes.c_int, _i32, _P, _P, _P, _i32, _P, _sz, _P]),
+    "kda_attn_prefill_workspace_bytes": (_sz, [_PKV, _i32, _i32, _P, _P, _i32, _i32]),
+    "kda_attn_prefill": (ctypes.c_int, [_PKV, _P, ctypes.c_int, _i64, _P, ctypes.c_int, _i32,
+                                        ctypes.c_float, _i32, _i32, _i32, _P, _P, _P, _i32, _P, _sz, _P]),
+    "kda_attn_decode_workspace_bytes": (_sz, [_PKV, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "kda_attn_decode": (ctypes.c_int, [_PKV, _P, ctypes.c_int, _i64, _P, ctypes.c_int, _i32, ctypes.c_float,
+                                       _i32, _i32, _i32, _i32, _P, _P, _i32, _P, _sz, _P]),
     "kda_xxh64": (ctypes.c_uint64, [_P, _i64, ctypes.c_uint64]),
     "kda_chain_hashes": (_i64, [_P, _i64, _i32, ctypes.c_uint64, _P, _i64]),
     "kda_ckpt_plan": (_i64, [_i64, _i64, _i32]),
@@ -405,6 +435,175 @@ def kda_short_conv_update(cpool, x, w, y, page_in, page_out, *, n=None, out_dtyp
     st = _lib.kda_short_conv_update(ctypes.byref(cpool), _dptr(x), _dptr(w), _dptr(y), outd, n,
                                     _dptr(page_in), _dptr(page_out), _stream(stream))
     _check(st)
+
+
+# ---- paged key/value cache and its attention -----------------------------------
+def make_kv_pool(base, page_bytes: int, num_pages: int, num_heads: int, head_dim: int, page_tokens: int,
+                 dtype: int):
+    """Key/value pool descriptor over caller-owned device memory (KDA_BF16 or KDA_INT8)."""
+    return kda_kv_pool(_dptr(base), int(page_bytes), int(num_pages), int(num_heads), int(head_dim),
+                       int(page_tokens), int(dtype))
+
+
+def make_rope(cos, sin, *, interleaved: bool = False):
+    """Rotation descriptor over caller-owned fp32 device tables [positions, rot_dim / 2]."""
+    if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32:
+        raise ValueError("cos and sin must be float32 tables of one shape [positions, rot_dim / 2]")
+    return kda_rope(_dptr(cos), _dptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(interleaved)))
+
+
+def _rows(name, x, heads, d, rows=None, dtype=None):
+    """(pointer, row distance in elements) of a [T, heads, d] tensor on the current device whose
+    rows are contiguous (they may be columns of a wider tensor)."""
+    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} must be a tensor of the current device")
+    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or (rows is not None and x.shape[0] != rows):
+        raise ValueError(f"{name} must be [{'T' if rows is None else rows}, {heads}, {d}] (got {tuple(x.shape)})")
+    if dtype is not None and x.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} (got {x.dtype})")
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+        raise ValueError(f"{name}: the heads of a row must be contiguous")
+    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else heads * d
+
+
+def _out(name, x, heads, d, rows):
+    ptr, ld = _rows(name, x, heads, d, rows)
+    if ld != heads * d:
+        raise ValueError(f"{name} must be contiguous")
+    return ptr
+
+
+def _table(page_table, n):
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n:
+        raise ValueError(f"page_table must be an int32 device tensor [{n}, max_pages]")
+    if page_table.device.index != torch.cuda.current_device():
+        raise ValueError("page_table must be on the current device")
+    return _dptr(page_table), page_table.shape[1]
+
+
+def _pos(pos, n=None):
+    if pos.dtype != torch.int32 or pos.dim() != 1 or (n is not None and pos.shape[0] != n):
+        raise ValueError("pos must be an int32 device tensor [n]")
+    if pos.device.index != torch.cuda.current_device():
+        raise ValueError("pos must be on the current device")
+    return _dptr(pos)
+
+
+def _packed(cu_seqlens, start_pos):
+    cu, sp = _HostArr(cu_seqlens, np.int64), _HostArr(start_pos, np.int64)
+    if cu.a.ndim != 1 or len(cu.a) < 1:
+        raise ValueError("cu_seqlens must hold num_seqs + 1 entries")
+    _need_len("start_pos", sp, len(cu.a) - 1)
+    return cu, sp, len(cu.a) - 1
+
+
+def _ws(workspace):
+    return _dptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def kda_kv_pool_check(pool: kda_kv_pool) -> int:
+    return int(_lib.kda_kv_pool_check(ctypes.byref(pool)))
+
+
+def kda_kv_head_bytes(head_dim: int, page_tokens: int, dtype: int) -> int:
+    """Bytes of one head in a key/value page; -1 if unsupported."""
+    return int(_lib.kda_kv_head_bytes(head_dim, page_tokens, dtype))
+
+
+def kda_kv_workspace_bytes(num_seqs: int) -> int:
+    return int(_lib.kda_kv_workspace_bytes(num_seqs))
+
+
+def _append_tensors(pool, q, k, v, q_out, rows, rope):
+    """Arguments shared by the two appends: pointers, row distances, head count."""
+    kp, kl = _rows("k", k, pool.num_heads, pool.head_dim, rows)
+    vp, vl = _rows("v", v, pool.num_heads, pool.head_dim, rows, k.dtype)
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    qp, ql, op, hq = None, 0, None, 0
+    if q is not None:
+        hq = q.shape[1]
+        qp, ql = _rows("q", q, hq, pool.head_dim, rows, k.dtype)
+        op = _out("q_out", q_out, hq, pool.head_dim, rows)
+        if q_out.dtype != k.dtype:
+            raise ValueError("q_out must have the type of q")
+    return qp, kp, vp, _dtype_code(k), ql, kl, vl, op, hq, None if rope is None else ctypes.byref(rope)
+
+
+def kda_kv_append(pool, q, k, v, q_out, cu_seqlens, page_table, *, rope=None, start_pos=None, workspace=None,
+                  stream=None):
+    """q, q_out: [T, Hq, d] or both None; k, v: [T, H, d] (device tensors; q, k and v may be column
+    ranges of one projection); page_table: int32 device tensor [num_seqs, max_pages]; host metadata
+    as for kda_prefill_chunked; workspace: kda_kv_workspace_bytes (None up to 128 sequences)."""
+    cu, sp, ns = _packed(cu_seqlens, start_pos)
+    qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, int(cu.a[-1]), rope)
+    tp, mp = _table(page_table, ns)
+    wp, wb = _ws(workspace)
+    _check(_lib.kda_kv_append(ctypes.byref(pool), rp, qp, kp, vp, dt, ql, kl, vl, op, hq, ns, cu.ptr, sp.ptr, tp,
+                              mp, wp, wb, _stream(stream)))
+
+
+def kda_kv_append_step(pool, q, k, v, q_out, tokens, pos, page_table, *, rope=None, stream=None):
+    """`tokens` tokens per request at positions pos[r] + t: tensors as for kda_kv_append with rows
+    [n * tokens]; pos: int32 device tensor [n], negative for a request that takes no part."""
+    n = int(pos.numel())
+    qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, n * int(tokens), rope)
+    tp, mp = _table(page_table, n)
+    _check(_lib.kda_kv_append_step(ctypes.byref(pool), rp, qp, kp, vp, dt, ql, kl, vl, op, hq, n, int(tokens),
+                                   _pos(pos), tp, mp, _stream(stream)))
+
+
+def kda_kv_read(pool, k_out, v_out, cu_seqlens, page_table, *, start_pos=None, workspace=None, stream=None):
+    """Cached rows back at full precision: k_out, v_out [T, H, d] device tensors of one type."""
+    cu, sp, ns = _packed(cu_seqlens, start_pos)
+    rows = int(cu.a[-1])
+    kp, vp = (_out(name, x, pool.num_heads, pool.head_dim, rows) for name, x in (("k_out", k_out), ("v_out", v_out)))
+    if k_out.dtype != v_out.dtype:
+        raise ValueError("k_out and v_out must have one type")
+    tp, mp = _table(page_table, ns)
+    wp, wb = _ws(workspace)
+    _check(_lib.kda_kv_read(ctypes.byref(pool), kp, vp, _dtype_code(k_out), ns, cu.ptr, sp.ptr, tp, mp, wp, wb,
+                            _stream(stream)))
+
+
+def kda_attn_prefill_workspace_bytes(pool, num_q_heads: int, cu_seqlens, *, start_pos=None, window: int = 0,
+                                     sinks: int = 0) -> int:
+    cu, sp, ns = _packed(cu_seqlens, start_pos)
+    return int(_lib.kda_attn_prefill_workspace_bytes(ctypes.byref(pool), num_q_heads, ns, cu.ptr, sp.ptr, window,
+                                                     sinks))
+
+
+def kda_attn_prefill(pool, q, o, cu_seqlens, page_table, *, scale, start_pos=None, window=0, sinks=0,
+                     workspace=None, stream=None):
+    """q, o: [T, Hq, d] device tensors (q may be columns of a wider tensor), row i of sequence s at
+    position start_pos[s] + i; the cache holds every token up to it.  workspace: uint8 device tensor
+    of kda_attn_prefill_workspace_bytes for the same metadata."""
+    cu, sp, ns = _packed(cu_seqlens, start_pos)
+    rows, hq = int(cu.a[-1]), q.shape[1]
+    qp, ql = _rows("q", q, hq, pool.head_dim, rows)
+    op = _out("o", o, hq, pool.head_dim, rows)
+    tp, mp = _table(page_table, ns)
+    wp, wb = _ws(workspace)
+    _check(_lib.kda_attn_prefill(ctypes.byref(pool), qp, _dtype_code(q), ql, op, _dtype_code(o), hq, scale, window,
+                                 sinks, ns, cu.ptr, sp.ptr, tp, mp, wp, wb, _stream(stream)))
+
+
+def kda_attn_decode_workspace_bytes(pool, num_q_heads: int, n: int, tokens: int, max_pages: int, *,
+                                    window: int = 0, sinks: int = 0) -> int:
+    return int(_lib.kda_attn_decode_workspace_bytes(ctypes.byref(pool), num_q_heads, n, tokens, max_pages, window,
+                                                    sinks))
+
+
+def kda_attn_decode(pool, q, o, tokens, pos, page_table, *, scale, window=0, sinks=0, workspace=None, stream=None):
+    """`tokens` queries per request: q, o [n * tokens, Hq, d] device tensors, row r*tokens + t at
+    position pos[r] + t (pos: int32 device tensor [n], negative for a request that takes no part)."""
+    n, hq = int(pos.numel()), q.shape[1]
+    qp, ql = _rows("q", q, hq, pool.head_dim, n * int(tokens))
+    op = _out("o", o, hq, pool.head_dim, n * int(tokens))
+    tp, mp = _table(page_table, n)
+    wp, wb = _ws(workspace)
+    _check(_lib.kda_attn_decode(ctypes.byref(pool), qp, _dtype_code(q), ql, op, _dtype_code(o), hq, scale, window,
+                                sinks, n, int(tokens), _pos(pos), tp, mp, wp, wb, _stream(stream)))
 
 
 # ---- host prefix index (include/kda_index.h) --------------------------------

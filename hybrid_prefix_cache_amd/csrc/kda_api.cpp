@@ -20,6 +20,7 @@
 #include <vector>
 
 #include "../../include/kda.h"
+#include "kda_host.h"
 #include "kda_launch.h"
 #include "kda_plan.h"
 
@@ -27,8 +28,10 @@
 using namespace kda;
 
 namespace {
-
 thread_local std::string g_err;
+}  // namespace
+
+namespace kda {
 
 kda_status fail(kda_status st, const char* fmt, ...) {
   char buf[512];
@@ -45,7 +48,9 @@ kda_status ok() {
   return KDA_OK;
 }
 
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace kda
+
+namespace {
 
 // Largest accepted start position: positions plus a sequence length (at most
 // 2^30) and a hash block stay far from int64 overflow.
@@ -73,32 +78,32 @@ hipEvent_t take_event() {
   return e;
 }
 
-// Brackets one launch with events when timing is enabled.
-class Launch {
- public:
-  Launch(const char* name, hipStream_t st) : name_(name), st_(st) {
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    if (!g_prof_on) return;
-    ev0_ = take_event();
-    ev1_ = take_event();
-    if (ev0_ && ev1_) hipEventRecord(ev0_, st_);
-  }
-  ~Launch() {
-    if (!ev0_ || !ev1_) return;
-    hipEventRecord(ev1_, st_);
-    std::lock_guard<std::mutex> lk(g_prof_mu);
-    g_prof_pending.push_back({name_, ev0_, ev1_});
-  }
+}  // namespace
 
- private:
-  const char* name_;
-  hipStream_t st_;
-  hipEvent_t ev0_ = nullptr, ev1_ = nullptr;
-};
+namespace kda {
+
+Launch::Launch(const char* name, hipStream_t st) : name_(name), st_(st) {
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  if (!g_prof_on) return;
+  ev0_ = take_event();
+  ev1_ = take_event();
+  if (ev0_ && ev1_) hipEventRecord(ev0_, st_);
+}
+
+Launch::~Launch() {
+  if (!ev0_ || !ev1_) return;
+  hipEventRecord(ev1_, st_);
+  std::lock_guard<std::mutex> lk(g_prof_mu);
+  g_prof_pending.push_back({name_, ev0_, ev1_});
+}
 
 kda_status hip_fail(hipError_t e, const char* what) {
   return fail(KDA_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
 }
+
+}  // namespace kda
+
+namespace {
 
 kda_status check_pool(const kda_pool* p) {
   if (!p) return fail(KDA_ERR_NULL, "pool descriptor is NULL");
@@ -115,8 +120,6 @@ kda_status check_pool(const kda_pool* p) {
   return KDA_OK;
 }
 
-bool valid_dtype(int d) { return d == KDA_F32 || d == KDA_BF16; }
-
 int64_t state_bytes(const kda_pool* p) { return (int64_t)p->num_heads * p->d_k * p->d_v * 4; }
 
 // Metadata region sizes inside the prefill workspace.
@@ -132,7 +135,9 @@ MetaLayout meta_layout(int32_t num_seqs, int32_t num_ckpts) {
   return m;
 }
 
-kda_status ship_metadata(uint8_t* ws, const std::vector<uint8_t>& blob, hipStream_t st) {
+}  // namespace
+
+kda_status kda::ship_metadata(uint8_t* ws, const std::vector<uint8_t>& blob, hipStream_t st) {
   for (size_t off = 0; off < blob.size(); off += kMetaChunkBytes) {
     MetaFillArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -146,8 +151,6 @@ kda_status ship_metadata(uint8_t* ws, const std::vector<uint8_t>& blob, hipStrea
   }
   return KDA_OK;
 }
-
-}  // namespace
 
 namespace kda {
 // error text shared with the host-only translation units (the prefix index)

@@ -1,0 +1,139 @@
+// kda_kv.h -- the paged key/value cache: block layout, the sequences of a call,
+// kernel arguments and launch entry points (kda_kv.hip, kda_attn.hip).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/kda.h"
+
+namespace kda {
+
+constexpr int kKvBlock = 32;        // tokens per cache block
+constexpr int kKvInlineSeqs = 128;  // sequences whose table travels in the kernel arguments
+
+// The cache as the kernels see it.
+struct KvCache {
+  uint8_t* base;
+  int64_t page_bytes;
+  int64_t head_bytes;
+  const int32_t* table;  // [requests][max_pages]
+  int32_t max_pages;
+  int32_t num_pages;
+  int32_t page_tokens;
+  int32_t H;
+};
+
+// One sequence of a call: rows [row, row + len) sit at positions start + i;
+// `unit` is the sequence's first work unit (blocks or query tiles, counted over
+// the call).
+struct KvSeq {
+  int32_t row, start, len, unit;
+};
+
+// The sequences of a call: step form (pos set: `tokens` rows for each of n
+// requests, units_per units each), the workspace table, or the inline one.
+struct KvBatch {
+  const int32_t* pos;
+  const KvSeq* tab;
+  int32_t n;
+  int32_t tokens;
+  int32_t units_per;
+  int32_t pad;
+  KvSeq inl[kKvInlineSeqs];
+};
+
+struct KvAppendArgs {
+  KvCache c;
+  const float* cos;  // NULL: no rotation
+  const float* sin;
+  int64_t num_pos;
+  int32_t rot, interleaved;
+  const void* q;
+  const void* k;
+  const void* v;
+  void* q_out;
+  int64_t q_ld, k_ld, v_ld;
+  int32_t Hq;
+  int32_t kv_wgs;  // workgroups of the key/value part: units * H
+  int32_t rows;
+  KvBatch b;
+};
+static_assert(sizeof(KvAppendArgs) <= 4096, "kernel argument budget");
+
+struct KvReadArgs {
+  KvCache c;
+  void* k_out;
+  void* v_out;
+  KvBatch b;
+};
+static_assert(sizeof(KvReadArgs) <= 4096, "kernel argument budget");
+
+struct AttnArgs {
+  KvCache c;
+  const void* q;
+  void* o;
+  int64_t q_ld;
+  int32_t Hq, G;  // query heads, query heads per key/value head
+  float scale;
+  int32_t window, sinks;
+  int32_t rows;
+  KvBatch b;
+};
+static_assert(sizeof(AttnArgs) <= 4096, "kernel argument budget");
+
+hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, hipStream_t st);
+hipError_t launch_kv_read(int D, bool bf16, bool int8, const KvReadArgs& a, int64_t units, hipStream_t st);
+hipError_t launch_attn(int D, bool in_bf16, bool out_bf16, bool int8, const AttnArgs& a, hipStream_t st);
+
+// ---- device side --------------------------------------------------------------
+// Element offset of (token t, channel ch) in a block's K part / V part; the
+// order is that of include/kda.h.  EB: bytes of an element.
+template <int D, int EB> __device__ __forceinline__ int k_off(int t, int ch) {
+  constexpr int E = 16 / EB;
+  return (t >> 4) * (16 * D) + (ch / E) * (16 * E) + (t & 15) * E + ch % E;
+}
+template <int D, int EB> __device__ __forceinline__ int v_off(int t, int ch) {
+  constexpr int G = 2 / EB;
+  return (ch / (16 * G)) * (512 * G) + ((t & 15) >> 2) * (128 * G) + (ch & 15) * (8 * G) +
+         ((ch >> 4) % G) * 8 + (t & 3) + 4 * (t >> 4);
+}
+
+__device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int i) {
+  if (b.pos) return KvSeq{i * b.tokens, b.pos[i], b.tokens, i * b.units_per};
+  return b.tab ? b.tab[i] : b.inl[i];
+}
+// The sequence that owns a work unit / a row: the last one that begins at or
+// before it (empty sequences begin where the next one does).
+__device__ __forceinline__ int kv_find_unit(const KvBatch& b, int unit) {
+  if (b.pos) return unit / b.units_per;
+  int lo = 0, hi = b.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((b.tab ? b.tab[mid].unit : b.inl[mid].unit) <= unit) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+__device__ __forceinline__ int kv_find_row(const KvBatch& b, int row) {
+  if (b.pos) return row / b.tokens;
+  int lo = 0, hi = b.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if ((b.tab ? b.tab[mid].row : b.inl[mid].row) <= row) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
+// First byte of a request's 32-token block `blk` of head h, or NULL where its
+// page index is bad; *scales receives the block's scale pair (int8 caches).
+template <int D, int EB>
+__device__ __forceinline__ uint8_t* kv_block(const KvCache& c, int req, int blk, int h, float** scales) {
+  const int per = c.page_tokens / kKvBlock;
+  const int page = c.table[(int64_t)req * c.max_pages + blk / per];
+  if (page < 0 || page >= c.num_pages) return nullptr;
+  uint8_t* head = c.base + page * c.page_bytes + h * c.head_bytes;
+  constexpr int kBlockBytes = 2 * kKvBlock * D * EB;
+  if (EB == 1) *scales = reinterpret_cast<float*>(head + (int64_t)per * kBlockBytes) + 2 * (blk % per);
+  return head + (int64_t)(blk % per) * kBlockBytes;
+}
+
+}  // namespace kda

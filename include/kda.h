@@ -84,7 +84,7 @@ typedef enum {
  * pass any value and get KDA_ERR_DTYPE for an unknown one (a C++ enum object
  * may not hold values outside its enumerators). */
 typedef int32_t kda_dtype;
-enum { KDA_F32 = 0, KDA_BF16 = 1 };
+enum { KDA_F32 = 0, KDA_BF16 = 1, KDA_INT8 = 2 /* stored type of a kda_kv_pool only */ };
 
 /*
  * Paged state pool [PAGE].  `base` is device memory of num_pages * page_bytes
@@ -401,6 +401,181 @@ kda_status kda_short_conv(const kda_conv_pool* cpool, const void* x, const float
 kda_status kda_short_conv_update(const kda_conv_pool* cpool, const void* x, const float* w, void* y,
                                  kda_dtype out_dtype, int32_t n, const int32_t* page_in,
                                  const int32_t* page_out, void* stream);
+
+/*
+ * Paged key/value cache of the model's softmax-attention layers, the pages the
+ * prefix index (kda_index.h) hands out beside the recurrent checkpoints
+ * [PAGE]: pages of one fixed byte size, the heads of a page one after another,
+ * so that a head's bytes move as one run.  One pool holds one layer.
+ *
+ * A page holds page_tokens consecutive tokens of one request (any multiple of
+ * 32, e.g. the index's physical block).  Head h of page p starts at byte
+ *     p * page_bytes + h * kda_kv_head_bytes(head_dim, page_tokens, dtype)
+ * and holds page_tokens / 32 blocks of 32 tokens, each a K part and then a V
+ * part of 32 * head_dim elements, and after the blocks (KDA_INT8 only) two
+ * fp32 scales per block, K's and V's.  A cached value is element * scale
+ * (KDA_INT8) or the bf16 element (KDA_BF16).  Element order inside a part (the
+ * operand order of the matrix instructions, so that a wave loads an operand as
+ * one contiguous run), with E = 16 / sizeof(element), G = 2 / sizeof(element):
+ *     K part: [2][head_dim / E][16][E]         token 16 * a + c, channel E * b + e
+ *     V part: [head_dim / (16 G)][4][16][G][8] channel 16 * G * a + 16 * e + c,
+ *             token (x & 3) + 4 * b + 16 * (x >> 2) at slot x
+ * Requirements (kda_kv_pool_check): base and page_bytes multiples of 256,
+ * page_bytes >= num_heads * kda_kv_head_bytes(...), num_pages >= 1, num_heads
+ * (the key/value heads) >= 1, head_dim in {64, 128}, page_tokens a multiple of
+ * 32 in [32, 2^20], dtype KDA_BF16 or KDA_INT8.
+ *
+ * Page tables are int32 DEVICE arrays [requests][max_pages]: entry j of a row
+ * is the page of the request's tokens [j * page_tokens, (j + 1) * page_tokens).
+ * Entries no token of a call needs are not read as pages (-1 is usual: pages
+ * not allocated yet, or freed behind a sliding window).  Device-side: a token
+ * whose page index is outside [0, num_pages) is not stored, and an attention
+ * row that has to see such a page is NaN.  With KDA_VALIDATE=1 the tables (and
+ * positions) are copied to the host and checked first (this synchronises the
+ * stream; not for capture).  max_pages * page_tokens is at most 2^30.
+ */
+typedef struct {
+  void* base;
+  int64_t page_bytes;
+  int32_t num_pages;
+  int32_t num_heads;
+  int32_t head_dim;
+  int32_t page_tokens;
+  kda_dtype dtype;
+} kda_kv_pool;
+
+/*
+ * Position rotation: for a token at position p and pair i < rot_dim / 2 of
+ * channels (a, b) -- (i, i + rot_dim / 2), or (2i, 2i + 1) when interleaved --
+ *     a' = a * cos[p][i] - b * sin[p][i],  b' = b * cos[p][i] + a * sin[p][i]
+ * Channels from rot_dim on are copied.  cos, sin: fp32 DEVICE arrays
+ * [num_pos][rot_dim / 2], 16-byte aligned; rot_dim a multiple of 16 in
+ * [16, head_dim].  Both products and the sum are taken in 64 bits and rounded
+ * once to fp32.
+ */
+typedef struct {
+  const float* cos;
+  const float* sin;
+  int64_t num_pos;
+  int32_t rot_dim;
+  int32_t interleaved;
+} kda_rope;
+
+/* Validates a key/value pool descriptor (no device access). */
+kda_status kda_kv_pool_check(const kda_kv_pool* pool);
+
+/* Bytes of one head in a page, or -1 for unsupported arguments. */
+int64_t kda_kv_head_bytes(int32_t head_dim, int32_t page_tokens, kda_dtype dtype);
+
+/* Workspace bytes of kda_kv_append and kda_kv_read: 0 up to 128 sequences
+ * (their table travels in the kernel arguments), -1 for num_seqs < 0. */
+int64_t kda_kv_workspace_bytes(int32_t num_seqs);
+
+/*
+ * Appends the keys and values of a packed batch to the cache, rotating k, and
+ * q on the way.
+ *   q : [T, num_q_heads, d], k, v : [T, H, d] of in_dtype (KDA_F32 / KDA_BF16),
+ *       rows q_ld / k_ld / v_ld elements apart (so that they may be column
+ *       ranges of one fused projection), each row contiguous; pointers and row
+ *       distances multiples of 16 bytes.
+ *   q_out : [T, num_q_heads, d] in_dtype, contiguous, receives the rotated q;
+ *       must not overlap q, k or v.  q = q_out = NULL with num_q_heads = 0
+ *       appends only.
+ *   rope : NULL for no rotation (q is then copied).
+ *   Host metadata as in kda_prefill_chunked: cu_seqlens [num_seqs+1],
+ *   start_pos [num_seqs] or NULL (0): the tokens the cache already holds of the
+ *   sequence, any value.  start + len is at most max_pages * page_tokens and
+ *   rope->num_pos.
+ * A KDA_BF16 cache holds the values rounded to bf16.  A KDA_INT8 cache holds,
+ * per block, head and part (fp32 arithmetic, IEEE division):
+ *     scale = max(scale before, max |x| / 127)    before: 0 in a block that held nothing
+ *     code  = clamp(round_half_even(x / scale), -127, 127), 0 if scale == 0
+ * and where the scale of a block grows, its older codes c become
+ * clamp(round_half_even(c * scale_before / scale), -127, 127).  A block's codes
+ * therefore depend on which calls brought its tokens; complete blocks never
+ * change.  Values must be finite: one that is not makes its block's scale
+ * non-finite, and every read of the block NaN.
+ * Only the slots of the call's tokens (and, on growth, the older codes of the
+ * first block) are changed; two sequences must not share a written page's block.
+ */
+kda_status kda_kv_append(const kda_kv_pool* pool, const kda_rope* rope, const void* q,
+                         const void* k, const void* v, kda_dtype in_dtype, int64_t q_ld,
+                         int64_t k_ld, int64_t v_ld, void* q_out, int32_t num_q_heads,
+                         int32_t num_seqs, const int64_t* cu_seqlens, const int64_t* start_pos,
+                         const int32_t* page_table, int32_t max_pages, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * The decode-step form: `tokens` (1..64) tokens for each of n requests, rows
+ * r*tokens + t, at positions pos[r] + t (pos: int32 DEVICE array [n], so that a
+ * captured step follows its lengths).  Same arithmetic and equal bits.
+ * Device-side: a request with pos[r] < 0 takes no part (its q_out rows are 0);
+ * tokens past max_pages * page_tokens are not stored; a position past
+ * rope->num_pos is not stored either and its q_out row is NaN.
+ */
+kda_status kda_kv_append_step(const kda_kv_pool* pool, const kda_rope* rope, const void* q,
+                              const void* k, const void* v, kda_dtype in_dtype, int64_t q_ld,
+                              int64_t k_ld, int64_t v_ld, void* q_out, int32_t num_q_heads,
+                              int32_t n, int32_t tokens, const int32_t* pos,
+                              const int32_t* page_table, int32_t max_pages, void* stream);
+
+/*
+ * Reads cached rows back at full precision (the counterpart of
+ * kda_checkpoint_restore_int8): row i of sequence s is the token at position
+ * start_pos[s] + i.  k_out, v_out : [T, H, d] out_dtype, contiguous, 16-byte
+ * aligned.  Host metadata as in kda_kv_append.  Rows of bad pages are NaN.
+ */
+kda_status kda_kv_read(const kda_kv_pool* pool, void* k_out, void* v_out, kda_dtype out_dtype,
+                       int32_t num_seqs, const int64_t* cu_seqlens, const int64_t* start_pos,
+                       const int32_t* page_table, int32_t max_pages, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Attention of a packed batch over the cache, which holds every token up to
+ * each query's own (append first, then attend).  The query at position p sees
+ * the cached tokens j with
+ *     j <= p  and  (window == 0  or  j > p - window  or  j < sinks)
+ * i.e. causal, or the last `window` tokens (itself among them) and the first
+ * `sinks`.  Head h of q reads key/value head h / (num_q_heads / H).
+ *     o = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q . k_j)
+ *   q : [T, num_q_heads, d] of in_dtype, rows q_ld elements apart; o :
+ *   [T, num_q_heads, d] out_dtype, contiguous, not overlapping q.  16-byte
+ *   aligned.  scale > 0 and finite.  num_q_heads a multiple of H.
+ *   Host metadata: cu_seqlens, start_pos as in kda_kv_append (row i of sequence
+ *   s sits at position start_pos[s] + i).
+ * Pages that no row of the call sees are not read and may have been freed.
+ * What slots past a request's tokens, and tokens a row does not see, hold
+ * (NaN included) does not reach that row, but for KDA_INT8 blocks, whose scale
+ * all their tokens share.
+ * workspace: kda_attn_prefill_workspace_bytes with the same metadata.
+ */
+size_t kda_attn_prefill_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads,
+                                        int32_t num_seqs, const int64_t* cu_seqlens,
+                                        const int64_t* start_pos, int32_t window, int32_t sinks);
+
+kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype,
+                            int64_t q_ld, void* o, kda_dtype out_dtype, int32_t num_q_heads,
+                            float scale, int32_t window, int32_t sinks, int32_t num_seqs,
+                            const int64_t* cu_seqlens, const int64_t* start_pos,
+                            const int32_t* page_table, int32_t max_pages, void* workspace,
+                            size_t workspace_bytes, void* stream);
+
+/*
+ * The decode-step form: `tokens` (1..64) queries for each of n requests, rows
+ * r*tokens + t at positions pos[r] + t (pos: int32 DEVICE array [n]).  Rows of a
+ * request with pos[r] < 0 are 0; rows of one whose pos[r] + tokens passes
+ * max_pages * page_tokens are NaN.  workspace: kda_attn_decode_workspace_bytes;
+ * two calls that may overlap (streams, captured graphs) need one each.
+ */
+size_t kda_attn_decode_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n,
+                                       int32_t tokens, int32_t max_pages, int32_t window,
+                                       int32_t sinks);
+
+kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld,
+                           void* o, kda_dtype out_dtype, int32_t num_q_heads, float scale,
+                           int32_t window, int32_t sinks, int32_t n, int32_t tokens,
+                           const int32_t* pos, const int32_t* page_table, int32_t max_pages,
+                           void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * Optional per-kernel timing (tracing aid).  When enabled, every kernel the
