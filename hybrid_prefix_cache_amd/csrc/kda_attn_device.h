@@ -1,0 +1,145 @@
+// kda_attn_device.h -- matrix operands and softmax pieces shared by the
+// attention kernels (kda_attn.hip).
+//
+// Operand types.  A bf16 cache is multiplied as it is (bf16).  An int8 cache's
+// codes are exact in fp16, and one byte permute and one packed subtraction turn
+// four of them into fp16 (1024 + (code + 128) is the bit pattern 0x64xx), so
+// its products run in fp16, where the weights keep 11 bits instead of 8:
+//   - q rows are brought to [2^7, 2^8) by a power of two, undone in the logit's
+//     factor, so that no bf16 or fp32 q leaves fp16's range;
+//   - the block's value scale goes into the weight, w' = exp2(x + log2 vs - m'),
+//     m' the running maximum of x + log2 vs, so that w' <= 1 whatever the
+//     scales; the normaliser sums w' / vs.  w' carries a factor 2^14, which
+//     leaves 38 binary orders of weights above fp16's smallest number.
+// fp32 queries (and their weights) are split into parts that add up to 22 bits
+// (two fp16) or 24 (three bf16), one product each: the cached operand is exact
+// in either type, so the products keep fp32's accuracy.
+#pragma once
+#include "kda_device.h"
+#include "kda_kv.h"
+
+namespace kda {
+
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+constexpr float kNegInf = -__builtin_inff();
+
+template <int EB> struct AttnOp;
+template <> struct AttnOp<2> {
+  typedef bf16x8 Frag;
+  typedef __bf16 T;
+  static constexpr float kLift = 0.f;  // log2 of the weights' extra factor
+  static constexpr int kParts = 3;     // of an fp32 operand
+  __device__ static __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+  }
+  __device__ static __forceinline__ f32x16 mma32(Frag a, Frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+  }
+};
+template <> struct AttnOp<1> {
+  typedef f16x8 Frag;
+  typedef _Float16 T;
+  static constexpr float kLift = 14.f;
+  static constexpr int kParts = 2;
+  __device__ static __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+  }
+  __device__ static __forceinline__ f32x16 mma32(Frag a, Frag b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+  }
+};
+
+// Four int8 codes -> four fp16 (exact).
+__device__ __forceinline__ void codes4(uint32_t w, uint32_t* out) {
+  const uint32_t u = w ^ 0x80808080u;  // code + 128
+  const f16x2 bias = {(_Float16)1152.f, (_Float16)1152.f};
+  out[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04010400u)) - bias);
+  out[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(0x64646464u, u, 0x04030402u)) - bias);
+}
+// Eight codes (half of a 16-byte unit) as an operand.
+__device__ __forceinline__ f16x8 codes8(uint32_t lo, uint32_t hi) {
+  u32x4_t w;
+  codes4(lo, reinterpret_cast<uint32_t*>(&w));
+  codes4(hi, reinterpret_cast<uint32_t*>(&w) + 2);
+  return __builtin_bit_cast(f16x8, w);
+}
+
+// x as NP operand parts whose sum is x to the operand's (NP = 1) or fp32's bits.
+template <int EB, int NP> __device__ __forceinline__ void split8(const float* x, typename AttnOp<EB>::Frag* out) {
+  float r[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = x[i];
+#pragma unroll
+  for (int p = 0; p < NP; ++p) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const typename AttnOp<EB>::T h = static_cast<typename AttnOp<EB>::T>(r[i]);
+      out[p][i] = h;
+      if (p + 1 < NP) r[i] -= static_cast<float>(h);
+    }
+  }
+}
+
+// Reductions over the four 16-lane groups of a wave (lanes of one column).
+__device__ __forceinline__ float group_max(float x) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float group_sum(float x) {
+  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+__device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f(x); }
+// exp2(x - m) where m may be -inf (nothing seen yet): the weight of what has been summed so far.
+__device__ __forceinline__ float decay(float m, float mn) { return m == kNegInf ? 0.f : exp2_f(m - mn); }
+
+// The power of two that brings amax to [2^7, 2^8), and its inverse.
+__device__ __forceinline__ float fit_f16(float amax, float* inverse) {
+  int e = __builtin_amdgcn_frexp_expf(amax);  // amax in [2^(e-1), 2^e); 0 for 0, inf and NaN
+  e = e < -110 ? -110 : e;
+  *inverse = __builtin_ldexpf(1.f, e - 8);
+  return __builtin_ldexpf(1.f, 8 - e);
+}
+
+// The blocks a run of queries at positions [first, last] sees: [0, sink_end) and [win, end).
+struct Reach {
+  int sink_end, win, end;
+  __device__ __forceinline__ int count() const { return sink_end + end - win; }
+  __device__ __forceinline__ int block(int i) const { return i < sink_end ? i : win + i - sink_end; }
+};
+__device__ __forceinline__ Reach reach_of(int64_t first, int64_t last, int window, int sinks) {
+  Reach r;
+  r.end = (int)(last / kKvBlock) + 1;
+  r.win = 0;
+  if (window) r.win = (int)(max((int64_t)0, first - window + 1) / kKvBlock);
+  r.sink_end = (int)min((int64_t)r.win, ((int64_t)sinks + kKvBlock - 1) / kKvBlock);
+  return r;
+}
+// Whether every query at [first, last] sees all of block blk.
+__device__ __forceinline__ bool all_seen(int64_t first, int64_t last, int window, int sinks, int blk) {
+  const int64_t j0 = (int64_t)blk * kKvBlock, j1 = j0 + kKvBlock - 1;
+  return j1 <= first && (!window || j0 > last - window || j1 < sinks);
+}
+__device__ __forceinline__ bool sees(int64_t p, int64_t j, int window, int sinks) {
+  return j <= p && (!window || j > p - window || j < sinks);
+}
+
+// How the blocks a request sees are divided among `splits` workgroups: chunks of
+// at least kMinTiles.
+struct Chunk {
+  int begin, end, used;
+};
+__device__ __forceinline__ Chunk chunk_of(int tiles, int splits, int s) {
+  const int size = max(kMinTiles, (tiles + splits - 1) / splits);
+  return Chunk{s * size, min(tiles, (s + 1) * size), max(1, (tiles + size - 1) / size)};
+}
+
+}  // namespace kda

@@ -1,0 +1,405 @@
+// kda_decode_attn.hip -- attention of a few rows per request over the paged
+// cache (decode and draft verification), gfx950.
+//
+// o = sum_j w_j v_j / sum_j w_j, w_j = exp(scale q . k_j), for the rows of one
+// request and key/value head together (tokens * G of them): up to 16 or 32 rows
+// are one or two column tiles of the matrix products, so every cached byte is
+// read once for all of them.  The step is a stream over the cache.
+//
+// Per 32-token block: S^T = K Q^T (keys as rows), one running maximum and sum per
+// row, O^T += V^T P^T.  With keys as rows a lane's eight weights are one row's at
+// tokens {4g + r, 16 + 4g + r}, which is the order of the tokens in the cache's V
+// part: P^T needs no exchange between lanes, and K and V units go from memory to
+// the matrix operand without LDS.
+//
+// The blocks of a request are split over `splits` workgroups and inside one over
+// its four waves; the waves join through LDS, the workgroups through the
+// workspace and a second kernel (skipped for one split).  No atomics: a result
+// depends on the call's arguments alone.
+#include "kda_attn_device.h"
+
+namespace kda {
+
+template <int D, int EB> struct TileRegs {
+  u32x4_t k[2 * D * EB / 64], v[2 * D * EB / 64];
+  float ks, vs;
+};
+
+template <int D, int EB>
+__device__ __forceinline__ void load_tile(const KvCache& c, const uint8_t* head0, int page, int inner, int lane,
+                                          TileRegs<D, EB>& t) {
+  constexpr int N = 2 * D * EB / 64, PART = kKvBlock * D * EB;
+  const int per = c.page_tokens / kKvBlock;
+  const uint8_t* head = head0 + (int64_t)page * c.page_bytes;
+  const uint8_t* b = head + (int64_t)inner * (2 * PART) + 16 * lane;
+#pragma unroll
+  for (int i = 0; i < N; ++i) t.k[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(b + 1024 * i));
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    t.v[i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(b + PART + 1024 * i));
+  if constexpr (EB == 1) {
+    const float* s = reinterpret_cast<const float*>(head + (int64_t)per * (2 * PART)) + 2 * inner;
+    t.ks = s[0];
+    t.vs = s[1];
+  }
+}
+
+// In a block that some row does not see, 0 * V must not make that row NaN: where V
+// holds infinities or NaN (bf16 caches), they are taken out of the operand, and
+// rows that see one get it added: a product of 0/1 operands counts them.
+template <int MT>
+__device__ __forceinline__ void spread_nonfinite(u32x4_t& v, const bf16x8* seen, f32x4* const* acc) {
+  u16x8 w = __builtin_bit_cast(u16x8, v), f[3];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const bool odd = (w[i] & 0x7f80u) == 0x7f80u;
+    f[0][i] = w[i] == 0x7f80u ? 0x3f80u : 0;
+    f[1][i] = w[i] == 0xff80u ? 0x3f80u : 0;
+    f[2][i] = odd && (w[i] & 0x7fu) ? 0x3f80u : 0;
+    if (odd) w[i] = 0;
+  }
+  v = __builtin_bit_cast(u32x4_t, w);
+  const float add[3] = {__builtin_inff(), kNegInf, __builtin_nanf("")};
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      const f32x4 n = AttnOp<2>::mma(__builtin_bit_cast(bf16x8, f[k]), seen[mt], zero4());
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (n[r] > 0.f) (*acc[mt])[r] += add[k];
+    }
+}
+
+template <int D, int EB, int NP, int MT>
+__global__ __launch_bounds__(256) void decode_attn_kernel(DecodeAttnArgs a) {
+  typedef AttnOp<EB> Op;
+  typedef typename Op::Frag Frag;
+  constexpr int KS = D / 32, DT = D / 16, LD = D + 4;
+  __shared__ float sh_o[4][16][LD];
+  __shared__ float sh_m[4][MT * 16], sh_l[4][MT * 16];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int g = lane >> 4, col = lane & 15;
+  const int item = blockIdx.x % (a.n * a.c.H), sp = blockIdx.x / (a.n * a.c.H);
+  const int req = item / a.c.H, h = item % a.c.H;
+  const int M = a.tokens * a.G;
+  const int64_t p0 = a.pos[req], p1 = p0 + a.tokens - 1;
+  const bool off = p0 < 0, over = p1 >= (int64_t)a.c.max_pages * a.c.page_tokens;
+  if (off || over) {
+    if (sp == 0)
+      for (int i = threadIdx.x; i < M * D; i += 256) {
+        const int row = i / D;
+        const int64_t at = ((int64_t)(req * a.tokens + row / a.G) * a.Hq + h * a.G + row % a.G) * D + i % D;
+        const float y = off ? 0.f : __builtin_nanf("");
+        if (a.out_bf16) reinterpret_cast<uint16_t*>(a.o)[at] = f32_to_bf16(y);
+        else reinterpret_cast<float*>(a.o)[at] = y;
+      }
+    return;
+  }
+  const Reach reach = reach_of(p0, p1, a.window, a.sinks);
+  const Chunk ch = chunk_of(reach.count(), a.splits, sp);
+  if (ch.begin >= ch.end) return;
+
+  // ---- queries: lane (g, col) holds row col's channels of k-group g
+  Frag qf[MT][KS][NP];
+  float qc[MT];     // logit factor of the lane's row
+  int64_t qp[MT];   // its position
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int row = 16 * mt + col;
+    const bool live = row < M;
+    qp[mt] = p0 + (live ? row / a.G : 0);
+    const int64_t at = (int64_t)(req * a.tokens + (live ? row / a.G : 0)) * a.q_ld +
+                       (int64_t)(h * a.G + (live ? row % a.G : 0)) * D;
+    float x[KS][8], amax = 0.f;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      // channels of matrix step ks and group g, in the order of the K part's 16-byte units
+      const int d0 = EB == 1 ? 64 * (ks >> 1) + 16 * g + 8 * (ks & 1) : 32 * ks + 8 * g;
+      if constexpr (NP == 1) {
+        const u16x8 w = *reinterpret_cast<const u16x8*>(reinterpret_cast<const uint16_t*>(a.q) + at + d0);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[ks][i] = bf16_to_f32(w[i]);
+      } else {
+        const float* p = reinterpret_cast<const float*>(a.q) + at + d0;
+        const f32x4 u = *reinterpret_cast<const f32x4*>(p), w = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) { x[ks][i] = u[i]; x[ks][4 + i] = w[i]; }
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        if (!live) x[ks][i] = 0.f;
+        amax = fmaxf(amax, fabsf(x[ks][i]));
+      }
+    }
+    float f = 1.f, inv = 1.f;
+    if constexpr (EB == 1) f = fit_f16(group_max(amax), &inv);
+    qc[mt] = a.scale_log2 * inv;
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      if constexpr (EB == 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[ks][i] *= f;
+      }
+      split8<EB, NP>(x[ks], qf[mt][ks]);
+    }
+  }
+
+  f32x4 acc[MT][DT];
+  float m[MT], l[MT];
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    m[mt] = kNegInf;
+    l[mt] = 0.f;
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) acc[mt][dt] = zero4();
+  }
+
+  // ---- this wave's blocks: tiles first, first + 4, ...; lane i looks up the page of the i-th of each 64
+  const int first = ch.begin + wv, count = first < ch.end ? (ch.end - first + 3) / 4 : 0;
+  const uint8_t* head0 = a.c.base + h * a.c.head_bytes;
+  const int per = a.c.page_tokens / kKvBlock;
+  int pg = 0, in = 0;
+  auto look_up = [&](int base) {
+    const int t = first + 4 * (base + lane);
+    if (t < ch.end) {
+      const int blk = reach.block(t);
+      const int j = blk / per;
+      in = blk - j * per;
+      pg = a.c.table[(int64_t)req * a.c.max_pages + j];
+      if (pg < 0 || pg >= a.c.num_pages) pg = -1;
+    }
+  };
+  TileRegs<D, EB> cur, nxt;
+  int cur_pg = 0, nxt_pg = 0;
+  auto fetch = [&](int i, TileRegs<D, EB>& t, int& page) {
+    page = __builtin_amdgcn_readlane(pg, i & 63);
+    const int inner = __builtin_amdgcn_readlane(in, i & 63);
+    load_tile<D, EB>(a.c, head0, max(page, 0), inner, lane, t);  // a bad page: page 0's bytes, never used
+  };
+  if (count > 0) {
+    look_up(0);
+    fetch(0, cur, cur_pg);
+  }
+  for (int i = 0; i < count; ++i) {
+    if (i + 1 < count) {
+      if (((i + 1) & 63) == 0) look_up(i + 1);
+      fetch(i + 1, nxt, nxt_pg);
+    }
+    const int blk = reach.block(first + 4 * i);
+    const bool bad = cur_pg < 0, full = !bad && all_seen(p0, p1, a.window, a.sinks, blk);
+    float ks = 1.f, lv = 0.f, iv = 1.f;
+    if (EB == 1 && !bad) {
+      ks = cur.ks;
+      const float vs = cur.vs == 0.f ? 1.f : cur.vs < 0x1p-120f ? 0x1p-120f : cur.vs;
+      lv = __builtin_amdgcn_logf(vs);
+      iv = 1.f / vs;
+    }
+    f32x4 s[MT][2];
+#pragma unroll
+    for (int kt = 0; kt < 2; ++kt) {
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) s[mt][kt] = zero4();
+#pragma unroll
+      for (int st = 0; st < KS; ++st) {
+        Frag kf;
+        if constexpr (EB == 1) {
+          const u32x4_t w = cur.k[kt * (KS / 2) + (st >> 1)];
+          kf = codes8(w[2 * (st & 1)], w[2 * (st & 1) + 1]);
+        } else {
+          kf = __builtin_bit_cast(Frag, cur.k[kt * KS + st]);
+        }
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int p = 0; p < NP; ++p) s[mt][kt] = Op::mma(kf, qf[mt][st][p], s[mt][kt]);
+      }
+    }
+    Frag pf[MT][NP];
+    bf16x8 seen[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const float c = qc[mt] * ks;
+      float x[8], mx = kNegInf;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(s[mt][e >> 2][e & 3], c, lv);
+      if (!full) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int64_t j = (int64_t)blk * kKvBlock + 16 * (e >> 2) + 4 * g + (e & 3);
+          const bool see = sees(qp[mt], j, a.window, a.sinks);
+          x[e] = !see ? kNegInf : bad ? __builtin_nanf("") : x[e];
+          seen[mt][e] = static_cast<__bf16>(see ? 1.f : 0.f);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) mx = fmaxf(mx, x[e]);
+      mx = group_max(mx);
+      if (__any(mx > m[mt])) {
+        const float mn = fmaxf(m[mt], mx), al = decay(m[mt], mn);
+        m[mt] = mn;
+        l[mt] *= al;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) acc[mt][dt] *= al;
+      }
+      const float mu = (m[mt] == kNegInf ? 0.f : m[mt]) - Op::kLift;
+      float sum = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        x[e] = exp2_f(x[e] - mu);
+        sum += x[e];
+      }
+      if (EB == 1) l[mt] += sum == 0.f ? 0.f : sum * iv;  // a block of which the row sees nothing adds nothing
+      else l[mt] += sum;
+      split8<EB, NP>(x, pf[mt]);
+    }
+    if constexpr (EB == 2) {
+      if (!full) {
+        bool odd = false;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          const u16x8 w = __builtin_bit_cast(u16x8, cur.v[dt]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) odd |= (w[e] & 0x7f80u) == 0x7f80u;
+        }
+        if (__any(odd)) {
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) {
+            f32x4* at[MT];
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) at[mt] = &acc[mt][dt];
+            spread_nonfinite<MT>(cur.v[dt], seen, at);
+          }
+        }
+      }
+    }
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) {
+      Frag vf;
+      if constexpr (EB == 1) {
+        const u32x4_t w = cur.v[dt >> 1];
+        vf = codes8(w[2 * (dt & 1)], w[2 * (dt & 1) + 1]);
+      } else {
+        vf = __builtin_bit_cast(Frag, cur.v[dt]);
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int p = 0; p < NP; ++p) acc[mt][dt] = Op::mma(vf, pf[mt][p], acc[mt][dt]);
+    }
+    cur = nxt;
+    cur_pg = nxt_pg;
+  }
+
+  // ---- join the four waves
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    l[mt] = group_sum(l[mt]);
+    if (g == 0) {
+      sh_m[wv][16 * mt + col] = m[mt];
+      sh_l[wv][16 * mt + col] = l[mt];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int mt = 0; mt < MT; ++mt) {
+    const int rc = 16 * mt + col;
+    const float mn = fmaxf(fmaxf(sh_m[0][rc], sh_m[1][rc]), fmaxf(sh_m[2][rc], sh_m[3][rc]));
+    const float al = decay(m[mt], mn);
+    if (mt) __syncthreads();
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt)
+      *reinterpret_cast<f32x4*>(&sh_o[wv][col][16 * dt + 4 * g]) = acc[mt][dt] * al;
+    __syncthreads();
+    for (int i = threadIdx.x; i < 16 * (D / 4); i += 256) {
+      const int row = i / (D / 4), d = 4 * (i % (D / 4)), rr = 16 * mt + row;
+      if (rr >= M) continue;
+      f32x4 y = zero4();
+      float mm = kNegInf, ll = 0.f;
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        y += *reinterpret_cast<const f32x4*>(&sh_o[w][row][d]);
+        mm = fmaxf(mm, sh_m[w][rr]);
+      }
+#pragma unroll
+      for (int w = 0; w < 4; ++w) ll += sh_l[w][rr] * decay(sh_m[w][rr], mm);
+      const int64_t at = (int64_t)(req * a.tokens + rr / a.G) * a.Hq + h * a.G + rr % a.G;
+      if (ch.used == 1) {
+        // ll is 0 only where nothing was seen, and every row sees itself
+        const float inv = 1.f / ll;
+        if (a.out_bf16)
+          *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.o) + at * D + d) =
+              pack_bf16x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+        else
+          *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.o) + at * D + d) = y * inv;
+      } else {
+        *reinterpret_cast<f32x4*>(a.part_o + (at * a.splits + sp) * D + d) = y;
+        if (d == 0) {
+          a.part_ml[2 * (at * a.splits + sp)] = mm;
+          a.part_ml[2 * (at * a.splits + sp) + 1] = ll;
+        }
+      }
+    }
+  }
+}
+
+// Joins the splits of one (row, head): one wave each.
+template <int D> __global__ __launch_bounds__(256) void join_kernel(DecodeAttnArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int row = (int)(at / a.Hq);
+  if (row >= a.n * a.tokens) return;
+  const int req = row / a.tokens;
+  const int64_t p0 = a.pos[req], p1 = p0 + a.tokens - 1;
+  if (p0 < 0 || p1 >= (int64_t)a.c.max_pages * a.c.page_tokens) return;
+  const int used = chunk_of(reach_of(p0, p1, a.window, a.sinks).count(), a.splits, 0).used;
+  if (used == 1) return;
+  const float* ml = a.part_ml + 2 * at * a.splits;
+  const float* po = a.part_o + at * a.splits * D;
+  float mm = kNegInf;
+  for (int s = lane; s < used; s += 64) mm = fmaxf(mm, ml[2 * s]);
+#pragma unroll
+  for (int x = 1; x < 64; x <<= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
+  float ll = 0.f, y[D / 64] = {};
+  for (int s = 0; s < used; ++s) {
+    const float w = decay(ml[2 * s], mm);
+    ll += w * ml[2 * s + 1];
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) y[i] += w * po[(int64_t)s * D + (D / 64) * lane + i];
+  }
+  const float inv = 1.f / ll;
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    const int64_t o = at * D + (D / 64) * lane + i;
+    if (a.out_bf16) reinterpret_cast<uint16_t*>(a.o)[o] = f32_to_bf16(y[i] * inv);
+    else reinterpret_cast<float*>(a.o)[o] = y[i] * inv;
+  }
+}
+
+template <int D, int EB, int NP> static void launch_mt(const DecodeAttnArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.n * a.c.H * a.splits)), block(256);
+  if (a.tokens * a.G <= 16) hipLaunchKernelGGL((decode_attn_kernel<D, EB, NP, 1>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((decode_attn_kernel<D, EB, NP, 2>), grid, block, 0, st, a);
+}
+template <int D> static void launch_dd(bool in_bf16, bool int8, const DecodeAttnArgs& a, hipStream_t st) {
+  if (int8) {
+    if (in_bf16) launch_mt<D, 1, 1>(a, st);
+    else launch_mt<D, 1, AttnOp<1>::kParts>(a, st);
+  } else {
+    if (in_bf16) launch_mt<D, 2, 1>(a, st);
+    else launch_mt<D, 2, AttnOp<2>::kParts>(a, st);
+  }
+}
+hipError_t launch_decode_attn(int D, bool in_bf16, bool int8, const DecodeAttnArgs& a, hipStream_t st) {
+  if (D == 128) launch_dd<128>(in_bf16, int8, a, st);
+  else launch_dd<64>(in_bf16, int8, a, st);
+  return hipGetLastError();
+}
+hipError_t launch_join(int D, const DecodeAttnArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(((int64_t)a.n * a.tokens * a.Hq + 3) / 4)), block(256);
+  if (D == 128) hipLaunchKernelGGL((join_kernel<128>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((join_kernel<64>), grid, block, 0, st, a);
+  return hipGetLastError();
+}
+
+}  // namespace kda

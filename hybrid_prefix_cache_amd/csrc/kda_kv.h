@@ -81,9 +81,32 @@ struct AttnArgs {
 };
 static_assert(sizeof(AttnArgs) <= 4096, "kernel argument budget");
 
+// Rows of a decode or verify step, with their split over the cache.
+struct DecodeAttnArgs {
+  KvCache c;
+  const void* q;
+  void* o;
+  float* part_o;   // [n * tokens][Hq][splits][D]
+  float* part_ml;  // [n * tokens][Hq][splits][2]: running maximum and sum
+  const int32_t* pos;
+  int64_t q_ld;
+  int32_t Hq, G;
+  float scale_log2;
+  int32_t window, sinks;
+  int32_t n, tokens, splits;
+  int32_t out_bf16;
+};
+
+constexpr int kDecodeRows = 32;  // rows per request and key/value head the decode kernel takes
+
+hipError_t launch_decode_attn(int D, bool in_bf16, bool int8, const DecodeAttnArgs& a, hipStream_t st);
+hipError_t launch_join(int D, const DecodeAttnArgs& a, hipStream_t st);
 hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, hipStream_t st);
 hipError_t launch_kv_read(int D, bool bf16, bool int8, const KvReadArgs& a, int64_t units, hipStream_t st);
 hipError_t launch_attn(int D, bool in_bf16, bool out_bf16, bool int8, const AttnArgs& a, hipStream_t st);
+
+// Blocks of at least this many are one split's share of a cache.
+constexpr int kMinTiles = 8;
 
 // ---- device side --------------------------------------------------------------
 // Element offset of (token t, channel ch) in a block's K part / V part; the

@@ -20,6 +20,7 @@ using namespace kda;
 namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // positions, rows, table capacity
+constexpr int64_t kSplitTarget = 2048;            // workgroups a decode step is split into, at least
 
 kda_status check_kv_pool(const kda_kv_pool* p) {
   if (!p) return fail(KDA_ERR_NULL, "kv pool descriptor is NULL");
@@ -293,6 +294,22 @@ AttnArgs attn_args(const kda_kv_pool* p, const void* q, int64_t q_ld, void* o, i
   return a;
 }
 
+// How many workgroups share the cache of one (request, head): enough of them
+// for the card, each with at least kMinTiles blocks of the longest reach.
+int32_t decode_splits(const kda_kv_pool* p, int32_t n, int32_t tokens, int32_t max_pages, int32_t window,
+                      int32_t sinks) {
+  int64_t tiles = (int64_t)max_pages * p->page_tokens / kKvBlock;
+  if (window)
+    tiles = std::min<int64_t>(tiles, ((int64_t)sinks + kKvBlock - 1) / kKvBlock +
+                                         ((int64_t)window + tokens + kKvBlock - 1) / kKvBlock + 1);
+  const int64_t want = (kSplitTarget + (int64_t)n * p->num_heads - 1) / ((int64_t)n * p->num_heads);
+  return (int32_t)std::max<int64_t>(1, std::min(want, (tiles + kMinTiles - 1) / kMinTiles));
+}
+size_t decode_workspace(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens, int32_t splits) {
+  if (splits == 1 || tokens * (Hq / p->num_heads) > kDecodeRows) return 256;
+  return (size_t)n * tokens * Hq * splits * (p->head_dim + 2) * 4;
+}
+
 // No exception leaves an entry point.
 template <typename F> kda_status guarded(F f) {
   try {
@@ -486,9 +503,10 @@ kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in
 size_t kda_attn_decode_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n, int32_t tokens,
                                        int32_t max_pages, int32_t window, int32_t sinks) {
   if (check_attn(pool, KDA_BF16, KDA_BF16, num_q_heads, 1.f, window, sinks) != KDA_OK || n < 0 || tokens < 1 ||
-      tokens > 64 || max_pages < 1)
+      tokens > 64 || max_pages < 1 || n > 1 << 24 || (int64_t)max_pages * pool->page_tokens > kMaxTokens)
     return 0;
-  return 256;
+  if (n == 0) return 256;
+  return decode_workspace(pool, num_q_heads, n, tokens, decode_splits(pool, n, tokens, max_pages, window, sinks));
 }
 
 kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld, void* o,
@@ -505,7 +523,10 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
     const int64_t rows = (int64_t)n * tokens;
     s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
     if (s != KDA_OK) return s;
-    s = check_workspace(workspace, workspace_bytes, 256);
+    const int32_t splits = decode_splits(pool, n, tokens, max_pages, window, sinks);
+    if ((int64_t)n * pool->num_heads * splits > kMaxTokens || rows * num_q_heads > kMaxTokens)
+      return fail(KDA_ERR_SHAPE, "too much work for one call");
+    s = check_workspace(workspace, workspace_bytes, decode_workspace(pool, num_q_heads, n, tokens, splits));
     if (s != KDA_OK) return s;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (validating()) {
@@ -513,6 +534,36 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
       s = step_seqs(pos, n, tokens, &seqs, st);
       if (s == KDA_OK) s = check_pages(pool, page_table, max_pages, seqs, window, sinks, false, true, st);
       if (s != KDA_OK) return s;
+    }
+    if (tokens * (num_q_heads / pool->num_heads) <= kDecodeRows) {
+      DecodeAttnArgs a;
+      std::memset(&a, 0, sizeof(a));
+      a.c = cache_of(pool, page_table, max_pages);
+      a.q = q;
+      a.o = o;
+      a.part_o = static_cast<float*>(workspace);
+      a.part_ml = a.part_o + (size_t)rows * num_q_heads * splits * pool->head_dim;
+      a.pos = pos;
+      a.q_ld = q_ld;
+      a.Hq = num_q_heads;
+      a.G = num_q_heads / pool->num_heads;
+      a.scale_log2 = scale * 1.44269504f;
+      a.window = window;
+      a.sinks = sinks;
+      a.n = n;
+      a.tokens = tokens;
+      a.splits = splits;
+      a.out_bf16 = out_dtype == KDA_BF16;
+      hipError_t e;
+      {
+        Launch L("kda_attn_decode", st);
+        e = launch_decode_attn(pool->head_dim, in_dtype == KDA_BF16, pool->dtype == KDA_INT8, a, st);
+      }
+      if (e == hipSuccess && splits > 1) {
+        Launch L("kda_attn_join", st);
+        e = launch_join(pool->head_dim, a, st);
+      }
+      return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
     }
     AttnArgs a = attn_args(pool, q, q_ld, o, num_q_heads, scale, window, sinks, page_table, max_pages, rows);
     a.b = step_batch(pos, n, tokens, 1);
