@@ -18,7 +18,7 @@ LIB = os.path.join(HERE, "libkda.so")
 PROBE_SRC = "kda_probe.hip"
 PROBE_LIB = os.path.join(HERE, "libkda_probe.so")
 SOURCES = ["kda_api.cpp", "kda_prefill.hip", "kda_decode.hip", "kda_copy.hip", "kda_ckpt_int8.hip", "kda_conv.hip",
-           "kda_index.cpp", "kda_noalloc.hip", "kda_kv.hip", "kda_attn.hip", "kda_decode_attn.hip", "kda_kv_api.cpp"]
+           "kda_index.cpp", "kda_noalloc.hip", "kda_kv.hip", "kda_attn_tiled.hip", "kda_attn_decode.hip", "kda_kv_api.cpp"]
 ARCH = os.environ.get("KDA_OFFLOAD_ARCH", "gfx950")
 FLAGS = ["-O3", "-fPIC", "-std=c++17", f"--offload-arch={ARCH}",
          # no packed fp32 instructions (v_pk_*_f32) in device code

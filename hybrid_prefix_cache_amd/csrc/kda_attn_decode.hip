@@ -1,4 +1,4 @@
-// kda_decode_attn.hip -- attention of a few rows per request over the paged
+// kda_attn_decode.hip -- attention of a few rows per request over the paged
 // cache (decode and draft verification), gfx950.
 //
 // o = sum_j w_j v_j / sum_j w_j, w_j = exp(scale q . k_j), for the rows of one
@@ -72,7 +72,7 @@ __device__ __forceinline__ void spread_nonfinite(u32x4_t& v, const bf16x8* seen,
 }
 
 template <int D, int EB, int NP, int MT>
-__global__ __launch_bounds__(256) void decode_attn_kernel(DecodeAttnArgs a) {
+__global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   typedef AttnOp<EB> Op;
   typedef typename Op::Frag Frag;
   constexpr int KS = D / 32, DT = D / 16, LD = D + 4;
@@ -80,16 +80,16 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(DecodeAttnArgs a) {
   __shared__ float sh_m[4][MT * 16], sh_l[4][MT * 16];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
-  const int item = blockIdx.x % (a.n * a.c.H), sp = blockIdx.x / (a.n * a.c.H);
+  const int item = blockIdx.x % (a.b.n * a.c.H), sp = blockIdx.x / (a.b.n * a.c.H);
   const int req = item / a.c.H, h = item % a.c.H;
-  const int M = a.tokens * a.G;
-  const int64_t p0 = a.pos[req], p1 = p0 + a.tokens - 1;
+  const int M = a.b.tokens * a.G;
+  const int64_t p0 = a.b.pos[req], p1 = p0 + a.b.tokens - 1;
   const bool off = p0 < 0, over = p1 >= (int64_t)a.c.max_pages * a.c.page_tokens;
   if (off || over) {
     if (sp == 0)
       for (int i = threadIdx.x; i < M * D; i += 256) {
         const int row = i / D;
-        const int64_t at = ((int64_t)(req * a.tokens + row / a.G) * a.Hq + h * a.G + row % a.G) * D + i % D;
+        const int64_t at = ((int64_t)(req * a.b.tokens + row / a.G) * a.Hq + h * a.G + row % a.G) * D + i % D;
         const float y = off ? 0.f : __builtin_nanf("");
         if (a.out_bf16) reinterpret_cast<uint16_t*>(a.o)[at] = f32_to_bf16(y);
         else reinterpret_cast<float*>(a.o)[at] = y;
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(DecodeAttnArgs a) {
     const int row = 16 * mt + col;
     const bool live = row < M;
     qp[mt] = p0 + (live ? row / a.G : 0);
-    const int64_t at = (int64_t)(req * a.tokens + (live ? row / a.G : 0)) * a.q_ld +
+    const int64_t at = (int64_t)(req * a.b.tokens + (live ? row / a.G : 0)) * a.q_ld +
                        (int64_t)(h * a.G + (live ? row % a.G : 0)) * D;
     float x[KS][8], amax = 0.f;
 #pragma unroll
@@ -323,7 +323,7 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(DecodeAttnArgs a) {
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) ll += sh_l[w][rr] * decay(sh_m[w][rr], mm);
-      const int64_t at = (int64_t)(req * a.tokens + rr / a.G) * a.Hq + h * a.G + rr % a.G;
+      const int64_t at = (int64_t)(req * a.b.tokens + rr / a.G) * a.Hq + h * a.G + rr % a.G;
       if (ch.used == 1) {
         // ll is 0 only where nothing was seen, and every row sees itself
         const float inv = 1.f / ll;
@@ -343,16 +343,18 @@ __global__ __launch_bounds__(256) void decode_attn_kernel(DecodeAttnArgs a) {
   }
 }
 
-// Joins the splits of one (row, head): one wave each.
-template <int D> __global__ __launch_bounds__(256) void join_kernel(DecodeAttnArgs a) {
+// Joins the splits of one (row, query head), of either kernel: one wave each.
+template <int D> __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int row = (int)(at / a.Hq);
-  if (row >= a.n * a.tokens) return;
-  const int req = row / a.tokens;
-  const int64_t p0 = a.pos[req], p1 = p0 + a.tokens - 1;
-  if (p0 < 0 || p1 >= (int64_t)a.c.max_pages * a.c.page_tokens) return;
-  const int used = chunk_of(reach_of(p0, p1, a.window, a.sinks).count(), a.splits, 0).used;
+  if (at >= (int64_t)a.rows * a.Hq) return;
+  const int row = (int)(at / a.Hq), g = (int)(at % a.Hq) % a.G;
+  const KvSeq sq = kv_seq(a.b, kv_find_row(a.b, row));
+  if (sq.start < 0 || (int64_t)sq.start + sq.len > (int64_t)a.c.max_pages * a.c.page_tokens) return;
+  // the reach of the row's tile, as the attention kernel divided it
+  const int t0 = ((row - sq.row) * a.G + g) / a.tile_rows * a.tile_rows, t1 = min(sq.len * a.G, t0 + a.tile_rows);
+  const Reach reach = reach_of(sq.start + t0 / a.G, sq.start + (t1 - 1) / a.G, a.window, a.sinks);
+  const int used = chunk_of(reach.count(), a.splits, 0).used;
   if (used == 1) return;
   const float* ml = a.part_ml + 2 * at * a.splits;
   const float* po = a.part_o + at * a.splits * D;
@@ -376,12 +378,12 @@ template <int D> __global__ __launch_bounds__(256) void join_kernel(DecodeAttnAr
   }
 }
 
-template <int D, int EB, int NP> static void launch_mt(const DecodeAttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.n * a.c.H * a.splits)), block(256);
-  if (a.tokens * a.G <= 16) hipLaunchKernelGGL((decode_attn_kernel<D, EB, NP, 1>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((decode_attn_kernel<D, EB, NP, 2>), grid, block, 0, st, a);
+template <int D, int EB, int NP> static void launch_mt(const AttnArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.b.n * a.c.H * a.splits)), block(256);
+  if (a.b.tokens * a.G <= 16) hipLaunchKernelGGL((attn_decode_kernel<D, EB, NP, 1>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((attn_decode_kernel<D, EB, NP, 2>), grid, block, 0, st, a);
 }
-template <int D> static void launch_dd(bool in_bf16, bool int8, const DecodeAttnArgs& a, hipStream_t st) {
+template <int D> static void launch_dd(bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st) {
   if (int8) {
     if (in_bf16) launch_mt<D, 1, 1>(a, st);
     else launch_mt<D, 1, AttnOp<1>::kParts>(a, st);
@@ -390,13 +392,13 @@ template <int D> static void launch_dd(bool in_bf16, bool int8, const DecodeAttn
     else launch_mt<D, 2, AttnOp<2>::kParts>(a, st);
   }
 }
-hipError_t launch_decode_attn(int D, bool in_bf16, bool int8, const DecodeAttnArgs& a, hipStream_t st) {
+hipError_t launch_attn_decode(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st) {
   if (D == 128) launch_dd<128>(in_bf16, int8, a, st);
   else launch_dd<64>(in_bf16, int8, a, st);
   return hipGetLastError();
 }
-hipError_t launch_join(int D, const DecodeAttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(((int64_t)a.n * a.tokens * a.Hq + 3) / 4)), block(256);
+hipError_t launch_attn_join(int D, const AttnArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(((int64_t)a.rows * a.Hq + 3) / 4)), block(256);
   if (D == 128) hipLaunchKernelGGL((join_kernel<128>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((join_kernel<64>), grid, block, 0, st, a);
   return hipGetLastError();

@@ -68,42 +68,32 @@ struct KvReadArgs {
 };
 static_assert(sizeof(KvReadArgs) <= 4096, "kernel argument budget");
 
+// Attention of the rows of a call.  A sequence's rows per key/value head (row =
+// token * G + g) are cut into tiles of tile_rows; units counts the tiles.
 struct AttnArgs {
   KvCache c;
   const void* q;
   void* o;
-  int64_t q_ld;
-  int32_t Hq, G;  // query heads, query heads per key/value head
-  float scale;
-  int32_t window, sinks;
-  int32_t rows;
-  KvBatch b;
-};
-static_assert(sizeof(AttnArgs) <= 4096, "kernel argument budget");
-
-// Rows of a decode or verify step, with their split over the cache.
-struct DecodeAttnArgs {
-  KvCache c;
-  const void* q;
-  void* o;
-  float* part_o;   // [n * tokens][Hq][splits][D]
-  float* part_ml;  // [n * tokens][Hq][splits][2]: running maximum and sum
-  const int32_t* pos;
+  float* part_o;   // [rows][Hq][splits][D]
+  float* part_ml;  // [rows][Hq][splits][2]: running maximum and sum
   int64_t q_ld;
   int32_t Hq, G;
   float scale_log2;
   int32_t window, sinks;
-  int32_t n, tokens, splits;
+  int32_t rows, units, tile_rows;
+  int32_t splits;  // workgroups that share the blocks a tile sees
   int32_t out_bf16;
+  KvBatch b;
 };
+static_assert(sizeof(AttnArgs) <= 4096, "kernel argument budget");
 
 constexpr int kDecodeRows = 32;  // rows per request and key/value head the decode kernel takes
 
-hipError_t launch_decode_attn(int D, bool in_bf16, bool int8, const DecodeAttnArgs& a, hipStream_t st);
-hipError_t launch_join(int D, const DecodeAttnArgs& a, hipStream_t st);
+hipError_t launch_attn_decode(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
+hipError_t launch_attn_tiled(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
+hipError_t launch_attn_join(int D, const AttnArgs& a, hipStream_t st);
 hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, hipStream_t st);
 hipError_t launch_kv_read(int D, bool bf16, bool int8, const KvReadArgs& a, int64_t units, hipStream_t st);
-hipError_t launch_attn(int D, bool in_bf16, bool out_bf16, bool int8, const AttnArgs& a, hipStream_t st);
 
 // Blocks of at least this many are one split's share of a cache.
 constexpr int kMinTiles = 8;

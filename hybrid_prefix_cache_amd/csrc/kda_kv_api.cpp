@@ -20,7 +20,9 @@ using namespace kda;
 namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // positions, rows, table capacity
-constexpr int64_t kSplitTarget = 2048;            // workgroups a decode step is split into, at least
+constexpr int64_t kFullCard = 256;      // workgroups that give every CU one
+constexpr int64_t kDecodeTarget = 2048;  // workgroups a decode step is split into, at least
+constexpr int64_t kTiledTarget = 512;    // the same for tiles
 
 kda_status check_kv_pool(const kda_kv_pool* p) {
   if (!p) return fail(KDA_ERR_NULL, "kv pool descriptor is NULL");
@@ -279,35 +281,101 @@ kda_status check_attn_rows(const kda_kv_pool* p, const void* q, kda_dtype in, in
   return KDA_OK;
 }
 
-AttnArgs attn_args(const kda_kv_pool* p, const void* q, int64_t q_ld, void* o, int32_t Hq, float scale,
-                   int32_t window, int32_t sinks, const int32_t* table, int32_t max_pages, int64_t rows) {
+// How a call's rows are cut and how many workgroups share a tile's blocks.
+struct AttnPlan {
+  bool decode;        // the decode kernel: one tile per request, at most kDecodeRows rows
+  int32_t tile_rows;
+  int64_t units, splits;
+  size_t bytes;       // workspace of the partial results
+};
+
+// Blocks the farthest-reaching tile can see.
+int64_t reach_blocks(int64_t end, int64_t len, int32_t window, int32_t sinks) {
+  int64_t blocks = (end + kKvBlock - 1) / kKvBlock;
+  if (window)
+    blocks = std::min<int64_t>(blocks, ((int64_t)sinks + kKvBlock - 1) / kKvBlock +
+                                           ((int64_t)window + len + kKvBlock - 1) / kKvBlock + 1);
+  return blocks;
+}
+
+void plan_splits(AttnPlan* pl, const kda_kv_pool* p, int32_t Hq, int64_t rows, int64_t blocks, int64_t target) {
+  const int64_t wgs = std::max<int64_t>(1, pl->units * p->num_heads);
+  const int64_t want = (target + wgs - 1) / wgs;
+  pl->splits = std::max<int64_t>(1, std::min(want, (blocks + kMinTiles - 1) / kMinTiles));
+  pl->bytes = pl->splits == 1 ? 0 : (size_t)(rows * Hq * pl->splits * (p->head_dim + 2) * 4);
+}
+
+AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens, int32_t max_pages, int32_t window,
+                     int32_t sinks) {
+  const int64_t rows = (int64_t)tokens * (Hq / p->num_heads);
+  AttnPlan pl;
+  pl.decode = rows <= kDecodeRows;
+  pl.tile_rows = pl.decode ? kDecodeRows : 128;
+  pl.units = (int64_t)n * ((rows + pl.tile_rows - 1) / pl.tile_rows);
+  plan_splits(&pl, p, Hq, (int64_t)n * tokens,
+              reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks),
+              pl.decode ? kDecodeTarget : kTiledTarget);
+  return pl;
+}
+
+// Packed rows: 256-row tiles where they fill the card, 128-row ones otherwise
+// (and for fp32 queries, whose operand parts take the registers).
+AttnPlan plan_prefill(const kda_kv_pool* p, int32_t Hq, int32_t n, const int64_t* cu, const int64_t* start,
+                      int32_t window, int32_t sinks, kda_dtype in) {
+  const int64_t G = Hq / p->num_heads;
+  AttnPlan pl;
+  pl.decode = false;
+  int64_t blocks = 1;
+  for (pl.tile_rows = in == KDA_F32 ? 128 : 256;; pl.tile_rows = 128) {
+    pl.units = 0;
+    for (int32_t i = 0; i < n; ++i) {
+      const int64_t len = cu[i + 1] - cu[i], s = start ? start[i] : 0;
+      pl.units += (len * G + pl.tile_rows - 1) / pl.tile_rows;
+      blocks = std::max(blocks, reach_blocks(s + len, std::min<int64_t>(len, pl.tile_rows), window, sinks));
+    }
+    if (pl.tile_rows == 128 || pl.units * p->num_heads >= kFullCard) break;
+  }
+  plan_splits(&pl, p, Hq, cu[n], blocks, kTiledTarget);
+  return pl;
+}
+
+AttnArgs attn_args(const kda_kv_pool* p, const void* q, int64_t q_ld, void* o, kda_dtype out, int32_t Hq, float scale,
+                   int32_t window, int32_t sinks, const int32_t* table, int32_t max_pages, int64_t rows,
+                   const AttnPlan& pl, void* partial) {
   AttnArgs a;
   std::memset(&a, 0, sizeof(a));
   a.c = cache_of(p, table, max_pages);
-  a.q = q; a.o = o; a.q_ld = q_ld;
+  a.q = q;
+  a.o = o;
+  a.part_o = static_cast<float*>(partial);
+  a.part_ml = a.part_o + rows * Hq * pl.splits * p->head_dim;
+  a.q_ld = q_ld;
   a.Hq = Hq;
   a.G = Hq / p->num_heads;
-  a.scale = scale;
+  a.scale_log2 = scale * 1.44269504f;
   a.window = window;
   a.sinks = sinks;
   a.rows = (int32_t)rows;
+  a.units = (int32_t)pl.units;
+  a.tile_rows = pl.tile_rows;
+  a.splits = (int32_t)pl.splits;
+  a.out_bf16 = out == KDA_BF16;
   return a;
 }
 
-// How many workgroups share the cache of one (request, head): enough of them
-// for the card, each with at least kMinTiles blocks of the longest reach.
-int32_t decode_splits(const kda_kv_pool* p, int32_t n, int32_t tokens, int32_t max_pages, int32_t window,
-                      int32_t sinks) {
-  int64_t tiles = (int64_t)max_pages * p->page_tokens / kKvBlock;
-  if (window)
-    tiles = std::min<int64_t>(tiles, ((int64_t)sinks + kKvBlock - 1) / kKvBlock +
-                                         ((int64_t)window + tokens + kKvBlock - 1) / kKvBlock + 1);
-  const int64_t want = (kSplitTarget + (int64_t)n * p->num_heads - 1) / ((int64_t)n * p->num_heads);
-  return (int32_t)std::max<int64_t>(1, std::min(want, (tiles + kMinTiles - 1) / kMinTiles));
-}
-size_t decode_workspace(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens, int32_t splits) {
-  if (splits == 1 || tokens * (Hq / p->num_heads) > kDecodeRows) return 256;
-  return (size_t)n * tokens * Hq * splits * (p->head_dim + 2) * 4;
+kda_status run_attn(const kda_kv_pool* p, kda_dtype in, const AttnArgs& a, bool decode, const char* name,
+                    hipStream_t st) {
+  hipError_t e;
+  {
+    Launch L(name, st);
+    e = decode ? launch_attn_decode(p->head_dim, in == KDA_BF16, p->dtype == KDA_INT8, a, st)
+               : launch_attn_tiled(p->head_dim, in == KDA_BF16, p->dtype == KDA_INT8, a, st);
+  }
+  if (e == hipSuccess && a.splits > 1) {
+    Launch L("kda_attn_join", st);
+    e = launch_attn_join(p->head_dim, a, st);
+  }
+  return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
 }
 
 // No exception leaves an entry point.
@@ -462,7 +530,17 @@ size_t kda_attn_prefill_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_h
                                         const int64_t* cu_seqlens, const int64_t* start_pos, int32_t window,
                                         int32_t sinks) {
   if (check_attn(pool, KDA_BF16, KDA_BF16, num_q_heads, 1.f, window, sinks) != KDA_OK || num_seqs < 0) return 0;
-  return 256 + seq_table_bytes(num_seqs);
+  if (num_seqs == 0) return 256;
+  if (!cu_seqlens || cu_seqlens[0] != 0) return 0;
+  for (int32_t i = 0; i < num_seqs; ++i)
+    if (cu_seqlens[i + 1] < cu_seqlens[i] || cu_seqlens[i + 1] > kMaxTokens ||
+        (start_pos && (start_pos[i] < 0 || start_pos[i] > kMaxTokens)))
+      return 0;
+  // either input type fits
+  size_t bytes = 256;
+  for (kda_dtype in : {(kda_dtype)KDA_BF16, (kda_dtype)KDA_F32})
+    bytes = std::max(bytes, plan_prefill(pool, num_q_heads, num_seqs, cu_seqlens, start_pos, window, sinks, in).bytes);
+  return seq_table_bytes(num_seqs) + bytes;
 }
 
 kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld, void* o,
@@ -479,24 +557,31 @@ kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in
     std::vector<KvSeq> seqs;
     int64_t rows, units;
     s = pack_seqs(num_seqs, cu_seqlens, start_pos, (int64_t)max_pages * pool->page_tokens, "page table",
-                  [](int64_t, int64_t len) { return len; }, &seqs, &rows, &units);
+                  [](int64_t, int64_t) { return (int64_t)0; }, &seqs, &rows, &units);
     if (s != KDA_OK || rows == 0) return s == KDA_OK ? ok() : s;
     s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
     if (s != KDA_OK) return s;
-    s = check_workspace(workspace, workspace_bytes, 256 + seq_table_bytes(num_seqs));
+    const AttnPlan pl = plan_prefill(pool, num_q_heads, num_seqs, cu_seqlens, start_pos, window, sinks, in_dtype);
+    if (pl.units * pool->num_heads * pl.splits > kMaxTokens || rows * num_q_heads > kMaxTokens)
+      return fail(KDA_ERR_SHAPE, "too much work for one call");
+    const size_t table_bytes = seq_table_bytes(num_seqs);
+    s = check_workspace(workspace, workspace_bytes, table_bytes + std::max<size_t>(256, pl.bytes));
     if (s != KDA_OK) return s;
+    int32_t unit = 0;
+    for (KvSeq& q1 : seqs) {
+      q1.unit = unit;
+      unit += (int32_t)(((int64_t)q1.len * (num_q_heads / pool->num_heads) + pl.tile_rows - 1) / pl.tile_rows);
+    }
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (validating()) {
       s = check_pages(pool, page_table, max_pages, seqs, window, sinks, false, true, st);
       if (s != KDA_OK) return s;
     }
-    AttnArgs a = attn_args(pool, q, q_ld, o, num_q_heads, scale, window, sinks, page_table, max_pages, rows);
+    AttnArgs a = attn_args(pool, q, q_ld, o, out_dtype, num_q_heads, scale, window, sinks, page_table, max_pages,
+                           rows, pl, static_cast<uint8_t*>(workspace) + table_bytes);
     s = ship_seqs(seqs, workspace, &a.b, st);
     if (s != KDA_OK) return s;
-    Launch L("kda_attn_prefill", st);
-    const hipError_t e = launch_attn(pool->head_dim, in_dtype == KDA_BF16, out_dtype == KDA_BF16,
-                                     pool->dtype == KDA_INT8, a, st);
-    return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
+    return run_attn(pool, in_dtype, a, false, "kda_attn_prefill", st);
   });
 }
 
@@ -506,7 +591,7 @@ size_t kda_attn_decode_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_he
       tokens > 64 || max_pages < 1 || n > 1 << 24 || (int64_t)max_pages * pool->page_tokens > kMaxTokens)
     return 0;
   if (n == 0) return 256;
-  return decode_workspace(pool, num_q_heads, n, tokens, decode_splits(pool, n, tokens, max_pages, window, sinks));
+  return std::max<size_t>(256, plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks).bytes);
 }
 
 kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld, void* o,
@@ -523,10 +608,10 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
     const int64_t rows = (int64_t)n * tokens;
     s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
     if (s != KDA_OK) return s;
-    const int32_t splits = decode_splits(pool, n, tokens, max_pages, window, sinks);
-    if ((int64_t)n * pool->num_heads * splits > kMaxTokens || rows * num_q_heads > kMaxTokens)
+    const AttnPlan pl = plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks);
+    if (pl.units * pool->num_heads * pl.splits > kMaxTokens || rows * num_q_heads > kMaxTokens)
       return fail(KDA_ERR_SHAPE, "too much work for one call");
-    s = check_workspace(workspace, workspace_bytes, decode_workspace(pool, num_q_heads, n, tokens, splits));
+    s = check_workspace(workspace, workspace_bytes, std::max<size_t>(256, pl.bytes));
     if (s != KDA_OK) return s;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (validating()) {
@@ -535,42 +620,10 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
       if (s == KDA_OK) s = check_pages(pool, page_table, max_pages, seqs, window, sinks, false, true, st);
       if (s != KDA_OK) return s;
     }
-    if (tokens * (num_q_heads / pool->num_heads) <= kDecodeRows) {
-      DecodeAttnArgs a;
-      std::memset(&a, 0, sizeof(a));
-      a.c = cache_of(pool, page_table, max_pages);
-      a.q = q;
-      a.o = o;
-      a.part_o = static_cast<float*>(workspace);
-      a.part_ml = a.part_o + (size_t)rows * num_q_heads * splits * pool->head_dim;
-      a.pos = pos;
-      a.q_ld = q_ld;
-      a.Hq = num_q_heads;
-      a.G = num_q_heads / pool->num_heads;
-      a.scale_log2 = scale * 1.44269504f;
-      a.window = window;
-      a.sinks = sinks;
-      a.n = n;
-      a.tokens = tokens;
-      a.splits = splits;
-      a.out_bf16 = out_dtype == KDA_BF16;
-      hipError_t e;
-      {
-        Launch L("kda_attn_decode", st);
-        e = launch_decode_attn(pool->head_dim, in_dtype == KDA_BF16, pool->dtype == KDA_INT8, a, st);
-      }
-      if (e == hipSuccess && splits > 1) {
-        Launch L("kda_attn_join", st);
-        e = launch_join(pool->head_dim, a, st);
-      }
-      return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
-    }
-    AttnArgs a = attn_args(pool, q, q_ld, o, num_q_heads, scale, window, sinks, page_table, max_pages, rows);
-    a.b = step_batch(pos, n, tokens, 1);
-    Launch L("kda_attn_decode", st);
-    const hipError_t e = launch_attn(pool->head_dim, in_dtype == KDA_BF16, out_dtype == KDA_BF16,
-                                     pool->dtype == KDA_INT8, a, st);
-    return e == hipSuccess ? ok() : hip_fail(e, "attention launch");
+    AttnArgs a = attn_args(pool, q, q_ld, o, out_dtype, num_q_heads, scale, window, sinks, page_table, max_pages,
+                           rows, pl, workspace);
+    a.b = step_batch(pos, n, tokens, (int32_t)(pl.units / n));
+    return run_attn(pool, in_dtype, a, pl.decode, "kda_attn_decode", st);
   });
 }
 
