@@ -128,7 +128,7 @@ __device__ __forceinline__ bool all_seen(int64_t first, int64_t last, int window
   const int64_t j0 = (int64_t)blk * kKvBlock, j1 = j0 + kKvBlock - 1;
   return j1 <= first && (!window || j0 > last - window || j1 < sinks);
 }
-__device__ __forceinline__ bool sees(int64_t p, int64_t j, int window, int sinks) {
+__device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {  // positions below 2^30
   return j <= p && (!window || j > p - window || j < sinks);
 }
 

@@ -40,28 +40,44 @@ __device__ __forceinline__ f32x16 zero16() {
   return z;
 }
 
-template <int D, int EB, int NP, int QT>
-__global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_kernel(AttnArgs a) {
+// Sum of an operand's eight weights, added to l.
+__device__ __forceinline__ float add8(f16x8 w, float l) {
+  const f16x2 one = {(_Float16)1.f, (_Float16)1.f};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) l = __builtin_amdgcn_fdot2(f16x2{w[2 * i], w[2 * i + 1]}, one, l, false);
+  return l;
+}
+__device__ __forceinline__ float add8(bf16x8 w, float l) {
+  const bf16x2_t one = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{w[2 * i], w[2 * i + 1]}, one, l, false);
+  return l;
+}
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+template <int D, int EB, int NP, int WV>
+__global__ __launch_bounds__(64 * WV, NP == 3 ? 1 : 2) void attn_tiled_kernel(AttnArgs a) {
   typedef AttnOp<EB> Op;
   typedef typename Op::Frag Frag;
-  constexpr int KS = D / 16, DT = D / 32, ROWS = 128 * QT;
+  constexpr int KS = D / 16, DT = D / 32, ROWS = 32 * WV, NT = 64 * WV;
   constexpr int PART = 2 * kKvBlock * D;    // bytes of a 16-bit K or V part in LDS
   constexpr int RAW = kKvBlock * D * EB;    // bytes of a part in the cache
   __shared__ __align__(1024) uint8_t lds[2][2][2 * PART];  // buffer, block of the tile, K part | V part
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
   // heads fastest: the workgroups of one head share an XCD's L2 where 8 divides the
   // heads; last tiles first, they see the most
   const int h = blockIdx.x % a.c.H, rest = blockIdx.x / a.c.H;
   const int sp = rest % a.splits, unit = a.units - 1 - rest / a.splits;
-  const int req = kv_find_unit(a.b, unit);
-  const KvSeq s = kv_seq(a.b, req);
+  const int req = uni(kv_find_unit(a.b, unit));
+  KvSeq s = kv_seq(a.b, req);
+  s.row = uni(s.row); s.start = uni(s.start); s.len = uni(s.len); s.unit = uni(s.unit);
   const int row0 = (unit - s.unit) * ROWS, rows = s.len * a.G;
   const int64_t cap = (int64_t)a.c.max_pages * a.c.page_tokens;
   const bool off = s.start < 0, over = (int64_t)s.start + s.len > cap;
   if (off || over) {
     if (sp == 0)
-      for (int i = threadIdx.x; i < min(ROWS, rows - row0) * D; i += 256) {
+      for (int i = threadIdx.x; i < min(ROWS, rows - row0) * D; i += NT) {
         const int row = row0 + i / D;
         const int64_t at = ((int64_t)(s.row + row / a.G) * a.Hq + h * a.G + row % a.G) * D + i % D;
         const float y = off ? 0.f : __builtin_nanf("");
@@ -70,33 +86,27 @@ __global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_ke
       }
     return;
   }
-  const int64_t tp0 = s.start + row0 / a.G, tp1 = s.start + (min(rows, row0 + ROWS) - 1) / a.G;
+  const int tp0 = s.start + row0 / a.G, tp1 = s.start + (min(rows, row0 + ROWS) - 1) / a.G;
   const Reach reach = reach_of(tp0, tp1, a.window, a.sinks);
   const Chunk ch = chunk_of(reach.count(), a.splits, sp);
   if (ch.begin >= ch.end) return;
 
   // ---- queries: lane (half, col) holds row col's channels 16 ks + 8 half ..
-  Frag qf[QT][KS][NP];
-  float qc[QT];
-  int qp[QT];  // positions (below 2^30)
-  int64_t oat[QT];
-  bool live[QT];
-#pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const int row = row0 + (wv * QT + t) * 32 + col;
-    live[t] = row < rows;
-    const int rr = live[t] ? row : rows - 1, tok = rr / a.G, hq = h * a.G + rr % a.G;
-    qp[t] = s.start + tok;
-    oat[t] = (int64_t)(s.row + tok) * a.Hq + hq;
+  const int row = row0 + wv * 32 + col;
+  const bool live = row < rows;
+  const int tok = (live ? row : rows - 1) / a.G, hq = h * a.G + (live ? row : rows - 1) % a.G;
+  const int qp = s.start + tok;  // position (below 2^30)
+  const int64_t oat = (int64_t)(s.row + tok) * a.Hq + hq;
+  Frag qf[KS][NP];
+  float qc = a.scale_log2;
+  {
     const int64_t at = (int64_t)(s.row + tok) * a.q_ld + (int64_t)hq * D + 8 * half;
-    float amax = 0.f;
     if constexpr (NP == 1 && EB == 2) {
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
-        qf[t][ks][0] = *reinterpret_cast<const Frag*>(reinterpret_cast<const uint16_t*>(a.q) + at + 16 * ks);
-      qc[t] = a.scale_log2;
+        qf[ks][0] = *reinterpret_cast<const Frag*>(reinterpret_cast<const uint16_t*>(a.q) + at + 16 * ks);
     } else {
-      float x[KS][8];
+      float x[KS][8], amax = 0.f;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         if constexpr (NP == 1) {
@@ -114,31 +124,26 @@ __global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_ke
       }
       float f = 1.f, inv = 1.f;
       if constexpr (EB == 1) f = fit_f16(half_max(amax), &inv);
-      qc[t] = a.scale_log2 * inv;
+      qc *= inv;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
         if constexpr (EB == 1) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) x[ks][i] *= f;
         }
-        split8<EB, NP>(x[ks], qf[t][ks]);
+        split8<EB, NP>(x[ks], qf[ks]);
       }
     }
   }
   // positions of the wave's rows
-  const int wr0 = row0 + wv * QT * 32, wr1 = min(rows, wr0 + QT * 32) - 1;
+  const int wr0 = row0 + wv * 32, wr1 = min(rows, wr0 + 32) - 1;
   const bool idle = wr0 >= rows;
-  const int64_t wp0 = s.start + min(wr0, rows - 1) / a.G, wp1 = s.start + max(wr1, 0) / a.G;
+  const int wp0 = s.start + min(wr0, rows - 1) / a.G, wp1 = s.start + max(wr1, 0) / a.G;
 
-  f32x16 acc[QT][DT];
-  float m[QT], l[QT];
+  f32x16 acc[DT];
+  float m = kNegInf, l = 0.f;
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    m[t] = kNegInf;
-    l[t] = 0.f;
-#pragma unroll
-    for (int d = 0; d < DT; ++d) acc[t][d] = zero16();
-  }
+  for (int d = 0; d < DT; ++d) acc[d] = zero16();
 
   // ---- staging: 64 tokens (two blocks) a step
   const int per = a.c.page_tokens / kKvBlock, count = ch.end - ch.begin;
@@ -154,10 +159,11 @@ __global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_ke
       if (pg < 0 || pg >= a.c.num_pages) pg = -1;
     }
   };
-  constexpr int UNITS = 2 * RAW / 16 / 256;  // 16-byte units of a raw block a thread moves
-  u32x4_t raw[2][UNITS];                     // int8: the next tile's codes
-  float nks[2], nvs[2], cks[2] = {1.f, 1.f}, cvs[2] = {1.f, 1.f};
-  bool nbad[2] = {false, false}, cbad[2] = {false, false};
+  constexpr int UNITS = 2 * RAW / 16 / NT;  // 16-byte units of a raw block a thread moves
+  static_assert(UNITS >= 1, "a block has a unit for every thread");
+  u32x4_t raw[2][UNITS];                    // int8: the next tile's codes
+  float nks[2] = {1.f, 1.f}, nvs[2] = {1.f, 1.f};
+  int nbad[2] = {0, 0};
   auto fetch = [&](int i0, int buf) {  // blocks i0, i0 + 1 of the chunk
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
@@ -169,7 +175,7 @@ __global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_ke
       if constexpr (EB == 2) {
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
-          const int o = (u * 256 + wv * 64) * 16;
+          const int o = (u * NT + wv * 64) * 16;
           __builtin_amdgcn_global_load_lds(
               reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(reinterpret_cast<uintptr_t>(src + o + 16 * lane)),
               (__attribute__((address_space(3))) uint32_t*)(&lds[buf][b][o]), 16, 0, 0);
@@ -177,7 +183,7 @@ __global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_ke
       } else {
 #pragma unroll
         for (int u = 0; u < UNITS; ++u)
-          raw[b][u] = *reinterpret_cast<const u32x4_t*>(src + (u * 256 + threadIdx.x) * 16);
+          raw[b][u] = *reinterpret_cast<const u32x4_t*>(src + (u * NT + threadIdx.x) * 16);
         const float* sc = reinterpret_cast<const float*>(head + (int64_t)per * (2 * RAW)) + 2 * inner;
         nks[b] = sc[0];
         nvs[b] = sc[1];
@@ -191,7 +197,7 @@ __global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_ke
         if (i0 + b >= count) break;
 #pragma unroll
         for (int u = 0; u < UNITS; ++u) {
-          const int i = u * 256 + threadIdx.x, part = i / (RAW / 16), x = i % (RAW / 16);
+          const int i = u * NT + threadIdx.x, part = i / (RAW / 16), x = i % (RAW / 16);
           // unit (.., c, inner 16 or 64 places) of codes becomes units (.., 2 c) and (.., 2 c + 1)
           const int low = part == 0 ? 16 : 64, c = x / low, y = x % low;
           uint8_t* to = &lds[buf][b][part * PART + (2 * c * low + y) * 16];
@@ -201,6 +207,112 @@ __global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_ke
       }
     }
   };
+  // byte offsets of the lane's operands in a block: matrix row i = 8 a + 4 half' + b
+  // of S^T holds token_of(a, half', b)
+  const int koff = 16 * (((col >> 3) & 1) * (32 * KS) + 8 * (col >> 4) + (col & 7) + 16 * half);
+  const int voff = PART + 16 * ((col >> 4) * 64 + half * 16 + (col & 15));
+
+  // One block against the wave's rows; full: every row sees all of it; bad: its page
+  // index or a scale is not usable, rows that see it become NaN.
+  auto step = [&](const uint8_t* kb, int blk, bool bad, bool full, float ksc, float vsc) __attribute__((always_inline)) {
+    float c = qc, lv = 0.f, iv = 1.f;
+    if constexpr (EB == 1) {
+      c = fmaxf(qc * ksc, 0x1p-126f);  // above 0, so that -inf stays -inf
+      vsc = vsc == 0.f ? 1.f : vsc < 0x1p-120f ? 0x1p-120f : vsc;
+      lv = __builtin_amdgcn_logf(vsc);
+      iv = __builtin_amdgcn_rcpf(vsc);
+    }
+    Frag kf[KS];
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) kf[ks] = *reinterpret_cast<const Frag*>(kb + koff + 512 * ks);
+    f32x16 x = zero16();
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) x = Op::mma32(kf[ks], qf[ks][p], x);
+    if (!full) {
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int j = blk * kKvBlock + token_of(e >> 2, half, e & 3);
+        x[e] = !sees(qp, j, a.window, a.sinks) ? kNegInf : bad ? __builtin_nanf("") : x[e];
+      }
+    }
+    float mx = x[0];
+#pragma unroll
+    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
+    mx = __builtin_fmaf(half_max(mx), c, lv);
+    if (__any(mx > m)) {
+      const float mn = fmaxf(m, mx), al = decay(m, mn);
+      m = mn;
+      l *= al;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) acc[d] *= al;
+    }
+    const float sub = lv + Op::kLift - (m == kNegInf ? 0.f : m);
+    Frag pf[2][NP];
+    float sum = 0.f;
+    {
+      float w[16];
+#pragma unroll
+      for (int e = 0; e < 16; ++e) w[e] = exp2_f(__builtin_fmaf(x[e], c, sub));
+      split8<EB, NP>(w, pf[0]);
+      split8<EB, NP>(w + 8, pf[1]);
+      if constexpr (NP == 1) {
+        sum = add8(pf[1][0], add8(pf[0][0], 0.f));
+      } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) sum += w[e];
+      }
+    }
+    l = __builtin_fmaf(sum, iv, l);
+    Frag vf[2 * DT];
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i) vf[i] = *reinterpret_cast<const Frag*>(kb + voff + (i >> 1) * 2048 + (i & 1) * 512);
+#pragma unroll
+    for (int i = 0; i < 2 * DT; ++i)
+#pragma unroll
+      for (int p = 0; p < NP; ++p) acc[i >> 1] = Op::mma32(vf[i], pf[i & 1][p], acc[i >> 1]);
+  };
+
+  // bf16 tiles of which some row does not see some token: 0 * V there (an infinity or
+  // NaN, or a slot never written) must not reach that row.  Where the tile has such
+  // values, rows that see one take it, and it is taken out of the operand.  Rare.
+  auto purify = [&](int buf, int i0) {
+    constexpr int VU = PART / 16;
+    const int n = min(2, count - i0) * VU;
+    bool odd = false;
+    for (int i = threadIdx.x; i < n; i += NT) {
+      const u16x8 u = *reinterpret_cast<const u16x8*>(&lds[buf][i / VU][PART + 16 * (i % VU)]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) odd |= (u[e] & 0x7f80u) == 0x7f80u;
+    }
+    if (!__syncthreads_or(odd)) return;
+    if (!idle) {
+#pragma unroll 1
+      for (int i = 0; i < 32 * (n / VU); ++i) {
+        const int t = i & 31, j = reach.block(ch.begin + i0 + (i >> 5)) * kKvBlock + t;
+        const bool see = sees(qp, j, a.window, a.sinks);
+        const uint8_t* vt = &lds[buf][i >> 5][PART + 16 * (16 * ((t & 15) >> 2) + 4 * half) + 2 * ((t & 3) + 4 * (t >> 4))];
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int chn = 32 * d + 8 * (r >> 2) + (r & 3);  // + 4 * half
+            const float v = bf16_to_f32(*reinterpret_cast<const uint16_t*>(vt + 16 * ((chn >> 4) * 64 + (chn & 15))));
+            acc[d][r] += see && !(fabsf(v) < __builtin_inff()) ? v : 0.f;
+          }
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < n; i += NT) {
+      u16x8* at = reinterpret_cast<u16x8*>(&lds[buf][i / VU][PART + 16 * (i % VU)]);
+      u16x8 u = *at;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = (u[e] & 0x7f80u) == 0x7f80u ? 0 : u[e];
+      *at = u;
+    }
+    __syncthreads();
+  };
 
   look_up(0);
   fetch(0, 0);
@@ -208,163 +320,71 @@ __global__ __launch_bounds__(256, QT == 2 || NP == 3 ? 1 : 2) void attn_tiled_ke
     put(i0, buf);
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();  // the tile is in LDS, and every wave has left the other buffer
+    float cks[2], cvs[2];
+    int cbad[2];
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-      cbad[b] = nbad[b];
-      if constexpr (EB == 1) { cks[b] = nks[b]; cvs[b] = nvs[b]; }
+      cks[b] = __uint_as_float(uni(__float_as_uint(nks[b])));
+      cvs[b] = __uint_as_float(uni(__float_as_uint(nvs[b])));
+      // a scale that is not finite: its block's values are NaN to every row that sees it
+      cbad[b] = nbad[b] || (EB == 1 && !(cks[b] < __builtin_inff() && cvs[b] < __builtin_inff()));
+      if (cbad[b]) cks[b] = cvs[b] = 1.f;
     }
     if (i0 + 2 < count) {
       if (((i0 + 2) & 63) == 0) look_up(i0 + 2);
       fetch(i0 + 2, buf ^ 1);
     }
+    if constexpr (EB == 2) {
+      bool part = false;
+      for (int b = 0; b < 2 && i0 + b < count; ++b)
+        part |= cbad[b] || !all_seen(tp0, tp1, a.window, a.sinks, reach.block(ch.begin + i0 + b));
+      if (part) purify(buf, i0);
+    }
     if (idle) continue;
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if (i0 + b >= count) break;
+#pragma unroll 1
+    for (int b = 0; b < 2 && i0 + b < count; ++b) {
       const int blk = reach.block(ch.begin + i0 + b);
-      if ((int64_t)blk * kKvBlock > wp1) continue;  // past every row of the wave
-      const bool bad = cbad[b], full = !bad && all_seen(wp0, wp1, a.window, a.sinks, blk);
-      float ksc = 1.f, lv = 0.f, iv = 1.f;
-      if (EB == 1 && !bad) {
-        ksc = cks[b];
-        const float vs = cvs[b] == 0.f ? 1.f : cvs[b] < 0x1p-120f ? 0x1p-120f : cvs[b];
-        lv = __builtin_amdgcn_logf(vs);
-        iv = 1.f / vs;
-      }
-      const uint8_t* kb = &lds[buf][b][0];
-      const uint8_t* vb = &lds[buf][b][PART];
-      f32x16 x[QT];
-#pragma unroll
-      for (int t = 0; t < QT; ++t) x[t] = zero16();
-      // matrix row i = 8 a + 4 half' + b holds token 16 (a & 1) + 8 (a >> 1) + 4 half' + b
-      const int krow = ((col >> 3) & 1) * (16 * 2 * KS) + 8 * (col >> 4) + (col & 7);
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const Frag kf = *reinterpret_cast<const Frag*>(kb + 16 * (krow + 16 * (2 * ks + half)));
-#pragma unroll
-        for (int t = 0; t < QT; ++t)
-#pragma unroll
-          for (int p = 0; p < NP; ++p) x[t] = Op::mma32(kf, qf[t][ks][p], x[t]);
-      }
-      Frag pf[QT][2][NP];
-      bf16x8 seen[QT][2];
-#pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        const float c = qc[t] * ksc;
-        float w[16], mx = kNegInf;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = __builtin_fmaf(x[t][e], c, lv);
-        if (!full) {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int j = blk * kKvBlock + token_of(e >> 2, half, e & 3);
-            const bool see = sees(qp[t], j, a.window, a.sinks);
-            w[e] = !see ? kNegInf : bad ? __builtin_nanf("") : w[e];
-            seen[t][e >> 3][e & 7] = static_cast<__bf16>(see ? 1.f : 0.f);
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) mx = fmaxf(mx, w[e]);
-        mx = half_max(mx);
-        if (__any(mx > m[t])) {
-          const float mn = fmaxf(m[t], mx), al = decay(m[t], mn);
-          m[t] = mn;
-          l[t] *= al;
-#pragma unroll
-          for (int d = 0; d < DT; ++d) acc[t][d] *= al;
-        }
-        const float mu = (m[t] == kNegInf ? 0.f : m[t]) - Op::kLift;
-        float sum = 0.f;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          w[e] = exp2_f(w[e] - mu);
-          sum += w[e];
-        }
-        if (EB == 1) l[t] += sum == 0.f ? 0.f : sum * iv;  // a block of which the row sees nothing adds nothing
-        else l[t] += sum;
-        split8<EB, NP>(w, pf[t][0]);
-        split8<EB, NP>(w + 8, pf[t][1]);
-      }
-#pragma unroll
-      for (int d = 0; d < DT; ++d) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          Frag vf = *reinterpret_cast<const Frag*>(vb + 16 * (((2 * d + (col >> 4)) * 4 + 2 * j + half) * 16 + (col & 15)));
-          if constexpr (EB == 2) {
-            if (!full) {  // 0 * V of a token a row does not see must not reach it: as in spread_nonfinite
-              u16x8 u = __builtin_bit_cast(u16x8, vf), f[3];
-              bool odd = false;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) odd |= (u[e] & 0x7f80u) == 0x7f80u;
-              if (__any(odd)) {
-                const float add[3] = {__builtin_inff(), kNegInf, __builtin_nanf("")};
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  const bool o = (u[e] & 0x7f80u) == 0x7f80u;
-                  f[0][e] = u[e] == 0x7f80u ? 0x3f80u : 0;
-                  f[1][e] = u[e] == 0xff80u ? 0x3f80u : 0;
-                  f[2][e] = o && (u[e] & 0x7fu) ? 0x3f80u : 0;
-                  if (o) u[e] = 0;
-                }
-                vf = __builtin_bit_cast(Frag, u);
-#pragma unroll
-                for (int t = 0; t < QT; ++t)
-#pragma unroll
-                  for (int k = 0; k < 3; ++k) {
-                    const f32x16 n = AttnOp<2>::mma32(__builtin_bit_cast(bf16x8, f[k]), seen[t][j], zero16());
-#pragma unroll
-                    for (int r = 0; r < 16; ++r)
-                      if (n[r] > 0.f) acc[t][d][r] += add[k];
-                  }
-              }
-            }
-          }
-#pragma unroll
-          for (int t = 0; t < QT; ++t)
-#pragma unroll
-            for (int p = 0; p < NP; ++p) acc[t][d] = Op::mma32(vf, pf[t][j][p], acc[t][d]);
-        }
-      }
+      if (blk * kKvBlock > wp1) continue;  // past every row of the wave
+      const bool bad = b ? cbad[1] : cbad[0];
+      step(&lds[buf][b][0], blk, bad, !bad && all_seen(wp0, wp1, a.window, a.sinks, blk), b ? cks[1] : cks[0],
+           b ? cvs[1] : cvs[0]);
     }
   }
 
+  const float ll = half_sum(l);
+  if (!live) return;
+  if (ch.used == 1) {
+    const float inv = 1.f / ll;
 #pragma unroll
-  for (int t = 0; t < QT; ++t) {
-    const float ll = half_sum(l[t]);
-    if (!live[t]) continue;
-    if (ch.used == 1) {
-      const float inv = 1.f / ll;
+    for (int d = 0; d < DT; ++d)
 #pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int64_t o = oat[t] * D + 32 * d + 8 * q + 4 * half;
-          const f32x4 y = f32x4{acc[t][d][4 * q], acc[t][d][4 * q + 1], acc[t][d][4 * q + 2], acc[t][d][4 * q + 3]} * inv;
-          if (a.out_bf16) *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.o) + o) = pack_bf16x4(y[0], y[1], y[2], y[3]);
-          else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.o) + o) = y;
-        }
-    } else {
-      float* po = a.part_o + (oat[t] * a.splits + sp) * D;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int q = 0; q < 4; ++q)
-          *reinterpret_cast<f32x4*>(po + 32 * d + 8 * q + 4 * half) =
-              f32x4{acc[t][d][4 * q], acc[t][d][4 * q + 1], acc[t][d][4 * q + 2], acc[t][d][4 * q + 3]};
-      if (half == 0) {
-        a.part_ml[2 * (oat[t] * a.splits + sp)] = m[t];
-        a.part_ml[2 * (oat[t] * a.splits + sp) + 1] = ll;
+      for (int q = 0; q < 4; ++q) {
+        const int64_t o = oat * D + 32 * d + 8 * q + 4 * half;
+        const f32x4 y = f32x4{acc[d][4 * q], acc[d][4 * q + 1], acc[d][4 * q + 2], acc[d][4 * q + 3]} * inv;
+        if (a.out_bf16) *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.o) + o) = pack_bf16x4(y[0], y[1], y[2], y[3]);
+        else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.o) + o) = y;
       }
+  } else {
+    float* po = a.part_o + (oat * a.splits + sp) * D;
+#pragma unroll
+    for (int d = 0; d < DT; ++d)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<f32x4*>(po + 32 * d + 8 * q + 4 * half) =
+            f32x4{acc[d][4 * q], acc[d][4 * q + 1], acc[d][4 * q + 2], acc[d][4 * q + 3]};
+    if (half == 0) {
+      a.part_ml[2 * (oat * a.splits + sp)] = m;
+      a.part_ml[2 * (oat * a.splits + sp) + 1] = ll;
     }
   }
 }
 
 template <int D, int EB, int NP> static void launch_qt(const AttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.units * a.c.H * a.splits)), block(256);
+  const dim3 grid((unsigned)(a.units * a.c.H * a.splits));
   if (a.tile_rows == 256) {
-    if constexpr (NP == 1) hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP, 2>), grid, block, 0, st, a);
+    if constexpr (NP == 1 && D * EB >= 128) hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP, 8>), grid, dim3(512), 0, st, a);
   } else {
-    hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP, 1>), grid, block, 0, st, a);
+    hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP, 4>), grid, dim3(256), 0, st, a);
   }
 }
 template <int D> static void launch_d(bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st) {

@@ -319,14 +319,16 @@ AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens
 }
 
 // Packed rows: 256-row tiles where they fill the card, 128-row ones otherwise
-// (and for fp32 queries, whose operand parts take the registers).
+// (and for fp32 queries, whose operand parts take the registers, and int8 blocks
+// of 64 channels, which have no 16-byte unit for every thread of the larger tile).
 AttnPlan plan_prefill(const kda_kv_pool* p, int32_t Hq, int32_t n, const int64_t* cu, const int64_t* start,
                       int32_t window, int32_t sinks, kda_dtype in) {
   const int64_t G = Hq / p->num_heads;
   AttnPlan pl;
   pl.decode = false;
   int64_t blocks = 1;
-  for (pl.tile_rows = in == KDA_F32 ? 128 : 256;; pl.tile_rows = 128) {
+  const bool wide = in == KDA_BF16 && p->head_dim * (p->dtype == KDA_INT8 ? 1 : 2) >= 128;
+  for (pl.tile_rows = wide ? 256 : 128;; pl.tile_rows = 128) {
     pl.units = 0;
     for (int32_t i = 0; i < n; ++i) {
       const int64_t len = cu[i + 1] - cu[i], s = start ? start[i] : 0;
