@@ -235,8 +235,9 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) mx = fmaxf(mx, x[e]);
       mx = group_max(mx);
-      if (__any(mx > m[mt])) {
-        const float mn = fmaxf(m[mt], mx), al = decay(m[mt], mn);
+      const bool grow = mx > m[mt] + kSlack;
+      if (__any(grow)) {
+        const float mn = grow ? mx : m[mt], al = grow ? decay(m[mt], mn) : 1.f;
         m[mt] = mn;
         l[mt] *= al;
 #pragma unroll

@@ -8,9 +8,12 @@
 //   - q rows are brought to [2^7, 2^8) by a power of two, undone in the logit's
 //     factor, so that no bf16 or fp32 q leaves fp16's range;
 //   - the block's value scale goes into the weight, w' = exp2(x + log2 vs - m'),
-//     m' the running maximum of x + log2 vs, so that w' <= 1 whatever the
-//     scales; the normaliser sums w' / vs.  w' carries a factor 2^14, which
-//     leaves 38 binary orders of weights above fp16's smallest number.
+//     m' the running reference of x + log2 vs, so that w' is bounded whatever the
+//     scales; the normaliser sums w' / vs.  w' carries a factor 2^6, which with
+//     the slack below stays in fp16's range and leaves 30 binary orders of
+//     weights above its smallest number.
+// The reference is the running maximum, or up to 2^kSlack below it: the sums are
+// rescaled only where a row's maximum passes its reference by more.
 // fp32 queries (and their weights) are split into parts that add up to 22 bits
 // (two fp16) or 24 (three bf16), one product each: the cached operand is exact
 // in either type, so the products keep fp32's accuracy.
@@ -25,6 +28,7 @@ typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 constexpr float kNegInf = -__builtin_inff();
+constexpr float kSlack = 8.f;
 
 template <int EB> struct AttnOp;
 template <> struct AttnOp<2> {
@@ -42,7 +46,7 @@ template <> struct AttnOp<2> {
 template <> struct AttnOp<1> {
   typedef f16x8 Frag;
   typedef _Float16 T;
-  static constexpr float kLift = 14.f;
+  static constexpr float kLift = 6.f;
   static constexpr int kParts = 2;
   __device__ static __forceinline__ f32x4 mma(Frag a, Frag b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);

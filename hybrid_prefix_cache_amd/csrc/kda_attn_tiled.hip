@@ -4,15 +4,15 @@
 //
 // o = sum_j w_j v_j / sum_j w_j, w_j = exp(scale q . k_j).  The rows of one
 // sequence and key/value head, token-major and head-minor (row = token * G + g),
-// are cut into tiles of 128 * QT; a tile's workgroup walks the blocks its rows
-// see, 64 tokens at a time, through two LDS buffers.
+// are cut into tiles of 128, 32 for each of a workgroup's four waves; the tile
+// walks the 32-token blocks its rows see through two LDS buffers.
 //
-// Per 32-token block and 32-row column tile: S^T = K Q^T, then O^T += V^T P^T on
-// 32x32x16 matrix instructions.  The cache stores operands in matrix order, so a
-// bf16 block goes to LDS as it is, by direct-to-LDS loads of 16 bytes a lane, and
-// every operand is one contiguous ds_read_b128; int8 codes become fp16 on the
-// way through registers.  A lane's 16 logits are one row's, in the order in which
-// the V part holds its tokens, so the weights feed the second product from
+// Per block: S^T = K Q^T, then O^T += V^T P^T on 32x32x16 matrix instructions.
+// The cache stores operands in matrix order, so a bf16 block goes to LDS as it
+// is, by direct-to-LDS loads of 16 bytes a lane, and every operand is one
+// contiguous ds_read_b128 without bank conflicts; int8 codes become fp16 on the
+// way through registers.  A lane's 16 logits are one row's, in the order in
+// which the V part holds its tokens, so the weights feed the second product from
 // registers and a row's maximum and sum cross one lane exchange.
 //
 // Few tiles (a short resumed prompt over a long cache) are split over the cache
@@ -40,6 +40,19 @@ __device__ __forceinline__ f32x16 zero16() {
   return z;
 }
 
+constexpr int kVmcnt0 = 0x0f70;  // s_waitcnt operand: vmcnt(0), the other counters not waited for
+
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+// Each lane's 16 bytes at src to LDS, lane after lane from dst (uniform).  Not the
+// builtin: with it the compiler, which cannot tell the two buffers apart, waits for
+// these loads before the next LDS read; the loop waits for them itself, before the
+// barrier that hands the buffer over.
+__device__ __forceinline__ void to_lds16(const uint8_t* src, uint8_t* dst) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)dst;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uni(at)), "v"(src) : "m0", "memory");
+}
+
 // Sum of an operand's eight weights, added to l.
 __device__ __forceinline__ float add8(f16x8 w, float l) {
   const f16x2 one = {(_Float16)1.f, (_Float16)1.f};
@@ -53,16 +66,14 @@ __device__ __forceinline__ float add8(bf16x8 w, float l) {
   for (int i = 0; i < 4; ++i) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{w[2 * i], w[2 * i + 1]}, one, l, false);
   return l;
 }
-__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
-template <int D, int EB, int NP, int WV>
-__global__ __launch_bounds__(64 * WV, NP == 3 ? 1 : 2) void attn_tiled_kernel(AttnArgs a) {
+template <int D, int EB, int NP>
+__global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled_kernel(AttnArgs a) {
   typedef AttnOp<EB> Op;
   typedef typename Op::Frag Frag;
-  constexpr int KS = D / 16, DT = D / 32, ROWS = 32 * WV, NT = 64 * WV;
+  constexpr int KS = D / 16, DT = D / 32, ROWS = kTileRows, NT = 256;
   constexpr int PART = 2 * kKvBlock * D;    // bytes of a 16-bit K or V part in LDS
   constexpr int RAW = kKvBlock * D * EB;    // bytes of a part in the cache
-  __shared__ __align__(1024) uint8_t lds[2][2][2 * PART];  // buffer, block of the tile, K part | V part
+  __shared__ __align__(1024) uint8_t lds[2][2 * PART];  // two blocks: K part | V part
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
   // heads fastest: the workgroups of one head share an XCD's L2 where 8 divides the
@@ -145,11 +156,11 @@ __global__ __launch_bounds__(64 * WV, NP == 3 ? 1 : 2) void attn_tiled_kernel(At
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = zero16();
 
-  // ---- staging: 64 tokens (two blocks) a step
+  // ---- staging: one block a step
   const int per = a.c.page_tokens / kKvBlock, count = ch.end - ch.begin;
   const uint8_t* head0 = a.c.base + h * a.c.head_bytes;
   int pg = 0, in = 0;
-  auto look_up = [&](int base) {
+  auto look_up = [&](int base) {  // lane i: page and place of block base + i of the chunk
     const int i = base + lane;
     if (i < count) {
       const int blk = reach.block(ch.begin + i);
@@ -161,49 +172,38 @@ __global__ __launch_bounds__(64 * WV, NP == 3 ? 1 : 2) void attn_tiled_kernel(At
   };
   constexpr int UNITS = 2 * RAW / 16 / NT;  // 16-byte units of a raw block a thread moves
   static_assert(UNITS >= 1, "a block has a unit for every thread");
-  u32x4_t raw[2][UNITS];                    // int8: the next tile's codes
-  float nks[2] = {1.f, 1.f}, nvs[2] = {1.f, 1.f};
-  int nbad[2] = {0, 0};
-  auto fetch = [&](int i0, int buf) {  // blocks i0, i0 + 1 of the chunk
+  u32x4_t raw[UNITS];                       // int8: the next block's codes
+  float nks, nvs;
+  int nbad = 0;
+  auto fetch = [&](int i, int buf) {  // block i of the chunk
+    const int page = __builtin_amdgcn_readlane(pg, i & 63), inner = __builtin_amdgcn_readlane(in, i & 63);
+    nbad = page < 0;  // a bad page: page 0's bytes, whose values never count
+    const uint8_t* head = head0 + (int64_t)max(page, 0) * a.c.page_bytes;
+    const uint8_t* src = head + (int64_t)inner * (2 * RAW);
+    if constexpr (EB == 2) {
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      if (i0 + b >= count) break;
-      const int page = __builtin_amdgcn_readlane(pg, (i0 + b) & 63), inner = __builtin_amdgcn_readlane(in, (i0 + b) & 63);
-      nbad[b] = page < 0;  // a bad page: page 0's bytes, whose values never count
-      const uint8_t* head = head0 + (int64_t)max(page, 0) * a.c.page_bytes;
-      const uint8_t* src = head + (int64_t)inner * (2 * RAW);
-      if constexpr (EB == 2) {
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int o = (u * NT + wv * 64) * 16;
-          __builtin_amdgcn_global_load_lds(
-              reinterpret_cast<const __attribute__((address_space(1))) uint32_t*>(reinterpret_cast<uintptr_t>(src + o + 16 * lane)),
-              (__attribute__((address_space(3))) uint32_t*)(&lds[buf][b][o]), 16, 0, 0);
-        }
-      } else {
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u)
-          raw[b][u] = *reinterpret_cast<const u32x4_t*>(src + (u * NT + threadIdx.x) * 16);
-        const float* sc = reinterpret_cast<const float*>(head + (int64_t)per * (2 * RAW)) + 2 * inner;
-        nks[b] = sc[0];
-        nvs[b] = sc[1];
+      for (int u = 0; u < UNITS; ++u) {
+        const int o = (u * NT + wv * 64) * 16;
+        to_lds16(src + o + 16 * lane, &lds[buf][o]);
       }
+    } else {
+#pragma unroll
+      for (int u = 0; u < UNITS; ++u) raw[u] = *reinterpret_cast<const u32x4_t*>(src + (u * NT + threadIdx.x) * 16);
+      const float* sc = reinterpret_cast<const float*>(head + (int64_t)per * (2 * RAW)) + 2 * inner;
+      nks = sc[0];
+      nvs = sc[1];
     }
   };
-  auto put = [&](int i0, int buf) {  // int8: codes to fp16 operands in LDS
+  auto put = [&](int buf) {  // int8: codes to fp16 operands in LDS
     if constexpr (EB == 1) {
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        if (i0 + b >= count) break;
-#pragma unroll
-        for (int u = 0; u < UNITS; ++u) {
-          const int i = u * NT + threadIdx.x, part = i / (RAW / 16), x = i % (RAW / 16);
-          // unit (.., c, inner 16 or 64 places) of codes becomes units (.., 2 c) and (.., 2 c + 1)
-          const int low = part == 0 ? 16 : 64, c = x / low, y = x % low;
-          uint8_t* to = &lds[buf][b][part * PART + (2 * c * low + y) * 16];
-          *reinterpret_cast<f16x8*>(to) = codes8(raw[b][u][0], raw[b][u][1]);
-          *reinterpret_cast<f16x8*>(to + low * 16) = codes8(raw[b][u][2], raw[b][u][3]);
-        }
+      for (int u = 0; u < UNITS; ++u) {
+        const int i = u * NT + threadIdx.x, part = i / (RAW / 16), x = i % (RAW / 16);
+        // unit (.., c, inner 16 or 64 places) of codes becomes units (.., 2 c) and (.., 2 c + 1)
+        const int low = part == 0 ? 16 : 64, c = x / low, y = x % low;
+        uint8_t* to = &lds[buf][part * PART + (2 * c * low + y) * 16];
+        *reinterpret_cast<f16x8*>(to) = codes8(raw[u][0], raw[u][1]);
+        *reinterpret_cast<f16x8*>(to + low * 16) = codes8(raw[u][2], raw[u][3]);
       }
     }
   };
@@ -211,6 +211,43 @@ __global__ __launch_bounds__(64 * WV, NP == 3 ? 1 : 2) void attn_tiled_kernel(At
   // of S^T holds token_of(a, half', b)
   const int koff = 16 * (((col >> 3) & 1) * (32 * KS) + 8 * (col >> 4) + (col & 7) + 16 * half);
   const int voff = PART + 16 * ((col >> 4) * 64 + half * 16 + (col & 15));
+
+  // bf16 blocks of which some row does not see some token: 0 * V there (an infinity or
+  // NaN, or a slot never written) must not reach that row.  Where the block has such
+  // values, rows that see one take it, and it is taken out of the operand.  Rare.
+  auto purify = [&](int buf, int blk) {
+    uint8_t* v = &lds[buf][PART];
+    bool odd = false;
+    for (int i = threadIdx.x; i < PART / 16; i += NT) {
+      const u16x8 u = *reinterpret_cast<const u16x8*>(v + 16 * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) odd |= (u[e] & 0x7f80u) == 0x7f80u;
+    }
+    if (!__syncthreads_or(odd)) return;
+    if (!idle) {
+#pragma unroll 1
+      for (int t = 0; t < kKvBlock; ++t) {
+        const bool see = sees(qp, blk * kKvBlock + t, a.window, a.sinks);
+        const uint8_t* vt = v + 16 * (16 * ((t & 15) >> 2) + 4 * half) + 2 * ((t & 3) + 4 * (t >> 4));
+#pragma unroll
+        for (int d = 0; d < DT; ++d)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int chn = 32 * d + 8 * (r >> 2) + (r & 3);  // + 4 * half
+            const float x = bf16_to_f32(*reinterpret_cast<const uint16_t*>(vt + 16 * ((chn >> 4) * 64 + (chn & 15))));
+            acc[d][r] += see && !(fabsf(x) < __builtin_inff()) ? x : 0.f;
+          }
+      }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < PART / 16; i += NT) {
+      u16x8 u = *reinterpret_cast<const u16x8*>(v + 16 * i);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) u[e] = (u[e] & 0x7f80u) == 0x7f80u ? 0 : u[e];
+      *reinterpret_cast<u16x8*>(v + 16 * i) = u;
+    }
+    __syncthreads();
+  };
 
   // One block against the wave's rows; full: every row sees all of it; bad: its page
   // index or a scale is not usable, rows that see it become NaN.
@@ -237,12 +274,15 @@ __global__ __launch_bounds__(64 * WV, NP == 3 ? 1 : 2) void attn_tiled_kernel(At
         x[e] = !sees(qp, j, a.window, a.sinks) ? kNegInf : bad ? __builtin_nanf("") : x[e];
       }
     }
-    float mx = x[0];
+    float mx = kNegInf;
 #pragma unroll
-    for (int e = 1; e < 16; ++e) mx = fmaxf(mx, x[e]);
+    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
     mx = __builtin_fmaf(half_max(mx), c, lv);
-    if (__any(mx > m)) {
-      const float mn = fmaxf(m, mx), al = decay(m, mn);
+    // the reference of the weights follows the maximum once it is kSlack behind, row by
+    // row, so that a row's bits do not depend on its neighbours'
+    const bool grow = mx > m + kSlack;
+    if (__any(grow)) {
+      const float mn = grow ? mx : m, al = grow ? decay(m, mn) : 1.f;
       m = mn;
       l *= al;
 #pragma unroll
@@ -274,81 +314,35 @@ __global__ __launch_bounds__(64 * WV, NP == 3 ? 1 : 2) void attn_tiled_kernel(At
       for (int p = 0; p < NP; ++p) acc[i >> 1] = Op::mma32(vf[i], pf[i & 1][p], acc[i >> 1]);
   };
 
-  // bf16 tiles of which some row does not see some token: 0 * V there (an infinity or
-  // NaN, or a slot never written) must not reach that row.  Where the tile has such
-  // values, rows that see one take it, and it is taken out of the operand.  Rare.
-  auto purify = [&](int buf, int i0) {
-    constexpr int VU = PART / 16;
-    const int n = min(2, count - i0) * VU;
-    bool odd = false;
-    for (int i = threadIdx.x; i < n; i += NT) {
-      const u16x8 u = *reinterpret_cast<const u16x8*>(&lds[buf][i / VU][PART + 16 * (i % VU)]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) odd |= (u[e] & 0x7f80u) == 0x7f80u;
-    }
-    if (!__syncthreads_or(odd)) return;
-    if (!idle) {
-#pragma unroll 1
-      for (int i = 0; i < 32 * (n / VU); ++i) {
-        const int t = i & 31, j = reach.block(ch.begin + i0 + (i >> 5)) * kKvBlock + t;
-        const bool see = sees(qp, j, a.window, a.sinks);
-        const uint8_t* vt = &lds[buf][i >> 5][PART + 16 * (16 * ((t & 15) >> 2) + 4 * half) + 2 * ((t & 3) + 4 * (t >> 4))];
-#pragma unroll
-        for (int d = 0; d < DT; ++d)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int chn = 32 * d + 8 * (r >> 2) + (r & 3);  // + 4 * half
-            const float v = bf16_to_f32(*reinterpret_cast<const uint16_t*>(vt + 16 * ((chn >> 4) * 64 + (chn & 15))));
-            acc[d][r] += see && !(fabsf(v) < __builtin_inff()) ? v : 0.f;
-          }
-      }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < n; i += NT) {
-      u16x8* at = reinterpret_cast<u16x8*>(&lds[buf][i / VU][PART + 16 * (i % VU)]);
-      u16x8 u = *at;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) u[e] = (u[e] & 0x7f80u) == 0x7f80u ? 0 : u[e];
-      *at = u;
-    }
-    __syncthreads();
-  };
-
+  // the queries are waited for here: the loop must not wait for a load of theirs, with
+  // which it would wait for the copies under way
+  __builtin_amdgcn_s_waitcnt(kVmcnt0);
   look_up(0);
   fetch(0, 0);
-  for (int i0 = 0, buf = 0; i0 < count; i0 += 2, buf ^= 1) {
-    put(i0, buf);
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();  // the tile is in LDS, and every wave has left the other buffer
-    float cks[2], cvs[2];
-    int cbad[2];
-#pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      cks[b] = __uint_as_float(uni(__float_as_uint(nks[b])));
-      cvs[b] = __uint_as_float(uni(__float_as_uint(nvs[b])));
+  for (int i = 0; i < count; ++i) {
+    const int buf = i & 1, blk = reach.block(ch.begin + i);
+    put(buf);
+    __builtin_amdgcn_s_waitcnt(kVmcnt0);
+    asm volatile("" ::: "memory");
+    __syncthreads();  // the block is in LDS, and every wave has left the other buffer
+    float ksc = 1.f, vsc = 1.f;
+    bool bad = nbad;
+    if constexpr (EB == 1) {
+      ksc = __uint_as_float(uni(__float_as_uint(nks)));
+      vsc = __uint_as_float(uni(__float_as_uint(nvs)));
       // a scale that is not finite: its block's values are NaN to every row that sees it
-      cbad[b] = nbad[b] || (EB == 1 && !(cks[b] < __builtin_inff() && cvs[b] < __builtin_inff()));
-      if (cbad[b]) cks[b] = cvs[b] = 1.f;
+      bad = bad || !(ksc < __builtin_inff() && vsc < __builtin_inff());
+      if (bad) ksc = vsc = 1.f;
     }
-    if (i0 + 2 < count) {
-      if (((i0 + 2) & 63) == 0) look_up(i0 + 2);
-      fetch(i0 + 2, buf ^ 1);
+    if (i + 1 < count) {
+      if (((i + 1) & 63) == 0) look_up(i + 1);
+      fetch(i + 1, buf ^ 1);
     }
     if constexpr (EB == 2) {
-      bool part = false;
-      for (int b = 0; b < 2 && i0 + b < count; ++b)
-        part |= cbad[b] || !all_seen(tp0, tp1, a.window, a.sinks, reach.block(ch.begin + i0 + b));
-      if (part) purify(buf, i0);
+      if (bad || !all_seen(tp0, tp1, a.window, a.sinks, blk)) purify(buf, blk);
     }
-    if (idle) continue;
-#pragma unroll 1
-    for (int b = 0; b < 2 && i0 + b < count; ++b) {
-      const int blk = reach.block(ch.begin + i0 + b);
-      if (blk * kKvBlock > wp1) continue;  // past every row of the wave
-      const bool bad = b ? cbad[1] : cbad[0];
-      step(&lds[buf][b][0], blk, bad, !bad && all_seen(wp0, wp1, a.window, a.sinks, blk), b ? cks[1] : cks[0],
-           b ? cvs[1] : cvs[0]);
-    }
+    if (idle || blk * kKvBlock > wp1) continue;  // no rows, or past every row of the wave
+    step(&lds[buf][0], blk, bad, !bad && all_seen(wp0, wp1, a.window, a.sinks, blk), ksc, vsc);
   }
 
   const float ll = half_sum(l);
@@ -379,21 +373,16 @@ __global__ __launch_bounds__(64 * WV, NP == 3 ? 1 : 2) void attn_tiled_kernel(At
   }
 }
 
-template <int D, int EB, int NP> static void launch_qt(const AttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.units * a.c.H * a.splits));
-  if (a.tile_rows == 256) {
-    if constexpr (NP == 1 && D * EB >= 128) hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP, 8>), grid, dim3(512), 0, st, a);
-  } else {
-    hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP, 4>), grid, dim3(256), 0, st, a);
-  }
+template <int D, int EB, int NP> static void launch_t(const AttnArgs& a, hipStream_t st) {
+  hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP>), dim3((unsigned)(a.units * a.c.H * a.splits)), dim3(256), 0, st, a);
 }
 template <int D> static void launch_d(bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st) {
   if (int8) {
-    if (in_bf16) launch_qt<D, 1, 1>(a, st);
-    else launch_qt<D, 1, AttnOp<1>::kParts>(a, st);
+    if (in_bf16) launch_t<D, 1, 1>(a, st);
+    else launch_t<D, 1, AttnOp<1>::kParts>(a, st);
   } else {
-    if (in_bf16) launch_qt<D, 2, 1>(a, st);
-    else launch_qt<D, 2, AttnOp<2>::kParts>(a, st);
+    if (in_bf16) launch_t<D, 2, 1>(a, st);
+    else launch_t<D, 2, AttnOp<2>::kParts>(a, st);
   }
 }
 hipError_t launch_attn_tiled(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st) {

@@ -87,6 +87,7 @@ struct AttnArgs {
 };
 static_assert(sizeof(AttnArgs) <= 4096, "kernel argument budget");
 
+constexpr int kTileRows = 128;   // rows of a tile of the tiled kernel
 constexpr int kDecodeRows = 32;  // rows per request and key/value head the decode kernel takes
 
 hipError_t launch_attn_decode(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);

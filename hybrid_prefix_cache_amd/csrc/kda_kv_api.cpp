@@ -20,7 +20,6 @@ using namespace kda;
 namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // positions, rows, table capacity
-constexpr int64_t kFullCard = 256;      // workgroups that give every CU one
 constexpr int64_t kDecodeTarget = 2048;  // workgroups a decode step is split into, at least
 constexpr int64_t kTiledTarget = 512;    // the same for tiles
 
@@ -310,7 +309,7 @@ AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens
   const int64_t rows = (int64_t)tokens * (Hq / p->num_heads);
   AttnPlan pl;
   pl.decode = rows <= kDecodeRows;
-  pl.tile_rows = pl.decode ? kDecodeRows : 128;
+  pl.tile_rows = pl.decode ? kDecodeRows : kTileRows;
   pl.units = (int64_t)n * ((rows + pl.tile_rows - 1) / pl.tile_rows);
   plan_splits(&pl, p, Hq, (int64_t)n * tokens,
               reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks),
@@ -318,24 +317,18 @@ AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens
   return pl;
 }
 
-// Packed rows: 256-row tiles where they fill the card, 128-row ones otherwise
-// (and for fp32 queries, whose operand parts take the registers, and int8 blocks
-// of 64 channels, which have no 16-byte unit for every thread of the larger tile).
 AttnPlan plan_prefill(const kda_kv_pool* p, int32_t Hq, int32_t n, const int64_t* cu, const int64_t* start,
-                      int32_t window, int32_t sinks, kda_dtype in) {
+                      int32_t window, int32_t sinks) {
   const int64_t G = Hq / p->num_heads;
   AttnPlan pl;
   pl.decode = false;
+  pl.tile_rows = kTileRows;
+  pl.units = 0;
   int64_t blocks = 1;
-  const bool wide = in == KDA_BF16 && p->head_dim * (p->dtype == KDA_INT8 ? 1 : 2) >= 128;
-  for (pl.tile_rows = wide ? 256 : 128;; pl.tile_rows = 128) {
-    pl.units = 0;
-    for (int32_t i = 0; i < n; ++i) {
-      const int64_t len = cu[i + 1] - cu[i], s = start ? start[i] : 0;
-      pl.units += (len * G + pl.tile_rows - 1) / pl.tile_rows;
-      blocks = std::max(blocks, reach_blocks(s + len, std::min<int64_t>(len, pl.tile_rows), window, sinks));
-    }
-    if (pl.tile_rows == 128 || pl.units * p->num_heads >= kFullCard) break;
+  for (int32_t i = 0; i < n; ++i) {
+    const int64_t len = cu[i + 1] - cu[i], s = start ? start[i] : 0;
+    pl.units += (len * G + kTileRows - 1) / kTileRows;
+    blocks = std::max(blocks, reach_blocks(s + len, std::min<int64_t>(len, kTileRows), window, sinks));
   }
   plan_splits(&pl, p, Hq, cu[n], blocks, kTiledTarget);
   return pl;
@@ -538,11 +531,8 @@ size_t kda_attn_prefill_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_h
     if (cu_seqlens[i + 1] < cu_seqlens[i] || cu_seqlens[i + 1] > kMaxTokens ||
         (start_pos && (start_pos[i] < 0 || start_pos[i] > kMaxTokens)))
       return 0;
-  // either input type fits
-  size_t bytes = 256;
-  for (kda_dtype in : {(kda_dtype)KDA_BF16, (kda_dtype)KDA_F32})
-    bytes = std::max(bytes, plan_prefill(pool, num_q_heads, num_seqs, cu_seqlens, start_pos, window, sinks, in).bytes);
-  return seq_table_bytes(num_seqs) + bytes;
+  const AttnPlan pl = plan_prefill(pool, num_q_heads, num_seqs, cu_seqlens, start_pos, window, sinks);
+  return seq_table_bytes(num_seqs) + std::max<size_t>(256, pl.bytes);
 }
 
 kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld, void* o,
@@ -563,7 +553,7 @@ kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in
     if (s != KDA_OK || rows == 0) return s == KDA_OK ? ok() : s;
     s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
     if (s != KDA_OK) return s;
-    const AttnPlan pl = plan_prefill(pool, num_q_heads, num_seqs, cu_seqlens, start_pos, window, sinks, in_dtype);
+    const AttnPlan pl = plan_prefill(pool, num_q_heads, num_seqs, cu_seqlens, start_pos, window, sinks);
     if (pl.units * pool->num_heads * pl.splits > kMaxTokens || rows * num_q_heads > kMaxTokens)
       return fail(KDA_ERR_SHAPE, "too much work for one call");
     const size_t table_bytes = seq_table_bytes(num_seqs);
