@@ -182,7 +182,6 @@ def _dptr(x):
 
 
 def _dtype_code(t):
-    import torch
     if t.dtype == torch.bfloat16:
         return KDA_BF16
     if t.dtype == torch.float32:
@@ -452,53 +451,61 @@ def make_rope(cos, sin, *, interleaved: bool = False):
     return kda_rope(_dptr(cos), _dptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(interleaved)))
 
 
-def _rows(name, x, heads, d, rows=None, dtype=None):
-    """(pointer, row distance in elements) of a [T, heads, d] tensor on the current device whose
-    rows are contiguous (they may be columns of a wider tensor)."""
-    if not x.is_cuda or x.device.index != torch.cuda.current_device():
+def _rows(name, x, rows, heads, d, dtype, dev):
+    """(pointer, row distance in elements) of a [rows, heads, d] tensor of device `dev` whose rows
+    are contiguous (they may be columns of a wider tensor)."""
+    if x.get_device() != dev:
         raise ValueError(f"{name} must be a tensor of the current device")
-    if x.dim() != 3 or x.shape[1] != heads or x.shape[2] != d or (rows is not None and x.shape[0] != rows):
-        raise ValueError(f"{name} must be [{'T' if rows is None else rows}, {heads}, {d}] (got {tuple(x.shape)})")
+    if x.shape != (rows, heads, d):
+        raise ValueError(f"{name} must be [{rows}, {heads}, {d}] (got {tuple(x.shape)})")
     if dtype is not None and x.dtype != dtype:
         raise ValueError(f"{name} must be {dtype} (got {x.dtype})")
-    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != d):
+    ld, sh, sd = x.stride()
+    if sd != 1 or (heads > 1 and sh != d):
         raise ValueError(f"{name}: the heads of a row must be contiguous")
-    return x.data_ptr(), x.stride(0) if x.shape[0] > 1 else heads * d
+    return x.data_ptr(), ld if rows > 1 else heads * d
 
 
-def _out(name, x, heads, d, rows):
-    ptr, ld = _rows(name, x, heads, d, rows)
+def _out(name, x, rows, heads, d, dtype, dev):
+    ptr, ld = _rows(name, x, rows, heads, d, dtype, dev)
     if ld != heads * d:
         raise ValueError(f"{name} must be contiguous")
     return ptr
 
 
-def _table(page_table, n):
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != n:
-        raise ValueError(f"page_table must be an int32 device tensor [{n}, max_pages]")
-    if page_table.device.index != torch.cuda.current_device():
-        raise ValueError("page_table must be on the current device")
-    return _dptr(page_table), page_table.shape[1]
+def _ints(name, x, shape, dev):
+    """Pointer of a contiguous int32 tensor of device `dev`; None in `shape` is any size."""
+    if x.dtype != torch.int32 or x.dim() != len(shape) or any(w not in (None, m) for w, m in zip(shape, x.shape)):
+        raise ValueError(f"{name} must be an int32 device tensor of shape {shape} (got {x.dtype}, {tuple(x.shape)})")
+    if x.get_device() != dev or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of the current device")
+    return x.data_ptr()
 
 
-def _pos(pos, n=None):
-    if pos.dtype != torch.int32 or pos.dim() != 1 or (n is not None and pos.shape[0] != n):
-        raise ValueError("pos must be an int32 device tensor [n]")
-    if pos.device.index != torch.cuda.current_device():
-        raise ValueError("pos must be on the current device")
-    return _dptr(pos)
+def _heads(x, d):
+    if x.dim() != 3:
+        raise ValueError(f"expected a [rows, heads, {d}] tensor (got {tuple(x.shape)})")
+    return x.shape[1]
 
 
 def _packed(cu_seqlens, start_pos):
     cu, sp = _HostArr(cu_seqlens, np.int64), _HostArr(start_pos, np.int64)
-    if cu.a.ndim != 1 or len(cu.a) < 1:
+    if cu.a is None or cu.a.ndim != 1 or len(cu.a) < 1:
         raise ValueError("cu_seqlens must hold num_seqs + 1 entries")
     _need_len("start_pos", sp, len(cu.a) - 1)
-    return cu, sp, len(cu.a) - 1
+    return cu.a.ctypes.data, None if sp.a is None else sp.a.ctypes.data, len(cu.a) - 1, int(cu.a[-1]), (cu, sp)
 
 
-def _ws(workspace):
-    return _dptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size()
+def _ws(workspace, dev):
+    if workspace is None:
+        return None, 0
+    if workspace.get_device() != dev:
+        raise ValueError("workspace must be a tensor of the current device")
+    return _dptr(workspace), workspace.numel() * workspace.element_size()
+
+
+def _on(stream, dev):
+    return torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
 
 
 def kda_kv_pool_check(pool: kda_kv_pool) -> int:
@@ -514,19 +521,18 @@ def kda_kv_workspace_bytes(num_seqs: int) -> int:
     return int(_lib.kda_kv_workspace_bytes(num_seqs))
 
 
-def _append_tensors(pool, q, k, v, q_out, rows, rope):
+def _append_tensors(pool, q, k, v, q_out, rows, rope, dev):
     """Arguments shared by the two appends: pointers, row distances, head count."""
-    kp, kl = _rows("k", k, pool.num_heads, pool.head_dim, rows)
-    vp, vl = _rows("v", v, pool.num_heads, pool.head_dim, rows, k.dtype)
+    d, dt = pool.head_dim, k.dtype
+    kp, kl = _rows("k", k, rows, pool.num_heads, d, None, dev)
+    vp, vl = _rows("v", v, rows, pool.num_heads, d, dt, dev)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     qp, ql, op, hq = None, 0, None, 0
     if q is not None:
-        hq = q.shape[1]
-        qp, ql = _rows("q", q, hq, pool.head_dim, rows, k.dtype)
-        op = _out("q_out", q_out, hq, pool.head_dim, rows)
-        if q_out.dtype != k.dtype:
-            raise ValueError("q_out must have the type of q")
+        hq = _heads(q, d)
+        qp, ql = _rows("q", q, rows, hq, d, dt, dev)
+        op = _out("q_out", q_out, rows, hq, d, dt, dev)
     return qp, kp, vp, _dtype_code(k), ql, kl, vl, op, hq, None if rope is None else ctypes.byref(rope)
 
 
@@ -535,42 +541,41 @@ def kda_kv_append(pool, q, k, v, q_out, cu_seqlens, page_table, *, rope=None, st
     """q, q_out: [T, Hq, d] or both None; k, v: [T, H, d] (device tensors; q, k and v may be column
     ranges of one projection); page_table: int32 device tensor [num_seqs, max_pages]; host metadata
     as for kda_prefill_chunked; workspace: kda_kv_workspace_bytes (None up to 128 sequences)."""
-    cu, sp, ns = _packed(cu_seqlens, start_pos)
-    qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, int(cu.a[-1]), rope)
-    tp, mp = _table(page_table, ns)
-    wp, wb = _ws(workspace)
-    _check(_lib.kda_kv_append(ctypes.byref(pool), rp, qp, kp, vp, dt, ql, kl, vl, op, hq, ns, cu.ptr, sp.ptr, tp,
-                              mp, wp, wb, _stream(stream)))
+    dev = torch.cuda.current_device()
+    cu, sp, ns, rows, _keep = _packed(cu_seqlens, start_pos)
+    qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, rows, rope, dev)
+    tp = _ints("page_table", page_table, (ns, None), dev)
+    wp, wb = _ws(workspace, dev)
+    _check(_lib.kda_kv_append(ctypes.byref(pool), rp, qp, kp, vp, dt, ql, kl, vl, op, hq, ns, cu, sp, tp,
+                              page_table.shape[1], wp, wb, _on(stream, dev)))
 
 
 def kda_kv_append_step(pool, q, k, v, q_out, tokens, pos, page_table, *, rope=None, stream=None):
     """`tokens` tokens per request at positions pos[r] + t: tensors as for kda_kv_append with rows
     [n * tokens]; pos: int32 device tensor [n], negative for a request that takes no part."""
-    n = int(pos.numel())
-    qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, n * int(tokens), rope)
-    tp, mp = _table(page_table, n)
-    _check(_lib.kda_kv_append_step(ctypes.byref(pool), rp, qp, kp, vp, dt, ql, kl, vl, op, hq, n, int(tokens),
-                                   _pos(pos), tp, mp, _stream(stream)))
+    dev, n = torch.cuda.current_device(), pos.numel()
+    qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, n * tokens, rope, dev)
+    tp = _ints("page_table", page_table, (n, None), dev)
+    _check(_lib.kda_kv_append_step(ctypes.byref(pool), rp, qp, kp, vp, dt, ql, kl, vl, op, hq, n, tokens,
+                                   _ints("pos", pos, (n,), dev), tp, page_table.shape[1], _on(stream, dev)))
 
 
 def kda_kv_read(pool, k_out, v_out, cu_seqlens, page_table, *, start_pos=None, workspace=None, stream=None):
     """Cached rows back at full precision: k_out, v_out [T, H, d] device tensors of one type."""
-    cu, sp, ns = _packed(cu_seqlens, start_pos)
-    rows = int(cu.a[-1])
-    kp, vp = (_out(name, x, pool.num_heads, pool.head_dim, rows) for name, x in (("k_out", k_out), ("v_out", v_out)))
-    if k_out.dtype != v_out.dtype:
-        raise ValueError("k_out and v_out must have one type")
-    tp, mp = _table(page_table, ns)
-    wp, wb = _ws(workspace)
-    _check(_lib.kda_kv_read(ctypes.byref(pool), kp, vp, _dtype_code(k_out), ns, cu.ptr, sp.ptr, tp, mp, wp, wb,
-                            _stream(stream)))
+    dev = torch.cuda.current_device()
+    cu, sp, ns, rows, _keep = _packed(cu_seqlens, start_pos)
+    kp = _out("k_out", k_out, rows, pool.num_heads, pool.head_dim, None, dev)
+    vp = _out("v_out", v_out, rows, pool.num_heads, pool.head_dim, k_out.dtype, dev)
+    tp = _ints("page_table", page_table, (ns, None), dev)
+    wp, wb = _ws(workspace, dev)
+    _check(_lib.kda_kv_read(ctypes.byref(pool), kp, vp, _dtype_code(k_out), ns, cu, sp, tp, page_table.shape[1], wp,
+                            wb, _on(stream, dev)))
 
 
 def kda_attn_prefill_workspace_bytes(pool, num_q_heads: int, cu_seqlens, *, start_pos=None, window: int = 0,
                                      sinks: int = 0) -> int:
-    cu, sp, ns = _packed(cu_seqlens, start_pos)
-    return int(_lib.kda_attn_prefill_workspace_bytes(ctypes.byref(pool), num_q_heads, ns, cu.ptr, sp.ptr, window,
-                                                     sinks))
+    cu, sp, ns, _rows_, _keep = _packed(cu_seqlens, start_pos)
+    return int(_lib.kda_attn_prefill_workspace_bytes(ctypes.byref(pool), num_q_heads, ns, cu, sp, window, sinks))
 
 
 def kda_attn_prefill(pool, q, o, cu_seqlens, page_table, *, scale, start_pos=None, window=0, sinks=0,
@@ -578,14 +583,15 @@ def kda_attn_prefill(pool, q, o, cu_seqlens, page_table, *, scale, start_pos=Non
     """q, o: [T, Hq, d] device tensors (q may be columns of a wider tensor), row i of sequence s at
     position start_pos[s] + i; the cache holds every token up to it.  workspace: uint8 device tensor
     of kda_attn_prefill_workspace_bytes for the same metadata."""
-    cu, sp, ns = _packed(cu_seqlens, start_pos)
-    rows, hq = int(cu.a[-1]), q.shape[1]
-    qp, ql = _rows("q", q, hq, pool.head_dim, rows)
-    op = _out("o", o, hq, pool.head_dim, rows)
-    tp, mp = _table(page_table, ns)
-    wp, wb = _ws(workspace)
+    dev = torch.cuda.current_device()
+    cu, sp, ns, rows, _keep = _packed(cu_seqlens, start_pos)
+    hq = _heads(q, pool.head_dim)
+    qp, ql = _rows("q", q, rows, hq, pool.head_dim, None, dev)
+    op = _out("o", o, rows, hq, pool.head_dim, None, dev)
+    tp = _ints("page_table", page_table, (ns, None), dev)
+    wp, wb = _ws(workspace, dev)
     _check(_lib.kda_attn_prefill(ctypes.byref(pool), qp, _dtype_code(q), ql, op, _dtype_code(o), hq, scale, window,
-                                 sinks, ns, cu.ptr, sp.ptr, tp, mp, wp, wb, _stream(stream)))
+                                 sinks, ns, cu, sp, tp, page_table.shape[1], wp, wb, _on(stream, dev)))
 
 
 def kda_attn_decode_workspace_bytes(pool, num_q_heads: int, n: int, tokens: int, max_pages: int, *,
@@ -597,13 +603,14 @@ def kda_attn_decode_workspace_bytes(pool, num_q_heads: int, n: int, tokens: int,
 def kda_attn_decode(pool, q, o, tokens, pos, page_table, *, scale, window=0, sinks=0, workspace=None, stream=None):
     """`tokens` queries per request: q, o [n * tokens, Hq, d] device tensors, row r*tokens + t at
     position pos[r] + t (pos: int32 device tensor [n], negative for a request that takes no part)."""
-    n, hq = int(pos.numel()), q.shape[1]
-    qp, ql = _rows("q", q, hq, pool.head_dim, n * int(tokens))
-    op = _out("o", o, hq, pool.head_dim, n * int(tokens))
-    tp, mp = _table(page_table, n)
-    wp, wb = _ws(workspace)
+    dev, n, hq = torch.cuda.current_device(), pos.numel(), _heads(q, pool.head_dim)
+    qp, ql = _rows("q", q, n * tokens, hq, pool.head_dim, None, dev)
+    op = _out("o", o, n * tokens, hq, pool.head_dim, None, dev)
+    tp = _ints("page_table", page_table, (n, None), dev)
+    wp, wb = _ws(workspace, dev)
     _check(_lib.kda_attn_decode(ctypes.byref(pool), qp, _dtype_code(q), ql, op, _dtype_code(o), hq, scale, window,
-                                sinks, n, int(tokens), _pos(pos), tp, mp, wp, wb, _stream(stream)))
+                                sinks, n, tokens, _ints("pos", pos, (n,), dev), tp, page_table.shape[1], wp, wb,
+                                _on(stream, dev)))
 
 
 # ---- host prefix index (include/kda_index.h) --------------------------------

@@ -42,8 +42,6 @@ __device__ __forceinline__ f32x16 zero16() {
 
 constexpr int kVmcnt0 = 0x0f70;  // s_waitcnt operand: vmcnt(0), the other counters not waited for
 
-__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
-
 // Each lane's 16 bytes at src to LDS, lane after lane from dst (uniform).  Not the
 // builtin: with it the compiler, which cannot tell the two buffers apart, waits for
 // these loads before the next LDS read; the loop waits for them itself, before the
@@ -81,8 +79,7 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   const int h = blockIdx.x % a.c.H, rest = blockIdx.x / a.c.H;
   const int sp = rest % a.splits, unit = a.units - 1 - rest / a.splits;
   const int req = uni(kv_find_unit(a.b, unit));
-  KvSeq s = kv_seq(a.b, req);
-  s.row = uni(s.row); s.start = uni(s.start); s.len = uni(s.len); s.unit = uni(s.unit);
+  const KvSeq s = kv_seq_uniform(a.b, req);
   const int row0 = (unit - s.unit) * ROWS, rows = s.len * a.G;
   const int64_t cap = (int64_t)a.c.max_pages * a.c.page_tokens;
   const bool off = s.start < 0, over = (int64_t)s.start + s.len > cap;

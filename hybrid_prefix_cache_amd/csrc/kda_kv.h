@@ -54,7 +54,7 @@ struct KvAppendArgs {
   void* q_out;
   int64_t q_ld, k_ld, v_ld;
   int32_t Hq;
-  int32_t kv_wgs;  // workgroups of the key/value part: units * H
+  int32_t kv_wgs;  // workgroups of the key/value part
   int32_t rows;
   KvBatch b;
 };
@@ -93,7 +93,8 @@ constexpr int kDecodeRows = 32;  // rows per request and key/value head the deco
 hipError_t launch_attn_decode(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_tiled(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_join(int D, const AttnArgs& a, hipStream_t st);
-hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, hipStream_t st);
+// one: the one-token step's kernel (b.pos set, b.tokens == 1)
+hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st);
 hipError_t launch_kv_read(int D, bool bf16, bool int8, const KvReadArgs& a, int64_t units, hipStream_t st);
 
 // Blocks of at least this many are one split's share of a cache.
@@ -116,25 +117,30 @@ __device__ __forceinline__ KvSeq kv_seq(const KvBatch& b, int i) {
   if (b.pos) return KvSeq{i * b.tokens, b.pos[i], b.tokens, i * b.units_per};
   return b.tab ? b.tab[i] : b.inl[i];
 }
-// The sequence that owns a work unit / a row: the last one that begins at or
-// before it (empty sequences begin where the next one does).
-__device__ __forceinline__ int kv_find_unit(const KvBatch& b, int unit) {
-  if (b.pos) return unit / b.units_per;
-  int lo = 0, hi = b.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((b.tab ? b.tab[mid].unit : b.inl[mid].unit) <= unit) lo = mid; else hi = mid - 1;
+// The sequence that owns a work unit / a row (uniform over the wave): the last
+// one that begins at or before it (empty sequences begin where the next one
+// does).  The whole wave looks, 64 entries at a time: a few independent loads
+// instead of a chain of dependent ones.
+template <int32_t KvSeq::*FIELD> __device__ __forceinline__ int kv_find(const KvBatch& b, int x) {
+  int found = 0;
+  for (int i0 = 0; i0 < b.n; i0 += 64) {
+    const int i = i0 + (threadIdx.x & 63);
+    const bool before = i < b.n && (b.tab ? b.tab[i].*FIELD : b.inl[i].*FIELD) <= x;
+    found += __popcll(__ballot(before));
   }
-  return lo;
+  return found - 1;
+}
+__device__ __forceinline__ int kv_find_unit(const KvBatch& b, int unit) {
+  return b.pos ? unit / b.units_per : b.n == 1 ? 0 : kv_find<&KvSeq::unit>(b, unit);
 }
 __device__ __forceinline__ int kv_find_row(const KvBatch& b, int row) {
-  if (b.pos) return row / b.tokens;
-  int lo = 0, hi = b.n - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if ((b.tab ? b.tab[mid].row : b.inl[mid].row) <= row) lo = mid; else hi = mid - 1;
-  }
-  return lo;
+  return b.pos ? row / b.tokens : b.n == 1 ? 0 : kv_find<&KvSeq::row>(b, row);
+}
+__device__ __forceinline__ int uni(int x) { return __builtin_amdgcn_readfirstlane(x); }
+// The same, with the sequence itself in scalar registers.
+__device__ __forceinline__ KvSeq kv_seq_uniform(const KvBatch& b, int i) {
+  const KvSeq s = kv_seq(b, i);
+  return KvSeq{uni(s.row), uni(s.start), uni(s.len), uni(s.unit)};
 }
 
 // First byte of a request's 32-token block `blk` of head h, or NULL where its

@@ -1,12 +1,14 @@
 // kda_kv.hip -- the paged key/value cache: append with rotation, and read-back
 // (gfx950).  Formulas, block layout and the int8 rule: include/kda.h.
 //
-// append: one workgroup owns one 32-token block of one head (so the block's
-// scale, its codes and a requantisation need no other workgroup), further
-// workgroups of the same launch rotate q, one token row each.  The rotation
-// runs in 64 bits (products of 32-bit operands are exact there), so the fp32
-// value that is quantised has one rounding whatever the instruction order, and
-// codes are a fixed function of the inputs.
+// append: one workgroup owns the K or the V part of one block of one head (so its
+// scale, its codes and a requantisation need no other workgroup), its keys or
+// its values; further workgroups of the same launch rotate q, a row a wave.  The
+// rotation runs in 64 bits (products of 32-bit operands are exact there), so the
+// fp32 value that is quantised has one rounding whatever the instruction order,
+// and codes are a fixed function of the inputs.  Bound by memory: values stay in
+// registers between the load, the block's maximum and the code; codes (not
+// values) cross LDS into the block's element order, 16 bytes a thread from there.
 #include "kda_device.h"
 #include "kda_kv.h"
 
@@ -37,32 +39,55 @@ __device__ __forceinline__ float turn(float x, float c, float y, float s) {  // 
   return (float)((double)x * (double)c + (double)y * (double)s);
 }
 
-// Channels [8 c, 8 c + 8) of the row at p, rotated for position pos.
-template <typename In>
-__device__ __forceinline__ void rotated8(const KvAppendArgs& a, const In* p, int c, int64_t pos, float* x) {
-  load8(p + 8 * c, x);
-  if (!a.cos || 8 * c >= a.rot) return;
-  const int half = a.rot >> 1;
-  const float* co = a.cos + pos * half;
-  const float* si = a.sin + pos * half;
-  if (a.interleaved) {
-    const f32x4 cv = *reinterpret_cast<const f32x4*>(co + 4 * c), sv = *reinterpret_cast<const f32x4*>(si + 4 * c);
+// A row is handled in D / 16 slots of two 8-channel chunks that rotate together:
+// slot i < rot / 16 holds the pairs [8 i, 8 i + 8) of the rotation, a slot past
+// them two chunks that are copied.
+struct Slot {
+  int a, b;  // its chunks
+  bool turns;
+};
+__device__ __forceinline__ Slot slot_of(const KvAppendArgs& p, int i) {
+  const int turning = p.cos ? p.rot >> 4 : 0;
+  if (i < turning && !p.interleaved) return Slot{i, i + turning, true};
+  return Slot{2 * i, 2 * i + 1, i < turning};
+}
+// The slot's chunks rotated by its eight pairs, one pair after the other: all at
+// once would hold every value in 64 bits, and cost half the waves of a CU.
+__device__ __forceinline__ void rotate_slot(bool interleaved, const float* co, const float* si, float* x, float* y) {
+  float u[8], w[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float u = x[2 * i], w = x[2 * i + 1];
-      x[2 * i] = turn(u, cv[i], w, -sv[i]);
-      x[2 * i + 1] = turn(w, cv[i], u, sv[i]);
-    }
-  } else {
-    const bool low = 8 * c < half;
-    const int i0 = low ? 8 * c : 8 * c - half;
-    float y[8], cv[8], sv[8];
-    load8(p + (low ? 8 * c + half : 8 * c - half), y);
-    load8(co + i0, cv);
-    load8(si + i0, sv);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = turn(x[i], cv[i], y[i], low ? -sv[i] : sv[i]);
+  for (int i = 0; i < 8; ++i) {
+    u[i] = !interleaved ? x[i] : i < 4 ? x[2 * i] : y[2 * i - 8];
+    w[i] = !interleaved ? y[i] : i < 4 ? x[2 * i + 1] : y[2 * i - 7];
   }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    __builtin_amdgcn_sched_barrier(0);
+    const float r = turn(u[i], co[i], w[i], -si[i]);
+    w[i] = turn(w[i], co[i], u[i], si[i]);
+    u[i] = r;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    x[i] = !interleaved ? u[i] : i & 1 ? w[i / 2] : u[i / 2];
+    y[i] = !interleaved ? w[i] : i & 1 ? w[4 + i / 2] : u[4 + i / 2];
+  }
+}
+__device__ __forceinline__ void load4(const uint16_t* p, float* x) {
+  const u16x4 w = *reinterpret_cast<const u16x4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = bf16_to_f32(w[i]);
+}
+__device__ __forceinline__ void load4(const float* p, float* x) {
+  const f32x4 w = *reinterpret_cast<const f32x4*>(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = w[i];
+}
+__device__ __forceinline__ void store4(uint16_t* p, const float* x) {
+  *reinterpret_cast<u16x4*>(p) = pack_bf16x4(x[0], x[1], x[2], x[3]);
+}
+__device__ __forceinline__ void store4(float* p, const float* x) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{x[0], x[1], x[2], x[3]};
 }
 
 // The code of x under scale s; 0 under a scale of 0, and under a non-finite one
@@ -72,178 +97,378 @@ __device__ __forceinline__ int quant(float x, float s) {
   return s > 0.f && s < __builtin_inff() ? (int)r : 0;
 }
 
-template <int D, typename In, int EB> __global__ __launch_bounds__(256) void kv_append_kernel(KvAppendArgs a) {
-  constexpr int NCH = D / 8, LD = D + 4, PART = kKvBlock * D * EB;
-  __shared__ float xs[2][kKvBlock][LD];
-  __shared__ uint32_t top[2][4];
-  const int tid = threadIdx.x;
-  if ((int)blockIdx.x >= a.kv_wgs) {  // one row of q
-    const int row = blockIdx.x - a.kv_wgs;
-    const KvSeq s = kv_seq(a.b, kv_find_row(a.b, row));
-    const int64_t pos = (int64_t)s.start + (row - s.row);
-    const In* q = reinterpret_cast<const In*>(a.q) + row * a.q_ld;
-    In* out = reinterpret_cast<In*>(a.q_out) + (int64_t)row * a.Hq * D;
-    for (int i = tid; i < a.Hq * NCH; i += 256) {
-      float x[8];
-      if (s.start >= 0 && (!a.cos || pos < a.num_pos)) {
-        rotated8(a, q + (i / NCH) * D, i % NCH, pos, x);
-      } else {
+// Four codes.  x * inv (inv = 1 / s) is within 5e-5 of the quotient for any code,
+// so it rounds to the quotient's code unless it is that close to a half.
+__device__ __forceinline__ uint32_t codes_word(const float* x, float s, float inv) {
+  int c[4];
+  bool near = false;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = s.start < 0 ? 0.f : __builtin_nanf("");
-      }
-      store8(out + 8 * i, x);
+  for (int i = 0; i < 4; ++i) {
+    const float r = x[i] * inv, n = rintf(r);
+    near |= !(fabsf(r - n) < 0.49995f);
+    c[i] = (int)n;
+  }
+  if (__any(near)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = quant(x[i], s);
+  }
+  return (uint32_t)(c[0] & 255) | (uint32_t)(c[1] & 255) << 8 | (uint32_t)(c[2] & 255) << 16 | (uint32_t)c[3] << 24;
+}
+__device__ __forceinline__ uint32_t top_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+
+template <int D, int WAVES, typename In> __device__ __forceinline__ void rotate_q(const KvAppendArgs& a, int tid) {
+  constexpr int SL = D / 16, HG = 64 / SL;  // slots of a row; heads a wave holds at a time
+  const int row = uni((blockIdx.x - a.kv_wgs) * WAVES + (tid >> 6));  // a wave each
+  if (row >= a.rows) return;
+  const KvSeq s = kv_seq_uniform(a.b, uni(kv_find_row(a.b, row)));
+  const int64_t pos = (int64_t)s.start + (row - s.row);
+  const int i = tid % SL, hg = (tid / SL) % HG;
+  const Slot sl = slot_of(a, i);
+  const In* q = reinterpret_cast<const In*>(a.q) + row * a.q_ld;
+  In* out = reinterpret_cast<In*>(a.q_out) + (int64_t)row * a.Hq * D;
+  const bool off = s.start < 0, lost = !off && a.cos && pos >= a.num_pos;
+  float co[8], si[8];
+  if (sl.turns && !off && !lost) {
+    load8(a.cos + pos * (a.rot >> 1) + 8 * i, co);
+    load8(a.sin + pos * (a.rot >> 1) + 8 * i, si);
+  }
+#pragma unroll 1
+  for (int h = hg; h < a.Hq; h += HG) {
+    float x[8], y[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) asm volatile("" : "+v"(co[j]), "+v"(si[j]));  // stay 32 bits wide between heads
+    load8(q + h * D + 8 * sl.a, x);
+    load8(q + h * D + 8 * sl.b, y);
+    if (off || lost) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = y[j] = off ? 0.f : __builtin_nanf("");
+    } else if (sl.turns) {
+      rotate_slot(a.interleaved, co, si, x, y);
     }
+    store8(out + h * D + 8 * sl.a, x);
+    store8(out + h * D + 8 * sl.b, y);
+  }
+}
+
+template <int D, typename In, int EB> __global__ __launch_bounds__(2 * D, 8) void kv_append_kernel(KvAppendArgs a) {
+  constexpr int SL = D / 16, PART = kKvBlock * D * EB, NE = 16 / EB, NT = 2 * D;
+  constexpr int NU = PART / 16 / NT;  // 16-byte units of the part a thread moves
+  __shared__ __align__(16) uint8_t blk[PART];
+  __shared__ uint32_t top[NT / 64];
+  const int tid = threadIdx.x;
+  if ((int)blockIdx.x >= a.kv_wgs) {
+    rotate_q<D, NT / 64, In>(a, tid);
     return;
   }
-  const int unit = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H;
-  const int req = kv_find_unit(a.b, unit);
-  const KvSeq s = kv_seq(a.b, req);
+  const int p = blockIdx.x & 1, h = (blockIdx.x >> 1) % a.c.H, unit = (blockIdx.x >> 1) / a.c.H;
+  const int req = uni(kv_find_unit(a.b, unit));
+  const KvSeq s = kv_seq_uniform(a.b, req);
   if (s.start < 0) return;
-  const int blk = s.start / kKvBlock + (unit - s.unit);
+  const int bi = s.start / kKvBlock + (unit - s.unit);
   int64_t hi = min((int64_t)s.start + s.len, (int64_t)a.c.max_pages * a.c.page_tokens);
   if (a.cos) hi = min(hi, a.num_pos);
-  const int64_t p0 = (int64_t)blk * kKvBlock;
+  const int64_t p0 = (int64_t)bi * kKvBlock;
   const int t0 = max(s.start - (int)p0, 0), t1 = (int)min(hi - p0, (int64_t)kKvBlock);
   if (t1 <= t0) return;
   float* scales = nullptr;
-  uint8_t* block = kv_block<D, EB>(a.c, req, blk, h, &scales);
+  uint8_t* block = kv_block<D, EB>(a.c, req, bi, h, &scales);
   if (!block) return;
-  uint32_t mk = 0, mv = 0;  // bits of the largest |x|: a NaN is larger than any number
-  for (int i = tid; i < kKvBlock * NCH; i += 256) {
-    const int t = i / NCH, c = i % NCH;
-    if (t < t0 || t >= t1) continue;
-    const int64_t row = s.row + (p0 + t - s.start);
-    float x[8];
-    rotated8(a, reinterpret_cast<const In*>(a.k) + row * a.k_ld + h * D, c, p0 + t, x);
-    store8(&xs[0][t][8 * c], x);
+  block += p * PART;
+  const bool whole = t0 == 0 && t1 == kKvBlock;
+  const int64_t row0 = s.row + (p0 - s.start);  // row of the block's token 0
+  // what the block holds already is asked for with the new values, not after them
+  u32x4_t was[NU];
+  float so = 0.f, sn = 1.f;
+  if (!whole) {
+    if (EB == 1 ? t0 > 0 || p == 1 : p == 1) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mk = max(mk, __float_as_uint(x[j]) & 0x7fffffffu);
-    load8(reinterpret_cast<const In*>(a.v) + row * a.v_ld + h * D + 8 * c, x);
-    store8(&xs[1][t][8 * c], x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) mv = max(mv, __float_as_uint(x[j]) & 0x7fffffffu);
-  }
-  float sn[2], so[2];
-  bool grown[2];
-  if constexpr (EB == 1) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) {
-      mk = max(mk, (uint32_t)__shfl_xor((int)mk, m));
-      mv = max(mv, (uint32_t)__shfl_xor((int)mv, m));
+      for (int i = 0; i < NU; ++i) was[i] = *reinterpret_cast<const u32x4_t*>(block + 16 * (tid + NT * i));
     }
-    if ((tid & 63) == 0) { top[0][tid >> 6] = mk; top[1][tid >> 6] = mv; }
-    so[0] = t0 ? scales[0] : 0.f;
-    so[1] = t0 ? scales[1] : 0.f;
+    if (EB == 1 && t0) so = scales[p];
+  }
+  // ---- load, maximum, code, and to LDS in the block's order: keys by (token, slot),
+  // values by 4 tokens x 4 channels
+  float x[4][4] = {};
+  const int kt = tid / SL, vt = tid / (D / 4) * 4, vc = tid % (D / 4) * 4;
+  const Slot sl = slot_of(a, tid % SL);
+  const bool kin = p == 0 && kt >= t0 && kt < t1;
+  if (p == 0) {
+    if (kin) {
+      const In* from = reinterpret_cast<const In*>(a.k) + (row0 + kt) * a.k_ld + h * D;
+      load8(from + 8 * sl.a, x[0]);
+      load8(from + 8 * sl.b, x[2]);
+      if (sl.turns) {
+        float co[8], si[8];
+        load8(a.cos + (p0 + kt) * (a.rot >> 1) + 8 * (tid % SL), co);
+        load8(a.sin + (p0 + kt) * (a.rot >> 1) + 8 * (tid % SL), si);
+        rotate_slot(a.interleaved, co, si, x[0], x[2]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (vt + j >= t0 && vt + j < t1)
+        load4(reinterpret_cast<const In*>(a.v) + (row0 + vt + j) * a.v_ld + h * D + vc, x[j]);
+  }
+  bool grown = false;
+  float inv = 1.f;
+  if constexpr (EB == 1) {
+    uint32_t m = 0;  // bits of the largest |x|: a NaN is larger than any number
+#pragma unroll
+    for (int j = 0; j < 16; ++j) m = max(m, top_bits(x[j >> 2][j & 3]));
+#pragma unroll
+    for (int i = 1; i < 64; i <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, i));
+    if ((tid & 63) == 0) top[tid >> 6] = m;
+    __syncthreads();
+    m = top[0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; ++i) m = max(m, top[i]);
+    const uint32_t nb = __float_as_uint(__uint_as_float(m) / 127.f), ob = __float_as_uint(so);
+    grown = t0 && nb > ob;
+    sn = __uint_as_float(max(nb, ob));
+    inv = 1.f / sn;
+    if (tid == 0) scales[p] = sn;  // every thread has read the old one before the barrier
+  }
+  if (p == 0) {
+    if (kin) {
+      if constexpr (EB == 1) {
+        *reinterpret_cast<uint2*>(&blk[k_off<D, 1>(kt, 8 * sl.a)]) = uint2{codes_word(x[0], sn, inv), codes_word(x[1], sn, inv)};
+        *reinterpret_cast<uint2*>(&blk[k_off<D, 1>(kt, 8 * sl.b)]) = uint2{codes_word(x[2], sn, inv), codes_word(x[3], sn, inv)};
+      } else {
+        store8(reinterpret_cast<uint16_t*>(blk) + k_off<D, 2>(kt, 8 * sl.a), x[0]);
+        store8(reinterpret_cast<uint16_t*>(blk) + k_off<D, 2>(kt, 8 * sl.b), x[2]);
+      }
+    }
+  } else {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const float y[4] = {x[0][c], x[1][c], x[2][c], x[3][c]};
+      if constexpr (EB == 1) *reinterpret_cast<uint32_t*>(&blk[v_off<D, 1>(vt, vc + c)]) = codes_word(y, sn, inv);
+      else store4(reinterpret_cast<uint16_t*>(blk) + v_off<D, 2>(vt, vc + c), y);
+    }
   }
   __syncthreads();
-  if constexpr (EB == 1) {
+  // ---- 16 bytes at a time to the cache; what the call does not bring stays, or is
+  // re-coded where the scale has grown
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const uint32_t m = max(max(top[p][0], top[p][1]), max(top[p][2], top[p][3]));
-      const uint32_t nb = __float_as_uint(__uint_as_float(m) / 127.f), ob = __float_as_uint(so[p]);
-      grown[p] = t0 && nb > ob;
-      sn[p] = __uint_as_float(max(nb, ob));
-    }
-    if (tid < 2) scales[tid] = sn[tid];  // every thread has read the old pair before the barrier
-  }
-  // one 16-byte unit of the block at a time: first the K part's, then the V part's
-  constexpr int NU = 2 * D * EB;  // units of a part: 32 D EB / 16
-  for (int i = tid; i < 2 * NU; i += 256) {
-    const int p = i / NU, u = i % NU;
-    uint8_t* at = block + p * PART + 16 * u;
-    constexpr int NE = 16 / EB;
-    auto token = [&](int e) {
-      if (p == 0) return (u / (D * EB)) * 16 + u % 16;
-      return ((u / 16) % 4) * 4 + (e & 3) + 16 * ((e & 7) >> 2);
-    };
-    auto chan = [&](int e) {
-      if (p == 0) return (u % (D * EB)) / 16 * NE + e;
-      return (u / 64) * (2 * NE) + (e >> 3) * 16 + u % 16;
-    };
-    bool any = false, all = true;
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const int t = token(e);
-      const bool w = (t >= t0 && t < t1) || (EB == 1 && t < t0 && grown[p]);
-      any |= w;
-      all &= w && t >= t0;
-    }
-    if (!any) continue;
-    if constexpr (EB == 1) {
-      u32x4_t w = {0, 0, 0, 0};
-      if (!all) w = *reinterpret_cast<const u32x4_t*>(at);
+  for (int i = 0; i < NU; ++i) {
+    const int u = tid + NT * i;
+    uint8_t* at = block + 16 * u;
+    u32x4_t w = *reinterpret_cast<const u32x4_t*>(&blk[16 * u]);
+    if (!whole) {
+      // tokens of the unit: one (keys), or 4 g .. and 16 + 4 g .. (values)
+      const int first = p == 0 ? u / (D * EB) * 16 + u % 16 : u / 16 % 4 * 4;
+      bool some = false;
 #pragma unroll
       for (int e = 0; e < NE; ++e) {
-        const int t = token(e);
-        const uint32_t old = (w[e / 4] >> (8 * (e % 4))) & 255u;
-        uint32_t code = old;
-        if (t >= t0 && t < t1) code = (uint32_t)quant(xs[p][t][chan(e)], sn[p]) & 255u;
-        else if (t < t0 && grown[p]) code = (uint32_t)quant((float)(int8_t)old * so[p], sn[p]) & 255u;
-        w[e / 4] = (w[e / 4] & ~(255u << (8 * (e % 4)))) | (code << (8 * (e % 4)));
+        const int t = p == 0 ? first : first + (e & 3) + 16 * ((e & 7) >> 2);
+        const bool fresh = t >= t0 && t < t1, recode = EB == 1 && t < t0 && grown;
+        some |= fresh || recode;
+        if (fresh) continue;
+        if constexpr (EB == 1) {
+          uint32_t c = (was[i][e / 4] >> (8 * (e % 4))) & 255u;
+          if (recode) c = (uint32_t)quant((float)(int8_t)c * so, sn) & 255u;
+          w[e / 4] = (w[e / 4] & ~(255u << (8 * (e % 4)))) | c << (8 * (e % 4));
+        } else {
+          const uint32_t keep = 0xffffu << (16 * (e % 2));
+          w[e / 2] = (w[e / 2] & ~keep) | (was[i][e / 2] & keep);
+        }
       }
-      *reinterpret_cast<u32x4_t*>(at) = w;
-    } else {
-      u16x8 w = {0, 0, 0, 0, 0, 0, 0, 0};
-      if (!all) w = *reinterpret_cast<const u16x8*>(at);
-#pragma unroll
-      for (int e = 0; e < NE; ++e) {
-        const int t = token(e);
-        if (t >= t0 && t < t1) w[e] = f32_to_bf16(xs[p][t][chan(e)]);
-      }
-      *reinterpret_cast<u16x8*>(at) = w;
+      if (!some) continue;
     }
+    *reinterpret_cast<u32x4_t*>(at) = w;
   }
 }
 
-// read-back: one workgroup per 32-token block and head.
+// One token a request (a decode step): nothing of the block has to be gathered, so
+// a workgroup takes a request and HP = 1024 / D of its heads, keys in its first
+// wave and values in all four.  A head's maximum is a lane reduction; codes go to
+// their places as they are (8 bytes of K, single elements of V).  Where a scale
+// grows, a wave re-codes the part first.  With the block kernel's two workgroups a
+// head, 256 requests x 8 heads spent 17 us in 4096 nearly empty workgroups.
+template <int D> __device__ __forceinline__ void recode_part(uint8_t* part, int t0, float so, float sn, bool values, int lane) {
+#pragma unroll 2
+  for (int u = lane; u < 2 * D; u += 64) {
+    const int first = values ? u / 16 % 4 * 4 : u / D * 16 + u % 16;
+    if (first >= t0) continue;
+    u32x4_t* at = reinterpret_cast<u32x4_t*>(part + 16 * u);
+    u32x4_t w = *at;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const int t = values ? first + (e & 3) + 16 * ((e & 7) >> 2) : first;
+      if (t >= t0) continue;
+      const uint32_t c = (uint32_t)quant((float)(int8_t)(w[e / 4] >> (8 * (e % 4))) * so, sn) & 255u;
+      w[e / 4] = (w[e / 4] & ~(255u << (8 * (e % 4)))) | c << (8 * (e % 4));
+    }
+    *at = w;
+  }
+}
+
+template <int D, typename In, int EB> __global__ __launch_bounds__(256) void kv_append_one_kernel(KvAppendArgs a) {
+  constexpr int SL = D / 16, HP = 1024 / D, PART = kKvBlock * D * EB;
+  const int tid = threadIdx.x, lane = tid & 63;
+  if ((int)blockIdx.x >= a.kv_wgs) {
+    rotate_q<D, 4, In>(a, tid);
+    return;
+  }
+  const int passes = (a.c.H + HP - 1) / HP, req = blockIdx.x / passes, h0 = blockIdx.x % passes * HP;
+  const int pos = uni(a.b.pos[req]);
+  if (pos < 0 || pos >= (int64_t)a.c.max_pages * a.c.page_tokens || (a.cos && pos >= a.num_pos)) return;
+  const int kh = h0 + lane / SL, vh = h0 + tid / (D / 4), vc = tid % (D / 4) * 4, t = pos % kKvBlock;
+  const bool kin = tid < 64 && kh < a.c.H, vin = vh < a.c.H;
+  const Slot sl = slot_of(a, lane % SL);
+  float ka[8] = {}, kb[8] = {}, x[4] = {};
+  if (vin) load4(reinterpret_cast<const In*>(a.v) + req * a.v_ld + vh * D + vc, x);
+  if (kin) {
+    const In* from = reinterpret_cast<const In*>(a.k) + req * a.k_ld + kh * D;
+    load8(from + 8 * sl.a, ka);
+    load8(from + 8 * sl.b, kb);
+    if (sl.turns) {
+      float co[8], si[8];
+      load8(a.cos + (int64_t)pos * (a.rot >> 1) + 8 * (lane % SL), co);
+      load8(a.sin + (int64_t)pos * (a.rot >> 1) + 8 * (lane % SL), si);
+      rotate_slot(a.interleaved, co, si, ka, kb);
+    }
+  }
+  float* scales0 = nullptr;
+  uint8_t* block0 = kv_block<D, EB>(a.c, req, pos / kKvBlock, 0, &scales0);
+  if (!block0) return;
+  // part p of head `head` (-1: the lane has none) from the lane's largest value
+  auto code = [&](int p, int head, float top, int lanes) -> float {
+    float* sc = scales0 + p + (int64_t)max(head, 0) * (a.c.head_bytes / 4);
+    const float so = head >= 0 && t ? *sc : 0.f;
+    uint32_t m = top_bits(top);  // bits: a NaN is larger than any number
+    for (int i = 1; i < lanes; i <<= 1) m = max(m, (uint32_t)__shfl_xor((int)m, i));
+    const uint32_t nb = __float_as_uint(__uint_as_float(m) / 127.f), ob = __float_as_uint(so);
+    const float sn = __uint_as_float(max(nb, ob));
+    uint64_t grown = __ballot(head >= 0 && t && nb > ob && lane % lanes == 0);
+    const bool some = grown != 0;
+    for (; grown; grown &= grown - 1) {  // head by head, the whole wave
+      const int from = __builtin_ctzll(grown), g = __builtin_amdgcn_readlane(head, from);
+      recode_part<D>(block0 + g * a.c.head_bytes + p * PART, t, __uint_as_float(__builtin_amdgcn_readlane(ob, from)),
+                     __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(sn), from)), p == 1, lane);
+    }
+    if (some) __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): the re-coded units are written before the new codes
+    if (head >= 0 && lane % lanes == 0) *sc = sn;
+    return sn;
+  };
+  if (tid < 64) {
+    float sn = 1.f;
+    if constexpr (EB == 1) {
+      uint32_t m = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m = max(m, max(top_bits(ka[j]), top_bits(kb[j])));
+      sn = code(0, kin ? kh : -1, __uint_as_float(m), SL);
+    }
+    if (kin) {
+      uint8_t* part = block0 + kh * a.c.head_bytes;
+      if constexpr (EB == 1) {
+        const float inv = 1.f / sn;
+        *reinterpret_cast<uint2*>(part + k_off<D, 1>(t, 8 * sl.a)) = uint2{codes_word(ka, sn, inv), codes_word(ka + 4, sn, inv)};
+        *reinterpret_cast<uint2*>(part + k_off<D, 1>(t, 8 * sl.b)) = uint2{codes_word(kb, sn, inv), codes_word(kb + 4, sn, inv)};
+      } else {
+        store8(reinterpret_cast<uint16_t*>(part) + k_off<D, 2>(t, 8 * sl.a), ka);
+        store8(reinterpret_cast<uint16_t*>(part) + k_off<D, 2>(t, 8 * sl.b), kb);
+      }
+    }
+  }
+  float sn = 1.f;
+  if constexpr (EB == 1) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) m = max(m, top_bits(x[j]));
+    sn = code(1, vin ? vh : -1, __uint_as_float(m), D / 4);
+  }
+  if (!vin) return;
+  uint8_t* part = block0 + vh * a.c.head_bytes + PART;
+  if constexpr (EB == 1) {
+    const uint32_t w = codes_word(x, sn, 1.f / sn);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) part[v_off<D, 1>(t, vc + j)] = (uint8_t)(w >> (8 * j));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) reinterpret_cast<uint16_t*>(part)[v_off<D, 2>(t, vc + j)] = f32_to_bf16(x[j]);
+  }
+}
+
+// read-back: one workgroup per 32-token block and head; the block crosses LDS as
+// it is and leaves it as rows.
 template <int D, typename Out, int EB> __global__ __launch_bounds__(256) void kv_read_kernel(KvReadArgs a) {
-  constexpr int NCH = D / 8, LD = D + 4, PART = kKvBlock * D * EB, NU = 2 * D * EB, NE = 16 / EB;
-  __shared__ float xs[2][kKvBlock][LD];
+  constexpr int PART = kKvBlock * D * EB, NU = PART / 16;
+  __shared__ __align__(16) uint8_t raw[2 * PART];
   const int tid = threadIdx.x, unit = blockIdx.x / a.c.H, h = blockIdx.x % a.c.H;
-  const int req = kv_find_unit(a.b, unit);
-  const KvSeq s = kv_seq(a.b, req);
-  const int blk = s.start / kKvBlock + (unit - s.unit), p0 = blk * kKvBlock;
+  const int req = uni(kv_find_unit(a.b, unit));
+  const KvSeq s = kv_seq_uniform(a.b, req);
+  const int bi = s.start / kKvBlock + (unit - s.unit), p0 = bi * kKvBlock;
   const int t0 = max(s.start - p0, 0), t1 = min(s.start + s.len - p0, kKvBlock);
   if (t1 <= t0) return;
   float* scales = nullptr;
-  const uint8_t* block = kv_block<D, EB>(a.c, req, blk, h, &scales);
-  float sc[2] = {1.f, 1.f};
-  if (EB == 1 && block) { sc[0] = scales[0]; sc[1] = scales[1]; }
-  for (int i = tid; i < 2 * NU; i += 256) {
-    const int p = i / NU, u = i % NU;
-    uint8_t raw[16];
-    if (block) *reinterpret_cast<u32x4_t*>(raw) = *reinterpret_cast<const u32x4_t*>(block + p * PART + 16 * u);
-#pragma unroll
-    for (int e = 0; e < NE; ++e) {
-      const int t = p == 0 ? (u / (D * EB)) * 16 + u % 16 : ((u / 16) % 4) * 4 + (e & 3) + 16 * ((e & 7) >> 2);
-      const int ch = p == 0 ? (u % (D * EB)) / 16 * NE + e : (u / 64) * (2 * NE) + (e >> 3) * 16 + u % 16;
-      float x;
-      if (!block) x = __builtin_nanf("");
-      else if constexpr (EB == 1) x = (float)(int8_t)raw[e] * sc[p];
-      else x = bf16_to_f32((uint16_t)(raw[2 * e] | (raw[2 * e + 1] << 8)));
-      xs[p][t][ch] = x;
-    }
-  }
+  const uint8_t* block = kv_block<D, EB>(a.c, req, bi, h, &scales);
+  float ks = block ? 1.f : __builtin_nanf(""), vs = ks;
+  if (EB == 1 && block) { ks = scales[0]; vs = scales[1]; }
+  if (block)
+    for (int i = tid; i < 2 * NU; i += 256)
+      *reinterpret_cast<u32x4_t*>(&raw[16 * i]) = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(block + 16 * i));
   __syncthreads();
-  for (int i = tid; i < 2 * kKvBlock * NCH; i += 256) {
-    const int p = i / (kKvBlock * NCH), t = i / NCH % kKvBlock, c = i % NCH;
+  const int64_t row0 = s.row + (p0 - s.start);
+  for (int i = tid; i < kKvBlock * D / 8; i += 256) {  // keys: (token, 8 channels)
+    const int t = i / (D / 8), c = i % (D / 8) * 8;
     if (t < t0 || t >= t1) continue;
-    Out* out = reinterpret_cast<Out*>(p == 0 ? a.k_out : a.v_out);
-    store8(out + ((int64_t)(s.row + p0 + t - s.start) * a.c.H + h) * D + 8 * c, &xs[p][t][8 * c]);
+    float x[8];
+    if constexpr (EB == 1) {
+      const uint2 w = *reinterpret_cast<const uint2*>(&raw[k_off<D, 1>(t, c)]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = (float)(int8_t)((e < 4 ? w.x : w.y) >> (8 * (e & 3))) * ks;
+    } else {
+      load8(reinterpret_cast<const uint16_t*>(raw) + k_off<D, 2>(t, c), x);
+    }
+    if (!block) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = ks;
+    }
+    store8(reinterpret_cast<Out*>(a.k_out) + ((row0 + t) * a.c.H + h) * D + c, x);
+  }
+  for (int i = tid; i < kKvBlock / 4 * D / 4; i += 256) {  // values: 4 tokens x 4 channels
+    const int t = i / (D / 4) * 4, c = i % (D / 4) * 4;
+    if (t + 3 < t0 || t >= t1) continue;
+    float x[4][4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float y[4];
+      if constexpr (EB == 1) {
+        const uint32_t w = *reinterpret_cast<const uint32_t*>(&raw[PART + v_off<D, 1>(t, c + k)]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) y[j] = (float)(int8_t)(w >> (8 * j)) * vs;
+      } else {
+        load4(reinterpret_cast<const uint16_t*>(raw + PART) + v_off<D, 2>(t, c + k), y);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[j][k] = block ? y[j] : vs;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (t + j >= t0 && t + j < t1) store4(reinterpret_cast<Out*>(a.v_out) + ((row0 + t + j) * a.c.H + h) * D + c, x[j]);
   }
 }
 
-hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, hipStream_t st) {
-  const dim3 g((unsigned)wgs), b(256);
-#define KDA_APPEND(DD, T, E) hipLaunchKernelGGL((kv_append_kernel<DD, T, E>), g, b, 0, st, a)
-  if (D == 128) {
-    if (bf16) { if (int8) KDA_APPEND(128, uint16_t, 1); else KDA_APPEND(128, uint16_t, 2); }
-    else { if (int8) KDA_APPEND(128, float, 1); else KDA_APPEND(128, float, 2); }
+template <int D, typename In, int EB>
+static void launch_append_t(const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st) {
+  if (one) hipLaunchKernelGGL((kv_append_one_kernel<D, In, EB>), dim3((unsigned)wgs), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((kv_append_kernel<D, In, EB>), dim3((unsigned)wgs), dim3(2 * D), 0, st, a);
+}
+template <int D>
+static void launch_append_d(bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st) {
+  if (bf16) {
+    if (int8) launch_append_t<D, uint16_t, 1>(a, wgs, one, st);
+    else launch_append_t<D, uint16_t, 2>(a, wgs, one, st);
   } else {
-    if (bf16) { if (int8) KDA_APPEND(64, uint16_t, 1); else KDA_APPEND(64, uint16_t, 2); }
-    else { if (int8) KDA_APPEND(64, float, 1); else KDA_APPEND(64, float, 2); }
+    if (int8) launch_append_t<D, float, 1>(a, wgs, one, st);
+    else launch_append_t<D, float, 2>(a, wgs, one, st);
   }
-#undef KDA_APPEND
+}
+hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st) {
+  if (D == 128) launch_append_d<128>(bf16, int8, a, wgs, one, st);
+  else launch_append_d<64>(bf16, int8, a, wgs, one, st);
   return hipGetLastError();
 }
 

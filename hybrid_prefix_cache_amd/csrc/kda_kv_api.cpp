@@ -238,7 +238,7 @@ kda_status check_append_rows(const kda_kv_pool* p, const void* q, const void* k,
 
 KvAppendArgs append_args(const kda_kv_pool* p, const kda_rope* rope, const void* q, const void* k, const void* v,
                          int64_t q_ld, int64_t k_ld, int64_t v_ld, void* q_out, int32_t Hq, const int32_t* table,
-                         int32_t max_pages, int64_t units, int64_t rows) {
+                         int32_t max_pages, int64_t rows) {
   KvAppendArgs a;
   std::memset(&a, 0, sizeof(a));
   a.c = cache_of(p, table, max_pages);
@@ -252,9 +252,20 @@ KvAppendArgs append_args(const kda_kv_pool* p, const kda_rope* rope, const void*
   a.q = q; a.k = k; a.v = v; a.q_out = q_out;
   a.q_ld = q_ld; a.k_ld = k_ld; a.v_ld = v_ld;
   a.Hq = Hq;
-  a.kv_wgs = (int32_t)(units * p->num_heads);
   a.rows = (int32_t)rows;
   return a;
+}
+
+// Launches an append.  One token a request has a kernel of its own; otherwise a
+// workgroup of 2 d threads takes a part (K or V) of a block.  q takes a wave a row.
+kda_status run_append(const kda_kv_pool* p, kda_dtype in, KvAppendArgs* a, int64_t units, hipStream_t st) {
+  const int32_t d = p->head_dim, H = p->num_heads;
+  const bool one = a->b.pos && a->b.tokens == 1;
+  a->kv_wgs = (int32_t)(one ? a->b.n * (((int64_t)H * d + 1023) / 1024) : units * H * 2);
+  const int64_t waves = one ? 4 : 2 * d / 64, wgs = a->kv_wgs + (a->Hq ? (a->rows + waves - 1) / waves : 0);
+  Launch L("kda_kv_append", st);
+  const hipError_t e = launch_kv_append(d, in == KDA_BF16, p->dtype == KDA_INT8, *a, wgs, one, st);
+  return e == hipSuccess ? ok() : hip_fail(e, "append launch");
 }
 
 kda_status check_attn(const kda_kv_pool* p, kda_dtype in, kda_dtype out, int32_t Hq, float scale, int32_t window,
@@ -426,7 +437,7 @@ kda_status kda_kv_append(const kda_kv_pool* pool, const kda_rope* rope, const vo
     if (s != KDA_OK || rows == 0) return s == KDA_OK ? ok() : s;
     s = check_append_rows(pool, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads, rows);
     if (s != KDA_OK) return s;
-    if (units * pool->num_heads + rows > kMaxTokens) return fail(KDA_ERR_SHAPE, "too much work for one call");
+    if (units * pool->num_heads * 2 + rows > kMaxTokens) return fail(KDA_ERR_SHAPE, "too much work for one call");
     s = check_workspace(workspace, workspace_bytes, seq_table_bytes(num_seqs));
     if (s != KDA_OK) return s;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -435,13 +446,10 @@ kda_status kda_kv_append(const kda_kv_pool* pool, const kda_rope* rope, const vo
       if (s != KDA_OK) return s;
     }
     KvAppendArgs a = append_args(pool, rope, q, k, v, q_ld, k_ld, v_ld, q_out, num_q_heads, page_table, max_pages,
-                                 units, rows);
+                                 rows);
     s = ship_seqs(seqs, workspace, &a.b, st);
     if (s != KDA_OK) return s;
-    Launch L("kda_kv_append", st);
-    const hipError_t e = launch_kv_append(pool->head_dim, in_dtype == KDA_BF16, pool->dtype == KDA_INT8, a,
-                                          a.kv_wgs + (num_q_heads ? rows : 0), st);
-    return e == hipSuccess ? ok() : hip_fail(e, "append launch");
+    return run_append(pool, in_dtype, &a, units, st);
   });
 }
 
@@ -460,7 +468,7 @@ kda_status kda_kv_append_step(const kda_kv_pool* pool, const kda_rope* rope, con
     s = check_append_rows(pool, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads, rows);
     if (s != KDA_OK) return s;
     const int per = (tokens + kKvBlock - 2) / kKvBlock + 1;  // blocks `tokens` consecutive tokens can touch
-    if ((int64_t)n * per * pool->num_heads + rows > kMaxTokens) return fail(KDA_ERR_SHAPE, "too much work for one call");
+    if ((int64_t)n * per * pool->num_heads * 2 + rows > kMaxTokens) return fail(KDA_ERR_SHAPE, "too much work for one call");
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (validating()) {
       std::vector<KvSeq> seqs;
@@ -469,12 +477,9 @@ kda_status kda_kv_append_step(const kda_kv_pool* pool, const kda_rope* rope, con
       if (s != KDA_OK) return s;
     }
     KvAppendArgs a = append_args(pool, rope, q, k, v, q_ld, k_ld, v_ld, q_out, num_q_heads, page_table, max_pages,
-                                 (int64_t)n * per, rows);
+                                 rows);
     a.b = step_batch(pos, n, tokens, per);
-    Launch L("kda_kv_append", st);
-    const hipError_t e = launch_kv_append(pool->head_dim, in_dtype == KDA_BF16, pool->dtype == KDA_INT8, a,
-                                          a.kv_wgs + (num_q_heads ? rows : 0), st);
-    return e == hipSuccess ? ok() : hip_fail(e, "append launch");
+    return run_append(pool, in_dtype, &a, (int64_t)n * per, st);
   });
 }
 
