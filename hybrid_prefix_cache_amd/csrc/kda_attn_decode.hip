@@ -97,7 +97,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     return;
   }
   const Reach reach = reach_of(p0, p1, a.window, a.sinks);
-  const Chunk ch = chunk_of(reach.count(), a.splits, sp);
+  const Chunk ch = chunk_of(reach.count(), a.splits, a.min_blocks, sp);
   if (ch.begin >= ch.end) return;
 
   // ---- queries: lane (g, col) holds row col's channels of k-group g
@@ -344,36 +344,56 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   }
 }
 
-// Joins the splits of one (row, query head), of either kernel: one wave each.
-template <int D> __global__ __launch_bounds__(256) void join_kernel(AttnArgs a) {
-  const int lane = threadIdx.x & 63;
-  const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  if (at >= (int64_t)a.rows * a.Hq) return;
+// Joins the splits of one (row, query head), of either kernel: W waves each, the
+// splits shared among them.
+template <int D, int W> __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  constexpr int C = D / 64;
+  __shared__ float sh[4][D + 1];
+  const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6), part = wv % W;
+  const int64_t at = (int64_t)blockIdx.x * (4 / W) + wv / W;
+  if (at >= (int64_t)a.rows * a.Hq) return;  // W = 1, or the whole workgroup
   const int row = (int)(at / a.Hq), g = (int)(at % a.Hq) % a.G;
-  const KvSeq sq = kv_seq(a.b, kv_find_row(a.b, row));
+  const KvSeq sq = kv_seq_uniform(a.b, uni(kv_find_row(a.b, row)));
   if (sq.start < 0 || (int64_t)sq.start + sq.len > (int64_t)a.c.max_pages * a.c.page_tokens) return;
   // the reach of the row's tile, as the attention kernel divided it
   const int t0 = ((row - sq.row) * a.G + g) / a.tile_rows * a.tile_rows, t1 = min(sq.len * a.G, t0 + a.tile_rows);
   const Reach reach = reach_of(sq.start + t0 / a.G, sq.start + (t1 - 1) / a.G, a.window, a.sinks);
-  const int used = chunk_of(reach.count(), a.splits, 0).used;
+  const int used = chunk_of(reach.count(), a.splits, a.min_blocks, 0).used;
   if (used == 1) return;
   const float* ml = a.part_ml + 2 * at * a.splits;
-  const float* po = a.part_o + at * a.splits * D;
+  const float* po = a.part_o + at * a.splits * D + C * lane;
   float mm = kNegInf;
   for (int s = lane; s < used; s += 64) mm = fmaxf(mm, ml[2 * s]);
 #pragma unroll
   for (int x = 1; x < 64; x <<= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
-  float ll = 0.f, y[D / 64] = {};
-  for (int s = 0; s < used; ++s) {
+  float ll = 0.f, y[C] = {};
+#pragma unroll 8
+  for (int s = part; s < used; s += W) {
     const float w = decay(ml[2 * s], mm);
     ll += w * ml[2 * s + 1];
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) y[i] += w * po[(int64_t)s * D + (D / 64) * lane + i];
+    for (int i = 0; i < C; ++i) y[i] += w * po[(int64_t)s * D + i];
+  }
+  if constexpr (W > 1) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) sh[wv][C * lane + i] = y[i];
+    if (lane == 0) sh[wv][D] = ll;
+    __syncthreads();
+    if (part) return;
+    ll = 0.f;
+#pragma unroll
+    for (int i = 0; i < C; ++i) y[i] = 0.f;
+#pragma unroll
+    for (int v = 0; v < W; ++v) {
+      ll += sh[v][D];
+#pragma unroll
+      for (int i = 0; i < C; ++i) y[i] += sh[v][C * lane + i];
+    }
   }
   const float inv = 1.f / ll;
 #pragma unroll
-  for (int i = 0; i < D / 64; ++i) {
-    const int64_t o = at * D + (D / 64) * lane + i;
+  for (int i = 0; i < C; ++i) {
+    const int64_t o = at * D + C * lane + i;
     if (a.out_bf16) reinterpret_cast<uint16_t*>(a.o)[o] = f32_to_bf16(y[i] * inv);
     else reinterpret_cast<float*>(a.o)[o] = y[i] * inv;
   }
@@ -399,9 +419,16 @@ hipError_t launch_attn_decode(int D, bool in_bf16, bool int8, const AttnArgs& a,
   return hipGetLastError();
 }
 hipError_t launch_attn_join(int D, const AttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(((int64_t)a.rows * a.Hq + 3) / 4)), block(256);
-  if (D == 128) hipLaunchKernelGGL((join_kernel<128>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((join_kernel<64>), grid, block, 0, st, a);
+  const int64_t n = (int64_t)a.rows * a.Hq;
+  // a wave reads its splits eight at a time: past two rounds, four waves share them
+  if (a.splits > 16) {
+    if (D == 128) hipLaunchKernelGGL((attn_join_kernel<128, 4>), dim3((unsigned)n), dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((attn_join_kernel<64, 4>), dim3((unsigned)n), dim3(256), 0, st, a);
+  } else {
+    const dim3 grid((unsigned)((n + 3) / 4));
+    if (D == 128) hipLaunchKernelGGL((attn_join_kernel<128, 1>), grid, dim3(256), 0, st, a);
+    else hipLaunchKernelGGL((attn_join_kernel<64, 1>), grid, dim3(256), 0, st, a);
+  }
   return hipGetLastError();
 }
 

@@ -136,14 +136,14 @@ __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {  // 
   return j <= p && (!window || j > p - window || j < sinks);
 }
 
-// How the blocks a request sees are divided among `splits` workgroups: chunks of
-// at least kMinTiles.
+// How the blocks a tile sees are divided among `splits` workgroups: chunks of at
+// least `least` blocks.
 struct Chunk {
   int begin, end, used;
 };
-__device__ __forceinline__ Chunk chunk_of(int tiles, int splits, int s) {
-  const int size = max(kMinTiles, (tiles + splits - 1) / splits);
-  return Chunk{s * size, min(tiles, (s + 1) * size), max(1, (tiles + size - 1) / size)};
+__device__ __forceinline__ Chunk chunk_of(int blocks, int splits, int least, int s) {
+  const int size = max(least, (blocks + splits - 1) / splits);
+  return Chunk{s * size, min(blocks, (s + 1) * size), max(1, (blocks + size - 1) / size)};
 }
 
 }  // namespace kda

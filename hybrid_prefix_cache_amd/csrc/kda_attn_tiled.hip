@@ -96,7 +96,7 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   }
   const int tp0 = s.start + row0 / a.G, tp1 = s.start + (min(rows, row0 + ROWS) - 1) / a.G;
   const Reach reach = reach_of(tp0, tp1, a.window, a.sinks);
-  const Chunk ch = chunk_of(reach.count(), a.splits, sp);
+  const Chunk ch = chunk_of(reach.count(), a.splits, a.min_blocks, sp);
   if (ch.begin >= ch.end) return;
 
   // ---- queries: lane (half, col) holds row col's channels 16 ks + 8 half ..

@@ -81,14 +81,17 @@ struct AttnArgs {
   float scale_log2;
   int32_t window, sinks;
   int32_t rows, units, tile_rows;
-  int32_t splits;  // workgroups that share the blocks a tile sees
+  int32_t splits, min_blocks;  // workgroups that share the blocks a tile sees; a share's least
   int32_t out_bf16;
   KvBatch b;
 };
 static_assert(sizeof(AttnArgs) <= 4096, "kernel argument budget");
 
 constexpr int kTileRows = 128;   // rows of a tile of the tiled kernel
-constexpr int kDecodeRows = 32;  // rows per request and key/value head the decode kernel takes
+// Rows per request and key/value head the decode kernel takes.  Beyond, column
+// tiles in one wave cost the second workgroup of a CU: 24 requests of 35 rows over
+// 5000 tokens took 57 us there, 39 us in 128-row tiles; 64 of 20 rows 80 against 102.
+constexpr int kDecodeRows = 32;
 
 hipError_t launch_attn_decode(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_tiled(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
@@ -96,9 +99,6 @@ hipError_t launch_attn_join(int D, const AttnArgs& a, hipStream_t st);
 // one: the one-token step's kernel (b.pos set, b.tokens == 1)
 hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st);
 hipError_t launch_kv_read(int D, bool bf16, bool int8, const KvReadArgs& a, int64_t units, hipStream_t st);
-
-// Blocks of at least this many are one split's share of a cache.
-constexpr int kMinTiles = 8;
 
 // ---- device side --------------------------------------------------------------
 // Element offset of (token t, channel ch) in a block's K part / V part; the

@@ -20,8 +20,12 @@ using namespace kda;
 namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // positions, rows, table capacity
-constexpr int64_t kDecodeTarget = 2048;  // workgroups a decode step is split into, at least
-constexpr int64_t kTiledTarget = 512;    // the same for tiles
+// Workgroups a call is split into, at least (and a share of the cache has no fewer
+// than min_blocks): two rounds of the decode kernel's three a CU (one million-token
+// request: 399 us at 2048, a third round nearly empty, 335 us at 1536; a third of
+// it past 16 rows, whose workgroups are two a CU), and the tiled kernel's three.
+constexpr int64_t kDecodeTarget = 1536;
+constexpr int64_t kTiledTarget = 768;
 
 kda_status check_kv_pool(const kda_kv_pool* p) {
   if (!p) return fail(KDA_ERR_NULL, "kv pool descriptor is NULL");
@@ -294,7 +298,7 @@ kda_status check_attn_rows(const kda_kv_pool* p, const void* q, kda_dtype in, in
 // How a call's rows are cut and how many workgroups share a tile's blocks.
 struct AttnPlan {
   bool decode;        // the decode kernel: one tile per request, at most kDecodeRows rows
-  int32_t tile_rows;
+  int32_t tile_rows, min_blocks;
   int64_t units, splits;
   size_t bytes;       // workspace of the partial results
 };
@@ -308,10 +312,10 @@ int64_t reach_blocks(int64_t end, int64_t len, int32_t window, int32_t sinks) {
   return blocks;
 }
 
-void plan_splits(AttnPlan* pl, const kda_kv_pool* p, int32_t Hq, int64_t rows, int64_t blocks, int64_t target) {
-  const int64_t wgs = std::max<int64_t>(1, pl->units * p->num_heads);
-  const int64_t want = (target + wgs - 1) / wgs;
-  pl->splits = std::max<int64_t>(1, std::min(want, (blocks + kMinTiles - 1) / kMinTiles));
+void plan_splits(AttnPlan* pl, const kda_kv_pool* p, int32_t Hq, int64_t rows, int64_t blocks, int64_t decode_rows) {
+  const int64_t wgs = std::max<int64_t>(1, pl->units * p->num_heads), target = !pl->decode ? kTiledTarget : decode_rows <= 16 ? kDecodeTarget : kDecodeTarget / 3;
+  pl->min_blocks = pl->decode ? 8 : 16;
+  pl->splits = std::max<int64_t>(1, std::min((target + wgs - 1) / wgs, blocks / pl->min_blocks));
   pl->bytes = pl->splits == 1 ? 0 : (size_t)(rows * Hq * pl->splits * (p->head_dim + 2) * 4);
 }
 
@@ -323,8 +327,7 @@ AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens
   pl.tile_rows = pl.decode ? kDecodeRows : kTileRows;
   pl.units = (int64_t)n * ((rows + pl.tile_rows - 1) / pl.tile_rows);
   plan_splits(&pl, p, Hq, (int64_t)n * tokens,
-              reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks),
-              pl.decode ? kDecodeTarget : kTiledTarget);
+              reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks), rows);
   return pl;
 }
 
@@ -341,7 +344,7 @@ AttnPlan plan_prefill(const kda_kv_pool* p, int32_t Hq, int32_t n, const int64_t
     pl.units += (len * G + kTileRows - 1) / kTileRows;
     blocks = std::max(blocks, reach_blocks(s + len, std::min<int64_t>(len, kTileRows), window, sinks));
   }
-  plan_splits(&pl, p, Hq, cu[n], blocks, kTiledTarget);
+  plan_splits(&pl, p, Hq, cu[n], blocks, 0);
   return pl;
 }
 
@@ -365,6 +368,7 @@ AttnArgs attn_args(const kda_kv_pool* p, const void* q, int64_t q_ld, void* o, k
   a.units = (int32_t)pl.units;
   a.tile_rows = pl.tile_rows;
   a.splits = (int32_t)pl.splits;
+  a.min_blocks = pl.min_blocks;
   a.out_bf16 = out == KDA_BF16;
   return a;
 }
