@@ -119,17 +119,16 @@ struct Reach {
   __device__ __forceinline__ int count() const { return sink_end + end - win; }
   __device__ __forceinline__ int block(int i) const { return i < sink_end ? i : win + i - sink_end; }
 };
-__device__ __forceinline__ Reach reach_of(int64_t first, int64_t last, int window, int sinks) {
+__device__ __forceinline__ Reach reach_of(int first, int last, int window, int sinks) {  // positions below 2^30
   Reach r;
-  r.end = (int)(last / kKvBlock) + 1;
-  r.win = 0;
-  if (window) r.win = (int)(max((int64_t)0, first - window + 1) / kKvBlock);
-  r.sink_end = (int)min((int64_t)r.win, ((int64_t)sinks + kKvBlock - 1) / kKvBlock);
+  r.end = last / kKvBlock + 1;
+  r.win = window ? max(0, first - window + 1) / kKvBlock : 0;
+  r.sink_end = min(r.win, (min(sinks, 1 << 30) + kKvBlock - 1) / kKvBlock);
   return r;
 }
 // Whether every query at [first, last] sees all of block blk.
-__device__ __forceinline__ bool all_seen(int64_t first, int64_t last, int window, int sinks, int blk) {
-  const int64_t j0 = (int64_t)blk * kKvBlock, j1 = j0 + kKvBlock - 1;
+__device__ __forceinline__ bool all_seen(int first, int last, int window, int sinks, int blk) {
+  const int j0 = blk * kKvBlock, j1 = j0 + kKvBlock - 1;
   return j1 <= first && (!window || j0 > last - window || j1 < sinks);
 }
 __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {  // positions below 2^30

@@ -17,53 +17,10 @@
 //
 // Few tiles (a short resumed prompt over a long cache) are split over the cache
 // like a decode step, and joined by the same kernel.
-#include "kda_attn_device.h"
+#include "kda_attn_rows.h"
 
 namespace kda {
 
-// Token of a block that matrix row i holds: the order that makes an
-// accumulator's registers the V part's slots.
-__device__ __forceinline__ int token_of(int a, int half, int b) { return 16 * (a & 1) + 8 * (a >> 1) + 4 * half + b; }
-
-__device__ __forceinline__ float half_max(float x) {
-  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
-}
-__device__ __forceinline__ float half_sum(float x) {
-  auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
-  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
-}
-__device__ __forceinline__ f32x16 zero16() {
-  f32x16 z;
-#pragma unroll
-  for (int i = 0; i < 16; ++i) z[i] = 0.f;
-  return z;
-}
-
-constexpr int kVmcnt0 = 0x0f70;  // s_waitcnt operand: vmcnt(0), the other counters not waited for
-
-// Each lane's 16 bytes at src to LDS, lane after lane from dst (uniform).  Not the
-// builtin: with it the compiler, which cannot tell the two buffers apart, waits for
-// these loads before the next LDS read; the loop waits for them itself, before the
-// barrier that hands the buffer over.
-__device__ __forceinline__ void to_lds16(const uint8_t* src, uint8_t* dst) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)dst;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(uni(at)), "v"(src) : "m0", "memory");
-}
-
-// Sum of an operand's eight weights, added to l.
-__device__ __forceinline__ float add8(f16x8 w, float l) {
-  const f16x2 one = {(_Float16)1.f, (_Float16)1.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) l = __builtin_amdgcn_fdot2(f16x2{w[2 * i], w[2 * i + 1]}, one, l, false);
-  return l;
-}
-__device__ __forceinline__ float add8(bf16x8 w, float l) {
-  const bf16x2_t one = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) l = __builtin_amdgcn_fdot2_f32_bf16(bf16x2_t{w[2 * i], w[2 * i + 1]}, one, l, false);
-  return l;
-}
 template <int D, int EB, int NP>
 __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled_kernel(AttnArgs a) {
   typedef AttnOp<EB> Op;
@@ -81,17 +38,9 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   const int req = uni(kv_find_unit(a.b, unit));
   const KvSeq s = kv_seq_uniform(a.b, req);
   const int row0 = (unit - s.unit) * ROWS, rows = s.len * a.G;
-  const int64_t cap = (int64_t)a.c.max_pages * a.c.page_tokens;
-  const bool off = s.start < 0, over = (int64_t)s.start + s.len > cap;
+  const bool off = s.start < 0, over = (int64_t)s.start + s.len > (int64_t)a.c.max_pages * a.c.page_tokens;
   if (off || over) {
-    if (sp == 0)
-      for (int i = threadIdx.x; i < min(ROWS, rows - row0) * D; i += NT) {
-        const int row = row0 + i / D;
-        const int64_t at = ((int64_t)(s.row + row / a.G) * a.Hq + h * a.G + row % a.G) * D + i % D;
-        const float y = off ? 0.f : __builtin_nanf("");
-        if (a.out_bf16) reinterpret_cast<uint16_t*>(a.o)[at] = f32_to_bf16(y);
-        else reinterpret_cast<float*>(a.o)[at] = y;
-      }
+    if (sp == 0) store_off(a, s, h, row0, ROWS, D, NT, off);
     return;
   }
   const int tp0 = s.start + row0 / a.G, tp1 = s.start + (min(rows, row0 + ROWS) - 1) / a.G;
@@ -99,54 +48,9 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   const Chunk ch = chunk_of(reach.count(), a.splits, a.min_blocks, sp);
   if (ch.begin >= ch.end) return;
 
-  // ---- queries: lane (half, col) holds row col's channels 16 ks + 8 half ..
-  const int row = row0 + wv * 32 + col;
-  const bool live = row < rows;
-  const int tok = (live ? row : rows - 1) / a.G, hq = h * a.G + (live ? row : rows - 1) % a.G;
-  const int qp = s.start + tok;  // position (below 2^30)
-  const int64_t oat = (int64_t)(s.row + tok) * a.Hq + hq;
+  const WaveRows wr = wave_rows(a, s, h, row0 + 32 * wv, col, D);
   Frag qf[KS][NP];
-  float qc = a.scale_log2;
-  {
-    const int64_t at = (int64_t)(s.row + tok) * a.q_ld + (int64_t)hq * D + 8 * half;
-    if constexpr (NP == 1 && EB == 2) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks)
-        qf[ks][0] = *reinterpret_cast<const Frag*>(reinterpret_cast<const uint16_t*>(a.q) + at + 16 * ks);
-    } else {
-      float x[KS][8], amax = 0.f;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if constexpr (NP == 1) {
-          const u16x8 w = *reinterpret_cast<const u16x8*>(reinterpret_cast<const uint16_t*>(a.q) + at + 16 * ks);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[ks][i] = bf16_to_f32(w[i]);
-        } else {
-          const float* p = reinterpret_cast<const float*>(a.q) + at + 16 * ks;
-          const f32x4 u = *reinterpret_cast<const f32x4*>(p), w = *reinterpret_cast<const f32x4*>(p + 4);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) { x[ks][i] = u[i]; x[ks][4 + i] = w[i]; }
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[ks][i]));
-      }
-      float f = 1.f, inv = 1.f;
-      if constexpr (EB == 1) f = fit_f16(half_max(amax), &inv);
-      qc *= inv;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        if constexpr (EB == 1) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) x[ks][i] *= f;
-        }
-        split8<EB, NP>(x[ks], qf[ks]);
-      }
-    }
-  }
-  // positions of the wave's rows
-  const int wr0 = row0 + wv * 32, wr1 = min(rows, wr0 + 32) - 1;
-  const bool idle = wr0 >= rows;
-  const int wp0 = s.start + min(wr0, rows - 1) / a.G, wp1 = s.start + max(wr1, 0) / a.G;
+  const float qc = load_queries<D, EB, NP>(a, wr.q + 8 * half, qf);
 
   f32x16 acc[DT];
   float m = kNegInf, l = 0.f;
@@ -181,7 +85,7 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) {
         const int o = (u * NT + wv * 64) * 16;
-        to_lds16(src + o + 16 * lane, &lds[buf][o]);
+        to_lds16(src + o, &lds[buf][o], lane);
       }
     } else {
 #pragma unroll
@@ -194,14 +98,7 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   auto put = [&](int buf) {  // int8: codes to fp16 operands in LDS
     if constexpr (EB == 1) {
 #pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int i = u * NT + threadIdx.x, part = i / (RAW / 16), x = i % (RAW / 16);
-        // unit (.., c, inner 16 or 64 places) of codes becomes units (.., 2 c) and (.., 2 c + 1)
-        const int low = part == 0 ? 16 : 64, c = x / low, y = x % low;
-        uint8_t* to = &lds[buf][part * PART + (2 * c * low + y) * 16];
-        *reinterpret_cast<f16x8*>(to) = codes8(raw[u][0], raw[u][1]);
-        *reinterpret_cast<f16x8*>(to + low * 16) = codes8(raw[u][2], raw[u][3]);
-      }
+      for (int u = 0; u < UNITS; ++u) put_codes<D>(&lds[buf][0], u * NT + threadIdx.x, raw[u]);
     }
   };
   // byte offsets of the lane's operands in a block: matrix row i = 8 a + 4 half' + b
@@ -221,10 +118,10 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
       for (int e = 0; e < 8; ++e) odd |= (u[e] & 0x7f80u) == 0x7f80u;
     }
     if (!__syncthreads_or(odd)) return;
-    if (!idle) {
+    if (!wr.idle) {
 #pragma unroll 1
       for (int t = 0; t < kKvBlock; ++t) {
-        const bool see = sees(qp, blk * kKvBlock + t, a.window, a.sinks);
+        const bool see = sees(wr.qp, blk * kKvBlock + t, a.window, a.sinks);
         const uint8_t* vt = v + 16 * (16 * ((t & 15) >> 2) + 4 * half) + 2 * ((t & 3) + 4 * (t >> 4));
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -246,16 +143,8 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
     __syncthreads();
   };
 
-  // One block against the wave's rows; full: every row sees all of it; bad: its page
-  // index or a scale is not usable, rows that see it become NaN.
-  auto step = [&](const uint8_t* kb, int blk, bool bad, bool full, float ksc, float vsc) __attribute__((always_inline)) {
-    float c = qc, lv = 0.f, iv = 1.f;
-    if constexpr (EB == 1) {
-      c = fmaxf(qc * ksc, 0x1p-126f);  // above 0, so that -inf stays -inf
-      vsc = vsc == 0.f ? 1.f : vsc < 0x1p-120f ? 0x1p-120f : vsc;
-      lv = __builtin_amdgcn_logf(vsc);
-      iv = __builtin_amdgcn_rcpf(vsc);
-    }
+  // One block against the wave's rows; full: every row sees all of it.
+  auto step = [&](const uint8_t* kb, int blk, bool full, const BlockScale<EB>& bs) __attribute__((always_inline)) {
     Frag kf[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) kf[ks] = *reinterpret_cast<const Frag*>(kb + koff + 512 * ks);
@@ -264,51 +153,16 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
       for (int p = 0; p < NP; ++p) x = Op::mma32(kf[ks], qf[ks][p], x);
-    if (!full) {
-#pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int j = blk * kKvBlock + token_of(e >> 2, half, e & 3);
-        x[e] = !sees(qp, j, a.window, a.sinks) ? kNegInf : bad ? __builtin_nanf("") : x[e];
-      }
-    }
-    float mx = kNegInf;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
-    mx = __builtin_fmaf(half_max(mx), c, lv);
-    // the reference of the weights follows the maximum once it is kSlack behind, row by
-    // row, so that a row's bits do not depend on its neighbours'
-    const bool grow = mx > m + kSlack;
-    if (__any(grow)) {
-      const float mn = grow ? mx : m, al = grow ? decay(m, mn) : 1.f;
-      m = mn;
-      l *= al;
-#pragma unroll
-      for (int d = 0; d < DT; ++d) acc[d] *= al;
-    }
-    const float sub = lv + Op::kLift - (m == kNegInf ? 0.f : m);
+    if (!full) mask16(x, wr.qp, blk, half, a.window, a.sinks, bs.bad);
     Frag pf[2][NP];
-    float sum = 0.f;
-    {
-      float w[16];
-#pragma unroll
-      for (int e = 0; e < 16; ++e) w[e] = exp2_f(__builtin_fmaf(x[e], c, sub));
-      split8<EB, NP>(w, pf[0]);
-      split8<EB, NP>(w + 8, pf[1]);
-      if constexpr (NP == 1) {
-        sum = add8(pf[1][0], add8(pf[0][0], 0.f));
-      } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) sum += w[e];
-      }
-    }
-    l = __builtin_fmaf(sum, iv, l);
+    weigh16<EB, NP, DT>(x, qc, bs, acc, m, l, pf);
     Frag vf[2 * DT];
 #pragma unroll
-    for (int i = 0; i < 2 * DT; ++i) vf[i] = *reinterpret_cast<const Frag*>(kb + voff + (i >> 1) * 2048 + (i & 1) * 512);
+    for (int i = 0; i < 2 * DT; ++i) vf[i] = *reinterpret_cast<const Frag*>(kb + voff + (i % DT) * 2048 + (i / DT) * 512);
 #pragma unroll
     for (int i = 0; i < 2 * DT; ++i)
 #pragma unroll
-      for (int p = 0; p < NP; ++p) acc[i >> 1] = Op::mma32(vf[i], pf[i & 1][p], acc[i >> 1]);
+      for (int p = 0; p < NP; ++p) acc[i % DT] = Op::mma32(vf[i], pf[i / DT][p], acc[i % DT]);
   };
 
   // the queries are waited for here: the loop must not wait for a load of theirs, with
@@ -322,52 +176,22 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
     __builtin_amdgcn_s_waitcnt(kVmcnt0);
     asm volatile("" ::: "memory");
     __syncthreads();  // the block is in LDS, and every wave has left the other buffer
-    float ksc = 1.f, vsc = 1.f;
-    bool bad = nbad;
-    if constexpr (EB == 1) {
-      ksc = __uint_as_float(uni(__float_as_uint(nks)));
-      vsc = __uint_as_float(uni(__float_as_uint(nvs)));
-      // a scale that is not finite: its block's values are NaN to every row that sees it
-      bad = bad || !(ksc < __builtin_inff() && vsc < __builtin_inff());
-      if (bad) ksc = vsc = 1.f;
-    }
+    BlockScale<EB> bs;
+    bs.set(EB == 1 ? __uint_as_float(uni(__float_as_uint(nks))) : 1.f, EB == 1 ? __uint_as_float(uni(__float_as_uint(nvs))) : 1.f,
+           nbad);
     if (i + 1 < count) {
       if (((i + 1) & 63) == 0) look_up(i + 1);
       fetch(i + 1, buf ^ 1);
     }
     if constexpr (EB == 2) {
-      if (bad || !all_seen(tp0, tp1, a.window, a.sinks, blk)) purify(buf, blk);
+      if (bs.bad || !all_seen(tp0, tp1, a.window, a.sinks, blk)) purify(buf, blk);
     }
-    if (idle || blk * kKvBlock > wp1) continue;  // no rows, or past every row of the wave
-    step(&lds[buf][0], blk, bad, !bad && all_seen(wp0, wp1, a.window, a.sinks, blk), ksc, vsc);
+    if (wr.idle || blk * kKvBlock > wr.p1) continue;  // no rows, or past every row of the wave
+    step(&lds[buf][0], blk, !bs.bad && all_seen(wr.p0, wr.p1, a.window, a.sinks, blk), bs);
   }
 
   const float ll = half_sum(l);
-  if (!live) return;
-  if (ch.used == 1) {
-    const float inv = 1.f / ll;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int64_t o = oat * D + 32 * d + 8 * q + 4 * half;
-        const f32x4 y = f32x4{acc[d][4 * q], acc[d][4 * q + 1], acc[d][4 * q + 2], acc[d][4 * q + 3]} * inv;
-        if (a.out_bf16) *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.o) + o) = pack_bf16x4(y[0], y[1], y[2], y[3]);
-        else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.o) + o) = y;
-      }
-  } else {
-    float* po = a.part_o + (oat * a.splits + sp) * D;
-#pragma unroll
-    for (int d = 0; d < DT; ++d)
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-        *reinterpret_cast<f32x4*>(po + 32 * d + 8 * q + 4 * half) =
-            f32x4{acc[d][4 * q], acc[d][4 * q + 1], acc[d][4 * q + 2], acc[d][4 * q + 3]};
-    if (half == 0) {
-      a.part_ml[2 * (oat * a.splits + sp)] = m;
-      a.part_ml[2 * (oat * a.splits + sp) + 1] = ll;
-    }
-  }
+  if (wr.live) store_row<DT>(a, wr.out, sp, ch.used, half, acc, m, ll);
 }
 
 template <int D, int EB, int NP> static void launch_t(const AttnArgs& a, hipStream_t st) {
