@@ -347,3 +347,63 @@ def test_random_calls(seed):
     for r, (s, m) in enumerate(zip(starts, lens)):
         check(o[at: at + m], q[at: at + m], f.held[r], s + np.arange(m), dtype, out, cache, window, sinks, r)
         at += m
+
+
+WIDE = [  # cache, out, hq, H, d, page_tokens, sequences, longest call, longest start, window, sinks
+    ("int8", "bf16", 6, 2, 128, 64, 140, 70, 300, 0, 0),
+    ("bf16", "bf16", 6, 2, 64, 96, 140, 70, 300, 0, 0),
+    ("bf16", "f32", 16, 8, 128, 32, 33, 40, 2700, 0, 0),
+    ("int8", "f32", 8, 8, 64, 160, 33, 300, 2700, 0, 0),
+    ("bf16", "bf16", 8, 8, 128, 64, 33, 300, 900, 75, 5),
+    ("int8", "bf16", 24, 8, 128, 64, 33, 90, 2700, 200, 40),
+]
+
+
+@pytest.mark.parametrize("case", WIDE)
+def test_wide_batches(case):
+    """Batches with a workgroup for every CU: sampled rows against the oracle, and a sequence's rows
+    bit for bit as in a call of its own, which is small and cut into other tiles (past 1000 tokens
+    such a call is split over the cache and joined, which rounds differently)."""
+    cache, out, hq, H, d, pt, n, longest, far, window, sinks = case
+    rng = np.random.default_rng(hq + d)
+    lens = [int(x) for x in rng.integers(0, longest + 1, n)]
+    starts = [int(x) for x in rng.integers(0, far + 1, n)]
+    lens[0], starts[0], lens[1], starts[1] = longest, far, 1, 0
+    f = Filled([s + m for s, m in zip(starts, lens)], H, d, pt, cache, seed=n + d)
+    q = queries(rng, sum(lens), hq, d, "bf16")
+    o = prefill(f, q, lens, starts, "bf16", out, window, sinks)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    for r in list(range(6)) + [n - 1]:
+        if not lens[r]:
+            continue
+        rows = slice(int(cu[r]), int(cu[r + 1]))
+        if starts[r] + lens[r] <= 1000:
+            alone = prefill(f, q[rows], [lens[r]], [starts[r]], "bf16", out, window, sinks,
+                            f.table[r: r + 1].contiguous())
+            assert torch.equal(alone, o[rows]), r
+        at = np.unique(np.linspace(0, lens[r] - 1, 9).astype(int))
+        check(o[rows][at], q[rows][at], f.held[r], starts[r] + at, "bf16", out, cache, window, sinks, r)
+
+
+@pytest.mark.parametrize("bad", [np.nan, np.inf, -np.inf])
+def test_wide_batches_and_values_out_of_sight(bad):
+    """Non-finite values in a bf16 cache, in a batch with a workgroup for every CU: rows before
+    and past the window of them are as without them, a bad page spoils the rows that see it."""
+    H, d, pt, n, m = 8, 64, 32, 34, 100
+    f = Filled([m] * n, H, d, pt, "bf16", seed=3)
+    q = queries(np.random.default_rng(10), n * m, 16, d, "bf16")
+    want = prefill(f, q, [m] * n, [0] * n, "bf16", "bf16", 40, 2)
+    x = [to_dev(y[50:51].copy(), "f32") for y in f.x]
+    x[1][0, :, 5] = bad
+    K.kda_kv_append(f.kb.pool, None, x[0], x[1], None, [0, 1], f.table[:1].contiguous(), start_pos=[50])
+    t = f.table_np.copy()
+    t[1, 1] = -1  # tokens 32..63 of the second sequence
+    got = prefill(f, q, [m] * n, [0] * n, "bf16", "bf16", 40, 2, torch.from_numpy(t).cuda())
+    p = np.arange(m)
+    sees = torch.from_numpy((p >= 50) & (p < 90))
+    assert torch.equal(got[2 * m:], want[2 * m:])
+    assert torch.equal(got[:m][~sees], want[:m][~sees])
+    assert not torch.isfinite(got[:m][sees][:, :, 5]).any()
+    assert torch.isfinite(got[:m][sees][:, :, [c for c in range(d) if c != 5]]).all()
+    sees = torch.from_numpy((p >= 32) & (p - 39 <= 63))
+    assert torch.isnan(got[m: 2 * m][sees]).all() and torch.equal(got[m: 2 * m][~sees], want[m: 2 * m][~sees])
