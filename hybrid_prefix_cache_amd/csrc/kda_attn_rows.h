@@ -1,5 +1,5 @@
-// kda_attn_rows.h -- 32 rows of a wave against one 32-token block: what the tiled
-// and the wide attention kernels share.
+// kda_attn_rows.h -- 32 rows of a wave against one 32-token block: the pieces of the
+// tiled attention kernel's step.
 //
 // S^T = K Q^T on 32x32x16 matrix instructions: a lane (half = lane / 32, col =
 // lane % 32) holds 16 logits of row col, at tokens token_of(e / 4, half, e % 4),
@@ -131,6 +131,17 @@ template <int EB> struct BlockScale {
       lv = __builtin_amdgcn_logf(vs);
       iv = __builtin_amdgcn_rcpf(vs);
     }
+  }
+  // Lane i's factors, to the whole wave.
+  __device__ __forceinline__ BlockScale of_lane(int i, bool is_bad) const {
+    BlockScale b;
+    b.bad = is_bad;
+    if constexpr (EB == 1) {
+      b.c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(c), i));
+      b.lv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv), i));
+      b.iv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(iv), i));
+    }
+    return b;
   }
 };
 

@@ -61,7 +61,11 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   const int per = a.c.page_tokens / kKvBlock, count = ch.end - ch.begin;
   const uint8_t* head0 = a.c.base + h * a.c.head_bytes;
   int pg = 0, in = 0;
-  auto look_up = [&](int base) {  // lane i: page and place of block base + i of the chunk
+  BlockScale<EB> scales;
+  // lane i: page, place and factors of block base + i of the chunk.  The scales are read
+  // here, 64 blocks at once: read block by block they would be scalar loads, whose wait
+  // is for all LDS reads under way too (8192-token int8 prompt, 32 heads: 604 us, so 584).
+  auto look_up = [&](int base) {
     const int i = base + lane;
     if (i < count) {
       const int blk = reach.block(ch.begin + i);
@@ -69,16 +73,21 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
       in = blk - j * per;
       pg = a.c.table[(int64_t)req * a.c.max_pages + j];
       if (pg < 0 || pg >= a.c.num_pages) pg = -1;
+      if constexpr (EB == 1) {
+        const uint8_t* at = head0 + (int64_t)max(pg, 0) * a.c.page_bytes + (int64_t)per * (2 * RAW);
+        const float2 sc = *reinterpret_cast<const float2*>(at + 8 * in);
+        scales.set(sc.x, sc.y, pg < 0);
+        if (scales.bad) pg = -1;
+      }
     }
   };
   constexpr int UNITS = 2 * RAW / 16 / NT;  // 16-byte units of a raw block a thread moves
   static_assert(UNITS >= 1, "a block has a unit for every thread");
   u32x4_t raw[UNITS];                       // int8: the next block's codes
-  float nks, nvs;
   int nbad = 0;
   auto fetch = [&](int i, int buf) {  // block i of the chunk
     const int page = __builtin_amdgcn_readlane(pg, i & 63), inner = __builtin_amdgcn_readlane(in, i & 63);
-    nbad = page < 0;  // a bad page: page 0's bytes, whose values never count
+    nbad = page < 0;  // a bad page or scale: page 0's bytes, whose values never count
     const uint8_t* head = head0 + (int64_t)max(page, 0) * a.c.page_bytes;
     const uint8_t* src = head + (int64_t)inner * (2 * RAW);
     if constexpr (EB == 2) {
@@ -90,9 +99,6 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
     } else {
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) raw[u] = *reinterpret_cast<const u32x4_t*>(src + (u * NT + threadIdx.x) * 16);
-      const float* sc = reinterpret_cast<const float*>(head + (int64_t)per * (2 * RAW)) + 2 * inner;
-      nks = sc[0];
-      nvs = sc[1];
     }
   };
   auto put = [&](int buf) {  // int8: codes to fp16 operands in LDS
@@ -176,9 +182,7 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
     __builtin_amdgcn_s_waitcnt(kVmcnt0);
     asm volatile("" ::: "memory");
     __syncthreads();  // the block is in LDS, and every wave has left the other buffer
-    BlockScale<EB> bs;
-    bs.set(EB == 1 ? __uint_as_float(uni(__float_as_uint(nks))) : 1.f, EB == 1 ? __uint_as_float(uni(__float_as_uint(nvs))) : 1.f,
-           nbad);
+    const BlockScale<EB> bs = scales.of_lane(i & 63, nbad);
     if (i + 1 < count) {
       if (((i + 1) & 63) == 0) look_up(i + 1);
       fetch(i + 1, buf ^ 1);
