@@ -70,6 +70,8 @@ class kda_conv_pool(ctypes.Structure):
 
 
 class kda_kv_pool(ctypes.Structure):
+    device = None  # of the tensor it was made from
+
     _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64),
                 ("num_pages", ctypes.c_int32), ("num_heads", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("page_tokens", ctypes.c_int32),
@@ -77,6 +79,8 @@ class kda_kv_pool(ctypes.Structure):
 
 
 class kda_rope(ctypes.Structure):
+    device = None  # of the tensors it was made from
+
     _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("num_pos", ctypes.c_int64),
                 ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
@@ -439,16 +443,26 @@ def kda_short_conv_update(cpool, x, w, y, page_in, page_out, *, n=None, out_dtyp
 # ---- paged key/value cache and its attention -----------------------------------
 def make_kv_pool(base, page_bytes: int, num_pages: int, num_heads: int, head_dim: int, page_tokens: int,
                  dtype: int):
-    """Key/value pool descriptor over caller-owned device memory (KDA_BF16 or KDA_INT8)."""
-    return kda_kv_pool(_dptr(base), int(page_bytes), int(num_pages), int(num_heads), int(head_dim),
+    """Key/value pool descriptor over caller-owned device memory (KDA_BF16 or KDA_INT8): a tensor,
+    which has to hold num_pages * page_bytes and which the descriptor keeps alive, or a pointer."""
+    pool = kda_kv_pool(_dptr(base), int(page_bytes), int(num_pages), int(num_heads), int(head_dim),
                        int(page_tokens), int(dtype))
+    if torch.is_tensor(base):
+        if base.numel() * base.element_size() < pool.num_pages * pool.page_bytes:
+            raise ValueError(f"base holds less than {num_pages} pages of {page_bytes} bytes")
+        pool.device, pool.base_tensor = base.get_device(), base
+    return pool
 
 
 def make_rope(cos, sin, *, interleaved: bool = False):
-    """Rotation descriptor over caller-owned fp32 device tables [positions, rot_dim / 2]."""
+    """Rotation descriptor over fp32 device tables [positions, rot_dim / 2], which it keeps alive."""
     if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32:
         raise ValueError("cos and sin must be float32 tables of one shape [positions, rot_dim / 2]")
-    return kda_rope(_dptr(cos), _dptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(interleaved)))
+    if cos.get_device() != sin.get_device():
+        raise ValueError("cos and sin must be tensors of one device")
+    rope = kda_rope(_dptr(cos), _dptr(sin), cos.shape[0], 2 * cos.shape[1], int(bool(interleaved)))
+    rope.device, rope.tables = cos.get_device(), (cos, sin)
+    return rope
 
 
 def _rows(name, x, rows, heads, d, dtype, dev):
@@ -504,6 +518,13 @@ def _ws(workspace, dev):
     return _dptr(workspace), workspace.numel() * workspace.element_size()
 
 
+def _here(what, dev):
+    """The current device; a descriptor made from tensors has to be of it."""
+    if what.device not in (None, dev):
+        raise ValueError(f"{type(what).__name__} must be of the current device")
+    return dev
+
+
 def _on(stream, dev):
     return torch.cuda.current_stream(dev).cuda_stream if stream is None else _stream(stream)
 
@@ -524,6 +545,8 @@ def kda_kv_workspace_bytes(num_seqs: int) -> int:
 def _append_tensors(pool, q, k, v, q_out, rows, rope, dev):
     """Arguments shared by the two appends: pointers, row distances, head count."""
     d, dt = pool.head_dim, k.dtype
+    if rope is not None:
+        _here(rope, dev)
     kp, kl = _rows("k", k, rows, pool.num_heads, d, None, dev)
     vp, vl = _rows("v", v, rows, pool.num_heads, d, dt, dev)
     if (q is None) != (q_out is None):
@@ -541,7 +564,7 @@ def kda_kv_append(pool, q, k, v, q_out, cu_seqlens, page_table, *, rope=None, st
     """q, q_out: [T, Hq, d] or both None; k, v: [T, H, d] (device tensors; q, k and v may be column
     ranges of one projection); page_table: int32 device tensor [num_seqs, max_pages]; host metadata
     as for kda_prefill_chunked; workspace: kda_kv_workspace_bytes (None up to 128 sequences)."""
-    dev = torch.cuda.current_device()
+    dev = _here(pool, torch.cuda.current_device())
     cu, sp, ns, rows, _keep = _packed(cu_seqlens, start_pos)
     qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, rows, rope, dev)
     tp = _ints("page_table", page_table, (ns, None), dev)
@@ -553,7 +576,7 @@ def kda_kv_append(pool, q, k, v, q_out, cu_seqlens, page_table, *, rope=None, st
 def kda_kv_append_step(pool, q, k, v, q_out, tokens, pos, page_table, *, rope=None, stream=None):
     """`tokens` tokens per request at positions pos[r] + t: tensors as for kda_kv_append with rows
     [n * tokens]; pos: int32 device tensor [n], negative for a request that takes no part."""
-    dev, n = torch.cuda.current_device(), pos.numel()
+    dev, n = _here(pool, torch.cuda.current_device()), pos.numel()
     qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, n * tokens, rope, dev)
     tp = _ints("page_table", page_table, (n, None), dev)
     _check(_lib.kda_kv_append_step(ctypes.byref(pool), rp, qp, kp, vp, dt, ql, kl, vl, op, hq, n, tokens,
@@ -562,7 +585,7 @@ def kda_kv_append_step(pool, q, k, v, q_out, tokens, pos, page_table, *, rope=No
 
 def kda_kv_read(pool, k_out, v_out, cu_seqlens, page_table, *, start_pos=None, workspace=None, stream=None):
     """Cached rows back at full precision: k_out, v_out [T, H, d] device tensors of one type."""
-    dev = torch.cuda.current_device()
+    dev = _here(pool, torch.cuda.current_device())
     cu, sp, ns, rows, _keep = _packed(cu_seqlens, start_pos)
     kp = _out("k_out", k_out, rows, pool.num_heads, pool.head_dim, None, dev)
     vp = _out("v_out", v_out, rows, pool.num_heads, pool.head_dim, k_out.dtype, dev)
@@ -583,7 +606,7 @@ def kda_attn_prefill(pool, q, o, cu_seqlens, page_table, *, scale, start_pos=Non
     """q, o: [T, Hq, d] device tensors (q may be columns of a wider tensor), row i of sequence s at
     position start_pos[s] + i; the cache holds every token up to it.  workspace: uint8 device tensor
     of kda_attn_prefill_workspace_bytes for the same metadata."""
-    dev = torch.cuda.current_device()
+    dev = _here(pool, torch.cuda.current_device())
     cu, sp, ns, rows, _keep = _packed(cu_seqlens, start_pos)
     hq = _heads(q, pool.head_dim)
     qp, ql = _rows("q", q, rows, hq, pool.head_dim, None, dev)
@@ -603,7 +626,7 @@ def kda_attn_decode_workspace_bytes(pool, num_q_heads: int, n: int, tokens: int,
 def kda_attn_decode(pool, q, o, tokens, pos, page_table, *, scale, window=0, sinks=0, workspace=None, stream=None):
     """`tokens` queries per request: q, o [n * tokens, Hq, d] device tensors, row r*tokens + t at
     position pos[r] + t (pos: int32 device tensor [n], negative for a request that takes no part)."""
-    dev, n, hq = torch.cuda.current_device(), pos.numel(), _heads(q, pool.head_dim)
+    dev, n, hq = _here(pool, torch.cuda.current_device()), pos.numel(), _heads(q, pool.head_dim)
     qp, ql = _rows("q", q, n * tokens, hq, pool.head_dim, None, dev)
     op = _out("o", o, n * tokens, hq, pool.head_dim, None, dev)
     tp = _ints("page_table", page_table, (n, None), dev)

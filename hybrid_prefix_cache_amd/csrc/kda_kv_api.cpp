@@ -20,6 +20,7 @@ using namespace kda;
 namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // positions, rows, table capacity
+constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;  // workgroups of 256 threads a launch can count
 // Workgroups a call is split into, at least (and a share of the cache has no fewer
 // than min_blocks): two rounds of the decode kernel's three a CU (one million-token
 // request: 399 us at 2048, a third round nearly empty, 335 us at 1536; a third of
@@ -280,7 +281,8 @@ kda_status check_attn(const kda_kv_pool* p, kda_dtype in, kda_dtype out, int32_t
     return fail(KDA_ERR_DTYPE, "unknown dtype code (in %d, out %d)", (int)in, (int)out);
   if (Hq < 1 || Hq > 1 << 16 || Hq % p->num_heads != 0)
     return fail(KDA_ERR_SHAPE, "num_q_heads %d must be a positive multiple of the pool's %d heads", Hq, p->num_heads);
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KDA_ERR_SHAPE, "scale must be positive and finite");
+  if (!(scale > 0.f) || !std::isfinite(scale * 1.44269504f))
+    return fail(KDA_ERR_SHAPE, "scale must be positive and finite (its product with log2 e too)");
   if (window < 0 || sinks < 0) return fail(KDA_ERR_SHAPE, "window and sinks must be >= 0 (got %d, %d)", window, sinks);
   return KDA_OK;
 }
@@ -441,7 +443,7 @@ kda_status kda_kv_append(const kda_kv_pool* pool, const kda_rope* rope, const vo
     if (s != KDA_OK || rows == 0) return s == KDA_OK ? ok() : s;
     s = check_append_rows(pool, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads, rows);
     if (s != KDA_OK) return s;
-    if (units * pool->num_heads * 2 + rows > kMaxTokens) return fail(KDA_ERR_SHAPE, "too much work for one call");
+    if (units * pool->num_heads * 2 + (rows + 1) / 2 > kMaxGroups) return fail(KDA_ERR_SHAPE, "too much work for one call");
     s = check_workspace(workspace, workspace_bytes, seq_table_bytes(num_seqs));
     if (s != KDA_OK) return s;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -472,7 +474,8 @@ kda_status kda_kv_append_step(const kda_kv_pool* pool, const kda_rope* rope, con
     s = check_append_rows(pool, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads, rows);
     if (s != KDA_OK) return s;
     const int per = (tokens + kKvBlock - 2) / kKvBlock + 1;  // blocks `tokens` consecutive tokens can touch
-    if ((int64_t)n * per * pool->num_heads * 2 + rows > kMaxTokens) return fail(KDA_ERR_SHAPE, "too much work for one call");
+    if ((int64_t)n * per * pool->num_heads * 2 + (rows + 1) / 2 > kMaxGroups)
+      return fail(KDA_ERR_SHAPE, "too much work for one call");
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (validating()) {
       std::vector<KvSeq> seqs;
@@ -508,7 +511,7 @@ kda_status kda_kv_read(const kda_kv_pool* pool, void* k_out, void* v_out, kda_dt
     if (s != KDA_OK) return s;
     if (overlap(k_out, row_bytes(rows, w, w, out_dtype), v_out, row_bytes(rows, w, w, out_dtype)))
       return fail(KDA_ERR_SHAPE, "k_out overlaps v_out");
-    if (units * pool->num_heads > kMaxTokens) return fail(KDA_ERR_SHAPE, "too much work for one call");
+    if (units * pool->num_heads > kMaxGroups) return fail(KDA_ERR_SHAPE, "too much work for one call");
     s = check_workspace(workspace, workspace_bytes, seq_table_bytes(num_seqs));
     if (s != KDA_OK) return s;
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
@@ -563,7 +566,7 @@ kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in
     s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
     if (s != KDA_OK) return s;
     const AttnPlan pl = plan_prefill(pool, num_q_heads, num_seqs, cu_seqlens, start_pos, window, sinks);
-    if (pl.units * pool->num_heads * pl.splits > kMaxTokens || rows * num_q_heads > kMaxTokens)
+    if (pl.units * pool->num_heads * pl.splits > kMaxGroups || rows * num_q_heads > kMaxTokens)
       return fail(KDA_ERR_SHAPE, "too much work for one call");
     const size_t table_bytes = seq_table_bytes(num_seqs);
     s = check_workspace(workspace, workspace_bytes, table_bytes + std::max<size_t>(256, pl.bytes));
@@ -610,7 +613,7 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
     s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
     if (s != KDA_OK) return s;
     const AttnPlan pl = plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks);
-    if (pl.units * pool->num_heads * pl.splits > kMaxTokens || rows * num_q_heads > kMaxTokens)
+    if (pl.units * pool->num_heads * pl.splits > kMaxGroups || rows * num_q_heads > kMaxTokens)
       return fail(KDA_ERR_SHAPE, "too much work for one call");
     s = check_workspace(workspace, workspace_bytes, std::max<size_t>(256, pl.bytes));
     if (s != KDA_OK) return s;

@@ -433,6 +433,12 @@ kda_status kda_short_conv_update(const kda_conv_pool* cpool, const void* x, cons
  * row that has to see such a page is NaN.  With KDA_VALIDATE=1 the tables (and
  * positions) are copied to the host and checked first (this synchronises the
  * stream; not for capture).  max_pages * page_tokens is at most 2^30.
+ *
+ * A call is refused (KDA_ERR_SHAPE) if it needs 2^24 workgroups or more: an
+ * append has two for a block of a head and, with q, at most one for two rows, a
+ * read one for a block of a head, an attention call one for a key/value head and
+ * 128 (step form: request or 128) of its rows, times the workgroups that share
+ * the cache where there are few of them.
  */
 typedef struct {
   void* base;
@@ -540,14 +546,18 @@ kda_status kda_kv_read(const kda_kv_pool* pool, void* k_out, void* v_out, kda_dt
  *     o = sum_j w_j v_j / sum_j w_j,   w_j = exp(scale * q . k_j)
  *   q : [T, num_q_heads, d] of in_dtype, rows q_ld elements apart; o :
  *   [T, num_q_heads, d] out_dtype, contiguous, not overlapping q.  16-byte
- *   aligned.  scale > 0 and finite.  num_q_heads a multiple of H.
+ *   aligned.  scale > 0 and scale * log2(e) finite.  num_q_heads a multiple of H.
  *   Host metadata: cu_seqlens, start_pos as in kda_kv_append (row i of sequence
  *   s sits at position start_pos[s] + i).
  * Pages that no row of the call sees are not read and may have been freed.
  * What slots past a request's tokens, and tokens a row does not see, hold
  * (NaN included) does not reach that row, but for KDA_INT8 blocks, whose scale
  * all their tokens share.
- * workspace: kda_attn_prefill_workspace_bytes with the same metadata.
+ * A KDA_INT8 value scale in (0, 2^-120) counts as 2^-120 (an error of o below
+ * 2^-113); a block with a scale that is not finite is NaN to the rows that see it.
+ * workspace: kda_attn_prefill_workspace_bytes with the same metadata.  Two calls
+ * that may overlap (streams, captured graphs) need one each, here and wherever
+ * this section takes a workspace.
  */
 size_t kda_attn_prefill_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads,
                                         int32_t num_seqs, const int64_t* cu_seqlens,
@@ -564,8 +574,7 @@ kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in
  * The decode-step form: `tokens` (1..64) queries for each of n requests, rows
  * r*tokens + t at positions pos[r] + t (pos: int32 DEVICE array [n]).  Rows of a
  * request with pos[r] < 0 are 0; rows of one whose pos[r] + tokens passes
- * max_pages * page_tokens are NaN.  workspace: kda_attn_decode_workspace_bytes;
- * two calls that may overlap (streams, captured graphs) need one each.
+ * max_pages * page_tokens are NaN.  workspace: kda_attn_decode_workspace_bytes.
  */
 size_t kda_attn_decode_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n,
                                        int32_t tokens, int32_t max_pages, int32_t window,

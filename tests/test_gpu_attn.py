@@ -407,3 +407,104 @@ def test_wide_batches_and_values_out_of_sight(bad):
     assert torch.isfinite(got[:m][sees][:, :, [c for c in range(d) if c != 5]]).all()
     sees = torch.from_numpy((p >= 32) & (p - 39 <= 63))
     assert torch.isnan(got[m: 2 * m][sees]).all() and torch.equal(got[m: 2 * m][~sees], want[m: 2 * m][~sees])
+
+
+def test_packed_calls_in_a_graph_and_on_two_streams():
+    """140 sequences (their table ships through the workspace): append and attention captured together,
+    replayed between eager calls; and two streams at once, a workspace each.  All bits as in plain calls."""
+    n, H, hq, d, pt = 140, 2, 4, 64, 32
+    rng = np.random.default_rng(31)
+    lens = [int(x) for x in rng.integers(0, 60, n)]
+    cu = np.concatenate([[0], np.cumsum(lens)]).astype(np.int64)
+    T = int(cu[-1])
+    table_np = tables([2] * n, 2 * n)
+    table = torch.from_numpy(table_np).cuda()
+    k, v = (to_dev(rng.standard_normal((T, H, d)), "bf16") for _ in range(2))
+    q = queries(rng, T, hq, d, "bf16", False)
+    kbs = [KvBuf(2 * n, H, d, pt, "int8") for _ in range(3)]
+
+    def call(kb, o, w):
+        K.kda_kv_append(kb.pool, None, k, v, None, cu, table, workspace=w[0])
+        K.kda_attn_prefill(kb.pool, q, o, cu, table, scale=0.11, window=50, sinks=3, workspace=w[1])
+
+    def spaces():
+        return (ws(K.kda_kv_workspace_bytes(n)),
+                ws(K.kda_attn_prefill_workspace_bytes(kbs[0].pool, hq, cu, window=50, sinks=3)))
+
+    outs, wss = [torch.zeros_like(q) for _ in range(3)], [spaces() for _ in range(3)]
+    call(kbs[0], outs[0], wss[0])
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call(kbs[1], outs[1], wss[1])
+    for i in range(3):
+        k.mul_(-1.5), q.mul_(1.25)
+        outs[1].fill_(7.0)
+        g.replay()
+        call(kbs[0], outs[0], wss[0])
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], outs[1]) and torch.equal(kbs[0].buf, kbs[1].buf), i
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    for i in range(4):
+        for s, kb, o, w in ((streams[0], kbs[1], outs[1], wss[1]), (streams[1], kbs[2], outs[2], wss[2])):
+            with torch.cuda.stream(s):
+                call(kb, o, w)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[1], outs[0]) and torch.equal(outs[2], outs[0])
+    # pages of the third buffer that no token reached keep their poison
+    assert torch.equal(kbs[2].buf, kbs[1].buf)
+
+
+def test_bindings_refuse():
+    """Tensors of another device, type, shape or layout are refused before the library is called."""
+    f = Filled([50, 40], 2, 64, 32, "int8", spare=8)
+    pool, table, q = f.kb.pool, f.table, queries(np.random.default_rng(5), 2, 4, 64, "bf16", False)
+    pos = torch.tensor([50, 40], dtype=torch.int32, device="cuda")
+    o, w = torch.zeros_like(q), ws(K.kda_attn_decode_workspace_bytes(pool, 4, 2, 1, table.shape[1]))
+    k = to_dev(np.zeros((2, 2, 64)), "bf16")
+    before = f.kb.buf.clone()
+
+    def dec(**kw):
+        a = dict(q=q, o=o, tokens=1, pos=pos, page_table=table)
+        K.kda_attn_decode(pool, **{**a, **kw}, scale=0.1, workspace=w)
+
+    def pre(**kw):
+        a = dict(q=q, o=o, cu_seqlens=[0, 1, 2], page_table=table, start_pos=[50, 40])
+        K.kda_attn_prefill(pool, **{**a, **kw}, scale=0.1, workspace=w)
+
+    def app(**kw):
+        a = dict(q=None, k=k, v=k, q_out=None, tokens=1, pos=pos, page_table=table)
+        K.kda_kv_append_step(pool, **{**a, **kw})
+
+    def rd(**kw):
+        a = dict(k_out=torch.zeros_like(k), v_out=torch.zeros_like(k), cu_seqlens=[0, 1, 2], page_table=table)
+        K.kda_kv_read(pool, **{**a, **kw})
+
+    wide = torch.zeros((2, 8, 64), dtype=torch.bfloat16, device="cuda")
+    calls = [
+        (dec, dict(q=q.cpu())), (dec, dict(q=q.half())), (dec, dict(q=q[:1])), (dec, dict(q=q[:, :, :32])),
+        (dec, dict(q=q.flatten(1))), (dec, dict(q=wide[:, ::2])), (dec, dict(o=wide[:, :4])), (dec, dict(o=o[:1])),
+        (dec, dict(o=o.cpu())), (dec, dict(pos=pos.long())), (dec, dict(pos=pos.cpu())), (dec, dict(pos=pos[:1])),
+        (dec, dict(page_table=table[:1])), (dec, dict(page_table=table.cpu())), (dec, dict(page_table=table.t())),
+        (dec, dict(page_table=table.flatten())), (dec, dict(page_table=table.long())), (dec, dict(tokens=2)),
+        (pre, dict(q=q.cpu())), (pre, dict(cu_seqlens=[0, 2])), (pre, dict(cu_seqlens=[0, 1, 3])),
+        (pre, dict(start_pos=[50])), (pre, dict(cu_seqlens=[])), (pre, dict(o=o.half())),
+        (app, dict(k=k.cpu())), (app, dict(v=k.float())), (app, dict(k=k[:, :1])), (app, dict(q=q)),
+        (app, dict(q=q, q_out=wide[:, :4])), (app, dict(v=k.transpose(0, 1))),
+        (app, dict(rope=K.kda_rope(0, 0, 8, 16, 0))),
+        (rd, dict(k_out=k.float())), (rd, dict(v_out=wide[:, :2])), (rd, dict(cu_seqlens=[0, 1])),
+    ]
+    for fn, kw in calls:
+        with pytest.raises((ValueError, K.KdaError)):
+            fn(**kw)
+    small = torch.zeros(f.kb.buf.numel() - 64, dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        K.make_kv_pool(small, f.kb.page_bytes, f.kb.pages, 2, 64, 32, K.KDA_INT8)
+    c = torch.zeros((64, 32), device="cuda")
+    for bad in ((c, c[:, :16]), (c, c.cpu()), (c.cpu(), c), (c.t(), c.t()), (c.bfloat16(), c.bfloat16()), (c[0], c[0])):
+        with pytest.raises(ValueError):
+            K.make_rope(*bad)
+    torch.cuda.synchronize()
+    assert torch.equal(before, f.kb.buf)

@@ -167,6 +167,29 @@ def test_workspace_bytes():
         assert K.kda_attn_decode_workspace_bytes(p, *args) == 0, args
 
 
+def step_only(heads, n, tokens):
+    return K.raw_call("kda_kv_append_step", ctypes.byref(pool(num_heads=heads)), None, None, FAKE, 2 * FAKE, K.KDA_BF16,
+                      0, heads * 128, heads * 128, None, 0, n, tokens, FAKE, FAKE, 4, None)
+
+
+@pytest.mark.parametrize("call,kw", [
+    (append, dict(p=pool(num_heads=64, page_tokens=32), k_ld=8192, v_ld=8192, q=None, q_out=None, hq=0,
+                  cu=(0, 1 << 22), max_pages=1 << 17)),
+    (step_only, dict(heads=4, n=1 << 21, tokens=1)),
+    (step_only, dict(heads=1, n=3 << 20, tokens=64)),
+    (read, dict(p=pool(num_heads=1), cu=(0, 1 << 29), max_pages=1 << 23, v=FAKE << 28)),
+    (decode, dict(p=pool(num_heads=32), n=1 << 19, q_ld=4096, hq=32, o=FAKE << 20)),
+])
+def test_calls_past_the_launch_limit(call, kw):
+    """2^24 workgroups and more are refused, before anything is enqueued."""
+    assert call(**kw) == K.KDA_ERR_SHAPE and "too much work" in K.kda_last_error()
+
+
+@pytest.mark.parametrize("call", [prefill, decode])
+def test_scale_past_fp32(call):
+    assert call(scale=3e38) == K.KDA_ERR_SHAPE
+
+
 def test_block_order_of_the_oracle_covers_every_slot():
     """The documented element order is a permutation of the block, for both parts and types."""
     from oracle import attention as A
