@@ -17,6 +17,17 @@
 //
 // Few tiles (a short resumed prompt over a long cache) are split over the cache
 // like a decode step, and joined by the same kernel.
+//
+// Bound by the matrix and vector units together, and by the power they draw: an
+// 8192-token prompt of 32 heads over 8 (550 GFLOP) takes 584 us over an int8 cache
+// (942 TFLOP/s) and 530 us over a bf16 one (1038); with a cache and queries of
+// zeros, the same instructions take 461 and 385 us.  The largest library products
+// of random bf16 matrices reach 1.31-1.34 PFLOP/s on this part (1.8 of zeros).
+// Of a block's 1100 SIMD cycles the matrix unit has 512, vector instructions 510
+// (bf16) or 680 (int8).  Taken for it: one 32-token block a step and three
+// workgroups a CU, whose waves fill each other's waits (64-token steps, two
+// workgroups a CU: 969 -> 686 us was as far as they came; 256 rows and eight waves
+// in one step 613 us; eight waves in two groups a phase apart 835 us).
 #include "kda_attn_rows.h"
 
 namespace kda {

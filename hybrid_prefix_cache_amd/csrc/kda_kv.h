@@ -1,5 +1,5 @@
 // kda_kv.h -- the paged key/value cache: block layout, the sequences of a call,
-// kernel arguments and launch entry points (kda_kv.hip, kda_attn.hip).
+// kernel arguments and launch entry points (kda_kv.hip, kda_attn_*.hip).
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
