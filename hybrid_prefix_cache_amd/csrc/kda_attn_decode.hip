@@ -109,6 +109,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     return;
   }
   const Reach reach = reach_of(p0, p1, a.window, a.sinks);
+  const Whole whole = whole_of(p0, p1, a.window, a.sinks);
   const Chunk ch = chunk_of(reach.count(), a.splits, a.min_blocks, sp);
   if (ch.begin >= ch.end) return;
 
@@ -199,7 +200,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       fetch(i + 1, nxt, nxt_pg);
     }
     const int blk = reach.block(first + 4 * i);
-    const bool bad = cur_pg < 0, full = !bad && all_seen(p0, p1, a.window, a.sinks, blk);
+    const bool bad = cur_pg < 0, full = !bad && whole.has(blk);
     float ks = 1.f, lv = 0.f, iv = 1.f;
     if (EB == 1 && !bad) {
       ks = cur.ks;

@@ -128,10 +128,17 @@ __device__ __forceinline__ Reach reach_of(int first, int last, int window, int s
   r.sink_end = min(r.win, (min(sinks, 1 << 30) + kKvBlock - 1) / kKvBlock);
   return r;
 }
-// Whether every query at [first, last] sees all of block blk.
-__device__ __forceinline__ bool all_seen(int first, int last, int window, int sinks, int blk) {
-  const int j0 = blk * kKvBlock, j1 = j0 + kKvBlock - 1;
-  return j1 <= first && (!window || j0 > last - window || j1 < sinks);
+// The blocks of which every query at [first, last] sees all.
+struct Whole {
+  int last, win, sinks;  // up to `last`, from `win` on or below `sinks`
+  __device__ __forceinline__ bool has(int blk) const { return blk <= last && (blk >= win || blk < sinks); }
+};
+__device__ __forceinline__ Whole whole_of(int first, int last, int window, int sinks) {
+  Whole w;
+  w.last = (first + 1) / kKvBlock - 1;
+  w.win = window ? max(0, last - window + kKvBlock) / kKvBlock : 0;  // 32 blk > last - window
+  w.sinks = sinks / kKvBlock;
+  return w;
 }
 __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {  // positions below 2^30
   return j <= p && (!window || j > p - window || j < sinks);

@@ -32,14 +32,20 @@ __device__ __forceinline__ f32x16 zero16() {
 
 constexpr int kVmcnt0 = 0x0f70;  // s_waitcnt operand: vmcnt(0), the other counters not waited for
 
-// 16 bytes a lane from src (uniform) + 16 * lane to LDS, from dst (uniform) on.  Not
-// the builtin: with it the compiler, which cannot tell the buffers apart, waits for
-// these loads before the next LDS read; the loops wait for them themselves, before
-// the barrier that hands a buffer over.
-__device__ __forceinline__ void to_lds16(const uint8_t* src, uint8_t* dst, int lane) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)dst;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(uni(at)), "v"(16 * lane), "s"(src)
-               : "m0", "memory");
+// N times 1 KB, 16 bytes a lane each, from src (uniform) on to the LDS address dst
+// (uniform) on; the instruction's offset counts on both sides.  Not the builtin: with
+// it the compiler, which cannot tell the buffers apart, waits for these loads before
+// the next LDS read; the loops wait for them themselves, before the barrier that hands
+// a buffer over.
+template <int N> __device__ __forceinline__ void to_lds(const uint8_t* src, uint32_t dst, int lane16) {
+  static_assert(N == 2 || N == 4, "");
+  if constexpr (N == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:1024" ::"s"(dst), "v"(lane16), "s"(src) : "m0", "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:1024\n\tglobal_load_lds_dwordx4 %1, %2 offset:2048\n\t"
+                 "global_load_lds_dwordx4 %1, %2 offset:3072" ::"s"(dst), "v"(lane16), "s"(src) : "m0", "memory");
 }
 
 // Sum of an operand's eight weights, added to l.

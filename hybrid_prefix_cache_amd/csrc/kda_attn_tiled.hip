@@ -56,10 +56,12 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   }
   const int tp0 = s.start + row0 / a.G, tp1 = s.start + (min(rows, row0 + ROWS) - 1) / a.G;
   const Reach reach = reach_of(tp0, tp1, a.window, a.sinks);
+  const Whole tile_sees = whole_of(tp0, tp1, a.window, a.sinks);
   const Chunk ch = chunk_of(reach.count(), a.splits, a.min_blocks, sp);
   if (ch.begin >= ch.end) return;
 
   const WaveRows wr = wave_rows(a, s, h, row0 + 32 * wv, col, D);
+  const Whole wave_sees = whole_of(wr.p0, wr.p1, a.window, a.sinks);
   Frag qf[KS][NP];
   const float qc = load_queries<D, EB, NP>(a, wr.q + 8 * half, qf);
 
@@ -71,42 +73,38 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   // ---- staging: one block a step
   const int per = a.c.page_tokens / kKvBlock, count = ch.end - ch.begin;
   const uint8_t* head0 = a.c.base + h * a.c.head_bytes;
-  int pg = 0, in = 0;
+  int64_t at = 0;  // of lane i's block in the head; negative: a bad page or scale
   BlockScale<EB> scales;
-  // lane i: page, place and factors of block base + i of the chunk.  The scales are read
+  // lane i: place and factors of block base + i of the chunk.  The scales are read
   // here, 64 blocks at once: read block by block they would be scalar loads, whose wait
   // is for all LDS reads under way too (8192-token int8 prompt, 32 heads: 604 us, so 584).
   auto look_up = [&](int base) {
     const int i = base + lane;
     if (i < count) {
       const int blk = reach.block(ch.begin + i);
-      const int j = blk / per;
-      in = blk - j * per;
-      pg = a.c.table[(int64_t)req * a.c.max_pages + j];
-      if (pg < 0 || pg >= a.c.num_pages) pg = -1;
+      const int j = blk / per, in = blk - j * per, pg = a.c.table[(int64_t)req * a.c.max_pages + j];
+      bool bad = pg < 0 || pg >= a.c.num_pages;
+      at = (bad ? 0 : pg) * a.c.page_bytes;
       if constexpr (EB == 1) {
-        const uint8_t* at = head0 + (int64_t)max(pg, 0) * a.c.page_bytes + (int64_t)per * (2 * RAW);
-        const float2 sc = *reinterpret_cast<const float2*>(at + 8 * in);
-        scales.set(sc.x, sc.y, pg < 0);
-        if (scales.bad) pg = -1;
+        const float2 sc = *reinterpret_cast<const float2*>(head0 + at + (int64_t)per * (2 * RAW) + 8 * in);
+        scales.set(sc.x, sc.y, bad);
+        bad = scales.bad;
       }
+      at = bad ? -1 : at + (int64_t)in * (2 * RAW);
     }
   };
   constexpr int UNITS = 2 * RAW / 16 / NT;  // 16-byte units of a raw block a thread moves
   static_assert(UNITS >= 1, "a block has a unit for every thread");
   u32x4_t raw[UNITS];                       // int8: the next block's codes
   int nbad = 0;
+  const uint32_t lds0 = uni((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0]);
   auto fetch = [&](int i, int buf) {  // block i of the chunk
-    const int page = __builtin_amdgcn_readlane(pg, i & 63), inner = __builtin_amdgcn_readlane(in, i & 63);
-    nbad = page < 0;  // a bad page or scale: page 0's bytes, whose values never count
-    const uint8_t* head = head0 + (int64_t)max(page, 0) * a.c.page_bytes;
-    const uint8_t* src = head + (int64_t)inner * (2 * RAW);
+    const int lo = __builtin_amdgcn_readlane((int)at, i & 63), hi = __builtin_amdgcn_readlane((int)(at >> 32), i & 63);
+    nbad = hi < 0;  // a bad page or scale: page 0's bytes, whose values never count
+    const uint8_t* src = head0 + (nbad ? 0 : (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo));
     if constexpr (EB == 2) {
-#pragma unroll
-      for (int u = 0; u < UNITS; ++u) {
-        const int o = (u * NT + wv * 64) * 16;
-        to_lds16(src + o, &lds[buf][o], lane);
-      }
+      constexpr int WAVE = 1024 * UNITS;  // bytes a wave moves
+      to_lds<UNITS>(src + wv * WAVE, lds0 + buf * (2 * PART) + wv * WAVE, 16 * lane);
     } else {
 #pragma unroll
       for (int u = 0; u < UNITS; ++u) raw[u] = *reinterpret_cast<const u32x4_t*>(src + (u * NT + threadIdx.x) * 16);
@@ -199,10 +197,10 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
       fetch(i + 1, buf ^ 1);
     }
     if constexpr (EB == 2) {
-      if (bs.bad || !all_seen(tp0, tp1, a.window, a.sinks, blk)) purify(buf, blk);
+      if (bs.bad || !tile_sees.has(blk)) purify(buf, blk);
     }
     if (wr.idle || blk * kKvBlock > wr.p1) continue;  // no rows, or past every row of the wave
-    step(&lds[buf][0], blk, !bs.bad && all_seen(wr.p0, wr.p1, a.window, a.sinks, blk), bs);
+    step(&lds[buf][0], blk, !bs.bad && wave_sees.has(blk), bs);
   }
 
   const float ll = half_sum(l);
