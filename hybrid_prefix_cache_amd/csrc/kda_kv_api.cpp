@@ -21,12 +21,17 @@ namespace {
 
 constexpr int64_t kMaxTokens = (int64_t)1 << 30;  // positions, rows, table capacity
 constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;  // workgroups of 256 threads a launch can count
-// Workgroups a call is split into, at least (and a share of the cache has no fewer
-// than min_blocks): two rounds of the decode kernel's three a CU (one million-token
-// request: 399 us at 2048, a third round nearly empty, 335 us at 1536; a third of
-// it past 16 rows, whose workgroups are two a CU), and the tiled kernel's three.
+// Workgroups a decode call is split into, at least (and a share of the cache has no
+// fewer than min_blocks): two rounds of the decode kernel's three a CU (one
+// million-token request: 399 us at 2048, a third round nearly empty, 335 us at 1536; a
+// third of it past 16 rows, whose workgroups are two a CU).
 constexpr int64_t kDecodeTarget = 1536;
-constexpr int64_t kTiledTarget = 768;
+// What the shares of the tiled kernel are weighed by, measured at 128 channels: us a
+// block takes a workgroup with one, two or three on the CU; us of the join's launch;
+// bytes of partial results a us.  Filling the card whatever it cost, prompts of 1024,
+// 2048 and 3000 tokens (32 heads, bf16 cache) took 43, 86 and 135 us; weighed, 31, 60 and 95.
+constexpr int64_t kCUs = 256;
+constexpr double kStepUs[4] = {0, 1.1, 1.15, 1.71}, kJoinUs = 4.0, kPartialRate = 5e6;
 
 kda_status check_kv_pool(const kda_kv_pool* p) {
   if (!p) return fail(KDA_ERR_NULL, "kv pool descriptor is NULL");
@@ -314,11 +319,41 @@ int64_t reach_blocks(int64_t end, int64_t len, int32_t window, int32_t sinks) {
   return blocks;
 }
 
-void plan_splits(AttnPlan* pl, const kda_kv_pool* p, int32_t Hq, int64_t rows, int64_t blocks, int64_t decode_rows) {
-  const int64_t wgs = std::max<int64_t>(1, pl->units * p->num_heads), target = !pl->decode ? kTiledTarget : decode_rows <= 16 ? kDecodeTarget : kDecodeTarget / 3;
-  pl->min_blocks = pl->decode ? 8 : 16;
+size_t partial_bytes(const kda_kv_pool* p, int32_t Hq, int64_t rows, int64_t splits) {
+  return splits == 1 ? 0 : (size_t)(rows * Hq * splits * (p->head_dim + 2) * 4);
+}
+
+// The decode kernel: its partial results are small beside the cache it reads, so the
+// card is filled wherever shares stay above min_blocks.
+void split_decode(AttnPlan* pl, const kda_kv_pool* p, int32_t Hq, int64_t rows, int64_t blocks, int64_t per) {
+  const int64_t wgs = std::max<int64_t>(1, pl->units * p->num_heads), target = per <= 16 ? kDecodeTarget : kDecodeTarget / 3;
+  pl->min_blocks = 8;
   pl->splits = std::max<int64_t>(1, std::min((target + wgs - 1) / wgs, blocks / pl->min_blocks));
-  pl->bytes = pl->splits == 1 ? 0 : (size_t)(rows * Hq * pl->splits * (p->head_dim + 2) * 4);
+  pl->bytes = partial_bytes(p, Hq, rows, pl->splits);
+}
+
+// The tiled kernel's partial results are 66 KB a tile and share (d = 128), so the
+// number of shares is weighed, at the numbers that give every CU one, two or three
+// workgroups: the farthest-reaching tile's blocks, one after the other, at what a
+// block takes beside that many workgroups, or all blocks (`steps`) at three; and for
+// more than one share the join's launch and the partial results, written and read.
+void split_tiles(AttnPlan* pl, const kda_kv_pool* p, int32_t Hq, int64_t rows, int64_t blocks, double steps) {
+  const int64_t wgs = std::max<int64_t>(1, pl->units * p->num_heads);
+  pl->min_blocks = 16;
+  const int64_t most = std::max<int64_t>(1, blocks / pl->min_blocks);
+  double best = 0;
+  pl->splits = 0;
+  for (int fill = 0; fill <= 3; ++fill) {
+    const int64_t s = std::max<int64_t>(1, std::min(most, fill * kCUs / wgs));
+    const int64_t beside = std::min<int64_t>(3, (wgs * s + kCUs - 1) / kCUs);
+    double us = std::max((double)((blocks + s - 1) / s) * kStepUs[beside], steps * kStepUs[3] / (3 * kCUs));
+    if (s > 1) us += kJoinUs + 2 * (double)partial_bytes(p, Hq, rows, s) / kPartialRate;
+    if (pl->splits == 0 || us < best) {
+      best = us;
+      pl->splits = s;
+    }
+  }
+  pl->bytes = partial_bytes(p, Hq, rows, pl->splits);
 }
 
 AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens, int32_t max_pages, int32_t window,
@@ -328,8 +363,9 @@ AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens
   pl.decode = rows <= kDecodeRows;
   pl.tile_rows = pl.decode ? kDecodeRows : kTileRows;
   pl.units = (int64_t)n * ((rows + pl.tile_rows - 1) / pl.tile_rows);
-  plan_splits(&pl, p, Hq, (int64_t)n * tokens,
-              reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks), rows);
+  const int64_t blocks = reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks);
+  if (pl.decode) split_decode(&pl, p, Hq, (int64_t)n * tokens, blocks, rows);
+  else split_tiles(&pl, p, Hq, (int64_t)n * tokens, blocks, (double)pl.units * p->num_heads * blocks);
   return pl;
 }
 
@@ -341,12 +377,15 @@ AttnPlan plan_prefill(const kda_kv_pool* p, int32_t Hq, int32_t n, const int64_t
   pl.tile_rows = kTileRows;
   pl.units = 0;
   int64_t blocks = 1;
+  double steps = 0;
   for (int32_t i = 0; i < n; ++i) {
-    const int64_t len = cu[i + 1] - cu[i], s = start ? start[i] : 0;
-    pl.units += (len * G + kTileRows - 1) / kTileRows;
-    blocks = std::max(blocks, reach_blocks(s + len, std::min<int64_t>(len, kTileRows), window, sinks));
+    const int64_t len = cu[i + 1] - cu[i], s = start ? start[i] : 0, tiles = (len * G + kTileRows - 1) / kTileRows;
+    const int64_t first = std::min<int64_t>(len, kTileRows), reach = reach_blocks(s + len, first, window, sinks);
+    pl.units += tiles;
+    blocks = std::max(blocks, reach);
+    steps += 0.5 * tiles * p->num_heads * (reach_blocks(s + (len + tiles - 1) / std::max<int64_t>(1, tiles), first, window, sinks) + reach);
   }
-  plan_splits(&pl, p, Hq, cu[n], blocks, 0);
+  split_tiles(&pl, p, Hq, cu[n], blocks, steps);
   return pl;
 }
 
