@@ -19,15 +19,15 @@
 // like a decode step, and joined by the same kernel.
 //
 // Bound by the matrix and vector units together, and by the power they draw: an
-// 8192-token prompt of 32 heads over 8 (550 GFLOP) takes 584 us over an int8 cache
-// (942 TFLOP/s) and 530 us over a bf16 one (1038); with a cache and queries of
-// zeros, the same instructions take 461 and 385 us.  The largest library products
-// of random bf16 matrices reach 1.31-1.34 PFLOP/s on this part (1.8 of zeros).
-// Of a block's 1100 SIMD cycles the matrix unit has 512, vector instructions 510
-// (bf16) or 680 (int8).  Taken for it: one 32-token block a step and three
-// workgroups a CU, whose waves fill each other's waits (64-token steps, two
-// workgroups a CU: 969 -> 686 us was as far as they came; 256 rows and eight waves
-// in one step 613 us; eight waves in two groups a phase apart 835 us).
+// 8192-token prompt of 32 heads over 8 (550 GFLOP) takes 565 to 586 us over an int8
+// cache, by the card (938 to 973 TFLOP/s), and 517 us over a bf16 one (1064); with a
+// cache and queries of zeros the same instructions take 453 and 374 us.  The largest
+// library products of random bf16 matrices reach 1.31-1.34 PFLOP/s on this part
+// (1.8 of zeros).  Of a block's 1100 SIMD cycles the matrix unit has 512, vector
+// instructions 510 (bf16) or 680 (int8).  Taken for it: one 32-token block a step and
+// three workgroups a CU, whose waves fill each other's waits (int8, when this took 594
+// us: 64-token steps and two workgroups a CU 686; 256 rows and eight waves in one step
+// 613; eight waves in two groups a phase apart 835).
 #include "kda_attn_rows.h"
 
 namespace kda {
@@ -77,7 +77,7 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   BlockScale<EB> scales;
   // lane i: place and factors of block base + i of the chunk.  The scales are read
   // here, 64 blocks at once: read block by block they would be scalar loads, whose wait
-  // is for all LDS reads under way too (8192-token int8 prompt, 32 heads: 604 us, so 584).
+  // is for all LDS reads under way too (8192-token int8 prompt: 604 us, so 584).
   auto look_up = [&](int base) {
     const int i = base + lane;
     if (i < count) {
