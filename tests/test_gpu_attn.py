@@ -508,3 +508,37 @@ def test_bindings_refuse():
             K.make_rope(*bad)
     torch.cuda.synchronize()
     assert torch.equal(before, f.kb.buf)
+
+
+@pytest.mark.parametrize("cache", ["int8", "bf16"])
+def test_pages_past_4_gib(cache):
+    """The same tokens in the first and in the last pages of a pool of 5 GiB: equal bits from prompts
+    (shared among workgroups and not) and decode steps."""
+    H, hq, d, pt, n = 2, 8, 128, 64, 1500
+    dtype = K.KDA_INT8 if cache == "int8" else K.KDA_BF16
+    page = H * K.kda_kv_head_bytes(d, pt, dtype)
+    need = -(-n // pt)
+    pages = (5 << 30) // page
+    buf = torch.zeros(pages * page // 4, dtype=torch.int32, device="cuda")
+    pool = K.make_kv_pool(buf, page, pages, H, d, pt, dtype)
+    near = torch.arange(need, dtype=torch.int32, device="cuda")[None].contiguous()
+    far = pages - 1 - near
+    rng = np.random.default_rng(17)
+    k, v = (to_dev(rng.standard_normal((n, H, d)), "bf16") for _ in range(2))
+    q = queries(rng, n, hq, d, "bf16")
+    got = []
+    for table in (near, far):
+        K.kda_kv_append(pool, None, k, v, None, [0, n], table)
+        for length, window in ((n, 0), (40, 0), (n, 100)):
+            start = n - length
+            w = ws(K.kda_attn_prefill_workspace_bytes(pool, hq, [0, length], start_pos=[start], window=window))
+            o = torch.zeros((length, hq, d), dtype=torch.float32, device="cuda")
+            K.kda_attn_prefill(pool, q[:length], o, [0, length], table, scale=0.1, start_pos=[start], window=window,
+                               workspace=w)
+            got.append(o)
+        o = torch.zeros((2, hq, d), dtype=torch.float32, device="cuda")
+        w = ws(K.kda_attn_decode_workspace_bytes(pool, hq, 1, 2, need))
+        K.kda_attn_decode(pool, q[:2], o, 2, torch.tensor([n - 2], dtype=torch.int32, device="cuda"), table, scale=0.1,
+                          workspace=w)
+        got.append(o)
+    assert all(torch.equal(a, b) and a.abs().sum() > 0 for a, b in zip(got[:4], got[4:]))
