@@ -163,6 +163,9 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
     Frag kf[KS];
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) kf[ks] = *reinterpret_cast<const Frag*>(kb + koff + 512 * ks);
+    // the whole operand asked for before its first product, where its registers are left
+    // (windowed bf16 prompt of 8192: 258 us, so 255; beside int8 codes under way it spills)
+    if constexpr (EB == 2 && NP == 1) __builtin_amdgcn_sched_barrier(0);
     f32x16 x = zero16();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
