@@ -1,9 +1,8 @@
 // kda_attn_device.h -- matrix operands and softmax pieces shared by the
 // attention kernels (kda_attn_decode.hip, kda_attn_tiled.hip).
 //
-// Operand types.  A bf16 cache is multiplied as it is (bf16; the tiled kernel then
-// rounds the weights of bf16 queries to bf16, 2^-9 of each, where a second part
-// would cost half of its second product's time again).  An int8 cache's
+// Operand types.  A bf16 cache is multiplied as it is, in bf16 (the weights in one
+// part or more: see the kernels).  An int8 cache's
 // codes are exact in fp16, and one byte permute and one packed subtraction turn
 // four of them into fp16 (1024 + (code + 128) is the bit pattern 0x64xx), so
 // its products run in fp16, where the weights keep 11 bits instead of 8:

@@ -160,10 +160,11 @@ __device__ __forceinline__ void mask16(f32x16& x, int qp, int blk, int half, int
   }
 }
 
-// The block's weights from its logits, as operands; m, l and the sums acc follow.
-template <int EB, int NP, int DT>
+// The block's weights from its logits, as operands of WP parts; m, l and the sums acc
+// follow.
+template <int EB, int WP, int DT>
 __device__ __forceinline__ void weigh16(const f32x16& x, float qc, const BlockScale<EB>& b, f32x16* acc, float& m, float& l,
-                                        typename AttnOp<EB>::Frag (*pf)[NP]) {
+                                        typename AttnOp<EB>::Frag (*pf)[WP]) {
   const float c = EB == 1 ? fmaxf(qc * b.c, 0x1p-126f) : qc;  // above 0, so that -inf stays -inf
   float mx = kNegInf;
 #pragma unroll
@@ -183,9 +184,9 @@ __device__ __forceinline__ void weigh16(const f32x16& x, float qc, const BlockSc
   float w[16], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) w[e] = exp2_f(__builtin_fmaf(x[e], c, sub));
-  split8<EB, NP>(w, pf[0]);
-  split8<EB, NP>(w + 8, pf[1]);
-  if constexpr (NP == 1) {
+  split8<EB, WP>(w, pf[0]);
+  split8<EB, WP>(w + 8, pf[1]);
+  if constexpr (WP == 1) {
     sum = add8(pf[1][0], add8(pf[0][0], 0.f));
   } else {
 #pragma unroll

@@ -32,28 +32,18 @@
 
 namespace kda {
 
-template <int D, int EB, int NP>
-__global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled_kernel(AttnArgs a) {
+// One tile: rows row0 .. of sequence s (request req) and head h, share sp of what they
+// see.  WP: parts of a weight.
+template <int D, int EB, int NP, int WP>
+__device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, int req, int h, int sp, int row0,
+                                            uint8_t (*lds)[4 * kKvBlock * D]) {
   typedef AttnOp<EB> Op;
   typedef typename Op::Frag Frag;
   constexpr int KS = D / 16, DT = D / 32, ROWS = kTileRows, NT = 256;
   constexpr int PART = 2 * kKvBlock * D;    // bytes of a 16-bit K or V part in LDS
   constexpr int RAW = kKvBlock * D * EB;    // bytes of a part in the cache
-  __shared__ __align__(1024) uint8_t lds[2][2 * PART];  // two blocks: K part | V part
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
-  const int half = lane >> 5, col = lane & 31;
-  // heads fastest: the workgroups of one head share an XCD's L2 where 8 divides the
-  // heads; last tiles first, they see the most
-  const int h = blockIdx.x % a.c.H, rest = blockIdx.x / a.c.H;
-  const int sp = rest % a.splits, unit = a.units - 1 - rest / a.splits;
-  const int req = uni(kv_find_unit(a.b, unit));
-  const KvSeq s = kv_seq_uniform(a.b, req);
-  const int row0 = (unit - s.unit) * ROWS, rows = s.len * a.G;
-  const bool off = s.start < 0, over = (int64_t)s.start + s.len > (int64_t)a.c.max_pages * a.c.page_tokens;
-  if (off || over) {
-    if (sp == 0) store_off(a, s, h, row0, ROWS, D, NT, off);
-    return;
-  }
+  const int half = lane >> 5, col = lane & 31, rows = s.len * a.G;
   const int tp0 = s.start + row0 / a.G, tp1 = s.start + (min(rows, row0 + ROWS) - 1) / a.G;
   const Reach reach = reach_of(tp0, tp1, a.window, a.sinks);
   const Whole tile_sees = whole_of(tp0, tp1, a.window, a.sinks);
@@ -73,7 +63,9 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   // ---- staging: one block a step
   const int per = a.c.page_tokens / kKvBlock, count = ch.end - ch.begin;
   const uint8_t* head0 = a.c.base + h * a.c.head_bytes;
-  int64_t at = 0;  // of lane i's block in the head; negative: a bad page or scale
+  // lane i's block, in units of 256 bytes from the head's first page on (all sizes are
+  // multiples of them); ~0: a bad page or scale
+  uint32_t at = 0;
   BlockScale<EB> scales;
   // lane i: place and factors of block base + i of the chunk.  The scales are read
   // here, 64 blocks at once: read block by block they would be scalar loads, whose wait
@@ -84,13 +76,13 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
       const int blk = reach.block(ch.begin + i);
       const int j = blk / per, in = blk - j * per, pg = a.c.table[(int64_t)req * a.c.max_pages + j];
       bool bad = pg < 0 || pg >= a.c.num_pages;
-      at = (bad ? 0 : pg) * a.c.page_bytes;
+      const int64_t page = (bad ? 0 : pg) * a.c.page_bytes;
       if constexpr (EB == 1) {
-        const float2 sc = *reinterpret_cast<const float2*>(head0 + at + (int64_t)per * (2 * RAW) + 8 * in);
+        const float2 sc = *reinterpret_cast<const float2*>(head0 + page + (int64_t)per * (2 * RAW) + 8 * in);
         scales.set(sc.x, sc.y, bad);
         bad = scales.bad;
       }
-      at = bad ? -1 : at + (int64_t)in * (2 * RAW);
+      at = bad ? ~0u : (uint32_t)((page + (int64_t)in * (2 * RAW)) >> 8);
     }
   };
   constexpr int UNITS = 2 * RAW / 16 / NT;  // 16-byte units of a raw block a thread moves
@@ -99,9 +91,9 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   int nbad = 0;
   const uint32_t lds0 = uni((uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint8_t*)&lds[0][0]);
   auto fetch = [&](int i, int buf) {  // block i of the chunk
-    const int lo = __builtin_amdgcn_readlane((int)at, i & 63), hi = __builtin_amdgcn_readlane((int)(at >> 32), i & 63);
-    nbad = hi < 0;  // a bad page or scale: page 0's bytes, whose values never count
-    const uint8_t* src = head0 + (nbad ? 0 : (int64_t)((uint64_t)(uint32_t)hi << 32 | (uint32_t)lo));
+    const uint32_t to = __builtin_amdgcn_readlane(at, i & 63);
+    nbad = to == ~0u;  // a bad page or scale: page 0's bytes, whose values never count
+    const uint8_t* src = head0 + ((uint64_t)(nbad ? 0 : to) << 8);
     if constexpr (EB == 2) {
       constexpr int WAVE = 1024 * UNITS;  // bytes a wave moves
       to_lds<UNITS>(src + wv * WAVE, lds0 + buf * (2 * PART) + wv * WAVE, 16 * lane);
@@ -162,25 +154,27 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   auto step = [&](const uint8_t* kb, int blk, bool full, const BlockScale<EB>& bs) __attribute__((always_inline)) {
     Frag kf[KS];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) kf[ks] = *reinterpret_cast<const Frag*>(kb + koff + 512 * ks);
-    // the whole operand asked for before its first product, where its registers are left
-    // (windowed bf16 prompt of 8192: 258 us, so 255; beside int8 codes under way it spills)
-    if constexpr (EB == 2 && NP == 1) __builtin_amdgcn_sched_barrier(0);
+    for (int ks = 0; ks < KS; ++ks) {
+      kf[ks] = *reinterpret_cast<const Frag*>(kb + koff + 512 * ks);
+      // most of the operand asked for before its first product, as the registers allow
+      // (beside int8 codes under way they do not)
+      if (EB == 2 && WP == 1 && ks == KS * 7 / 8 - 1) __builtin_amdgcn_sched_barrier(0);
+    }
     f32x16 x = zero16();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
       for (int p = 0; p < NP; ++p) x = Op::mma32(kf[ks], qf[ks][p], x);
     if (!full) mask16(x, wr.qp, blk, half, a.window, a.sinks, bs.bad);
-    Frag pf[2][NP];
-    weigh16<EB, NP, DT>(x, qc, bs, acc, m, l, pf);
+    Frag pf[2][WP];
+    weigh16<EB, WP, DT>(x, qc, bs, acc, m, l, pf);
     Frag vf[2 * DT];
 #pragma unroll
     for (int i = 0; i < 2 * DT; ++i) vf[i] = *reinterpret_cast<const Frag*>(kb + voff + (i % DT) * 2048 + (i / DT) * 512);
 #pragma unroll
     for (int i = 0; i < 2 * DT; ++i)
 #pragma unroll
-      for (int p = 0; p < NP; ++p) acc[i % DT] = Op::mma32(vf[i], pf[i / DT][p], acc[i % DT]);
+      for (int p = 0; p < WP; ++p) acc[i % DT] = Op::mma32(vf[i], pf[i / DT][p], acc[i % DT]);
   };
 
   // the queries are waited for here: the loop must not wait for a load of theirs, with
@@ -207,7 +201,41 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   }
 
   const float ll = half_sum(l);
-  if (wr.live) store_row<DT>(a, wr.out, sp, ch.used, half, acc, m, ll);
+  int c = threadIdx.x & 31;
+  asm volatile("" : "+v"(c));  // where the row goes is worked out again: kept, it would cost the loop registers
+  const WaveRows to = wave_rows(a, s, h, row0 + 32 * wv, c, D);
+  if (to.live) store_row<DT>(a, to.out, sp, ch.used, half, acc, m, ll);
+}
+
+template <int D, int EB, int NP>
+__global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled_kernel(AttnArgs a) {
+  __shared__ __align__(1024) uint8_t lds[2][4 * kKvBlock * D];  // two blocks: K part | V part, 16 bits
+  // heads fastest: the workgroups of one head share an XCD's L2 where 8 divides the
+  // heads; last tiles first, they see the most
+  const int h = blockIdx.x % a.c.H, rest = blockIdx.x / a.c.H;
+  const int sp = rest % a.splits, unit = a.units - 1 - rest / a.splits;
+  const int req = uni(kv_find_unit(a.b, unit));
+  const KvSeq s = kv_seq_uniform(a.b, req);
+  const int row0 = (unit - s.unit) * kTileRows;
+  const bool off = s.start < 0, over = (int64_t)s.start + s.len > (int64_t)a.c.max_pages * a.c.page_tokens;
+  if (off || over) {
+    if (sp == 0) store_off(a, s, h, row0, kTileRows, D, 256, off);
+    return;
+  }
+  // Beside a bf16 cache the weights of bf16 queries are rounded to bf16, 2^-9 of each: an
+  // error of the result of 1.3 to 1.4 times the output's own rounding over many rows, up
+  // to 1.55 times over few.  Sequences of few rows, which leave half of a tile's waves
+  // without any, have a second part instead (error 1.00; 256 sequences of 8 tokens and 4
+  // heads over 1000: 207 us with either, 64 of 16 tokens over 2000: 102 us, so 123).  For
+  // a long prompt it would be half of all products again (247 us, 333).  By the sequence:
+  // a row's bits do not depend on the rest of the call.
+  if constexpr (EB == 2 && NP == 1) {
+    if (s.len * a.G <= kFewRows) {
+      attend_tile<D, EB, NP, 2>(a, s, req, h, sp, row0, lds);
+      return;
+    }
+  }
+  attend_tile<D, EB, NP, NP>(a, s, req, h, sp, row0, lds);
 }
 
 template <int D, int EB, int NP> static void launch_t(const AttnArgs& a, hipStream_t st) {

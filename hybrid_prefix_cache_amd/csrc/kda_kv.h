@@ -88,6 +88,7 @@ struct AttnArgs {
 static_assert(sizeof(AttnArgs) <= 4096, "kernel argument budget");
 
 constexpr int kTileRows = 128;   // rows of a tile of the tiled kernel
+constexpr int kFewRows = 64;     // rows of a sequence and head that are few to it
 // Rows per request and key/value head the decode kernel takes.  Beyond, column
 // tiles in one wave cost the second workgroup of a CU: 24 requests of 35 rows over
 // 5000 tokens took 57 us there, 39 us in 128-row tiles; 64 of 20 rows 80 against 102.
