@@ -61,7 +61,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
   for (int d = 0; d < DT; ++d) acc[d] = zero16();
 
   // ---- staging: one block a step
-  const int per = a.c.page_tokens / kKvBlock, count = ch.end - ch.begin;
+  const int count = ch.end - ch.begin;
   const uint8_t* head0 = a.c.base + h * a.c.head_bytes;
   // lane i's block, in units of 256 bytes from the head's first page on (all sizes are
   // multiples of them); ~0: a bad page or scale
@@ -71,14 +71,19 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
   // here, 64 blocks at once: read block by block they would be scalar loads, whose wait
   // is for all LDS reads under way too (8192-token int8 prompt: 604 us, so 584).
   auto look_up = [&](int base) {
+    int per = a.c.page_tokens / kKvBlock, r = req;
+    int64_t page_bytes = a.c.page_bytes;
+    const uint8_t* head = head0;
+    // kept from being prepared outside the loop, in twelve of the loop's registers
+    asm volatile("" : "+s"(per), "+s"(r), "+s"(page_bytes), "+s"(head));
     const int i = base + lane;
     if (i < count) {
       const int blk = reach.block(ch.begin + i);
-      const int j = blk / per, in = blk - j * per, pg = a.c.table[(int64_t)req * a.c.max_pages + j];
+      const int j = blk / per, in = blk - j * per, pg = a.c.table[(int64_t)r * a.c.max_pages + j];
       bool bad = pg < 0 || pg >= a.c.num_pages;
-      const int64_t page = (bad ? 0 : pg) * a.c.page_bytes;
+      const int64_t page = (bad ? 0 : pg) * page_bytes;
       if constexpr (EB == 1) {
-        const float2 sc = *reinterpret_cast<const float2*>(head0 + page + (int64_t)per * (2 * RAW) + 8 * in);
+        const float2 sc = *reinterpret_cast<const float2*>(head + page + (int64_t)per * (2 * RAW) + 8 * in);
         scales.set(sc.x, sc.y, bad);
         bad = scales.bad;
       }
@@ -154,12 +159,10 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
   auto step = [&](const uint8_t* kb, int blk, bool full, const BlockScale<EB>& bs) __attribute__((always_inline)) {
     Frag kf[KS];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      kf[ks] = *reinterpret_cast<const Frag*>(kb + koff + 512 * ks);
-      // most of the operand asked for before its first product, as the registers allow
-      // (beside int8 codes under way they do not)
-      if (EB == 2 && WP == 1 && ks == KS * 7 / 8 - 1) __builtin_amdgcn_sched_barrier(0);
-    }
+    for (int ks = 0; ks < KS; ++ks) kf[ks] = *reinterpret_cast<const Frag*>(kb + koff + 512 * ks);
+    // the whole operand asked for before its first product, where its registers are left
+    // (windowed bf16 prompt of 8192: 258 us, so 255; beside int8 codes under way they are not)
+    if constexpr (EB == 2 && WP == 1) __builtin_amdgcn_sched_barrier(0);
     f32x16 x = zero16();
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks)
