@@ -19,8 +19,8 @@
 // like a decode step, and joined by the same kernel.
 //
 // Bound by the matrix and vector units together, and by the power they draw: an
-// 8192-token prompt of 32 heads over 8 (550 GFLOP) takes 565 to 586 us over an int8
-// cache, by the card (938 to 973 TFLOP/s), and 517 us over a bf16 one (1064); with a
+// 8192-token prompt of 32 heads over 8 (550 GFLOP) takes 563 to 589 us over an int8
+// cache, by the card (933 to 977 TFLOP/s), and 517 us over a bf16 one (1064); with a
 // cache and queries of zeros the same instructions take 453 and 374 us.  The largest
 // library products of random bf16 matrices reach 1.31-1.34 PFLOP/s on this part
 // (1.8 of zeros).  Of a block's 1100 SIMD cycles the matrix unit has 512, vector
