@@ -200,14 +200,13 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       fetch(i + 1, nxt, nxt_pg);
     }
     const int blk = reach.block(first + 4 * i);
-    const bool bad = cur_pg < 0, full = !bad && whole.has(blk);
-    float ks = 1.f, lv = 0.f, iv = 1.f;
-    if (EB == 1 && !bad) {
-      ks = cur.ks;
-      const float vs = cur.vs == 0.f ? 1.f : cur.vs < 0x1p-120f ? 0x1p-120f : cur.vs;
-      lv = __builtin_amdgcn_logf(vs);
-      iv = 1.f / vs;
+    BlockScale<EB> bs;  // from one lane's scales: the whole wave's decision
+    if constexpr (EB == 1) {
+      bs.set(__uint_as_float(uni(__float_as_uint(cur.ks))), __uint_as_float(uni(__float_as_uint(cur.vs))), cur_pg < 0);
+    } else {
+      bs.bad = cur_pg < 0;
     }
+    const bool full = !bs.bad && whole.has(blk);
     f32x4 s[MT][2];
 #pragma unroll
     for (int kt = 0; kt < 2; ++kt) {
@@ -232,16 +231,16 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     bf16x8 seen[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const float c = qc[mt] * ks;
+      const float c = qc[mt] * bs.c;
       float x[8], mx = kNegInf;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(s[mt][e >> 2][e & 3], c, lv);
+      for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(s[mt][e >> 2][e & 3], c, bs.lv);
       if (!full) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int64_t j = (int64_t)blk * kKvBlock + 16 * (e >> 2) + 4 * g + (e & 3);
           const bool see = sees(qp[mt], j, a.window, a.sinks);
-          x[e] = !see ? kNegInf : bad ? __builtin_nanf("") : x[e];
+          x[e] = !see ? kNegInf : bs.bad ? __builtin_nanf("") : x[e];
           seen[mt][e] = static_cast<__bf16>(see ? 1.f : 0.f);
         }
       }
@@ -263,7 +262,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
         x[e] = exp2_f(x[e] - mu);
         sum += x[e];
       }
-      if (EB == 1) l[mt] += sum == 0.f ? 0.f : sum * iv;  // a block of which the row sees nothing adds nothing
+      if (EB == 1) l[mt] += sum * bs.iv;
       else l[mt] += sum;
       split8<EB, WP>(x, pf[mt]);
     }

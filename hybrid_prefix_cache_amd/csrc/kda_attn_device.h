@@ -106,6 +106,35 @@ __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f
 // exp2(x - m) where m may be -inf (nothing seen yet): the weight of what has been summed so far.
 __device__ __forceinline__ float decay(float m, float mn) { return m == kNegInf ? 0.f : exp2_f(m - mn); }
 
+// A block's factors.  A scale that is not finite makes its block `bad`: NaN to every
+// row that sees it, nothing to the others.
+template <int EB> struct BlockScale {
+  float c = 1.f, lv = 0.f, iv = 1.f;  // logit factor, log2 of the value scale and its inverse
+  bool bad = false;
+  __device__ __forceinline__ void set(float ks, float vs, bool bad_page) {
+    bad = bad_page;
+    if constexpr (EB == 1) {
+      bad = bad || !(ks < __builtin_inff() && vs < __builtin_inff());
+      if (bad) ks = vs = 1.f;
+      vs = vs == 0.f ? 1.f : vs < 0x1p-120f ? 0x1p-120f : vs;
+      c = ks;
+      lv = __builtin_amdgcn_logf(vs);
+      iv = __builtin_amdgcn_rcpf(vs);
+    }
+  }
+  // Lane i's factors, to the whole wave.
+  __device__ __forceinline__ BlockScale of_lane(int i, bool is_bad) const {
+    BlockScale b;
+    b.bad = is_bad;
+    if constexpr (EB == 1) {
+      b.c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(c), i));
+      b.lv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv), i));
+      b.iv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(iv), i));
+    }
+    return b;
+  }
+};
+
 // The power of two that brings amax to [2^7, 2^8), and its inverse.
 __device__ __forceinline__ float fit_f16(float amax, float* inverse) {
   int e = __builtin_amdgcn_frexp_expf(amax);  // amax in [2^(e-1), 2^e); 0 for 0, inf and NaN

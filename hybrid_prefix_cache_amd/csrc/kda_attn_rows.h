@@ -122,35 +122,6 @@ __device__ __forceinline__ float load_queries(const AttnArgs& a, int64_t at, typ
   }
 }
 
-// A block's factors.  A scale that is not finite makes its block `bad`: NaN to every
-// row that sees it, nothing to the others.
-template <int EB> struct BlockScale {
-  float c = 1.f, lv = 0.f, iv = 1.f;  // logit factor, log2 of the value scale and its inverse
-  bool bad = false;
-  __device__ __forceinline__ void set(float ks, float vs, bool bad_page) {
-    bad = bad_page;
-    if constexpr (EB == 1) {
-      bad = bad || !(ks < __builtin_inff() && vs < __builtin_inff());
-      if (bad) ks = vs = 1.f;
-      vs = vs == 0.f ? 1.f : vs < 0x1p-120f ? 0x1p-120f : vs;
-      c = ks;
-      lv = __builtin_amdgcn_logf(vs);
-      iv = __builtin_amdgcn_rcpf(vs);
-    }
-  }
-  // Lane i's factors, to the whole wave.
-  __device__ __forceinline__ BlockScale of_lane(int i, bool is_bad) const {
-    BlockScale b;
-    b.bad = is_bad;
-    if constexpr (EB == 1) {
-      b.c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(c), i));
-      b.lv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv), i));
-      b.iv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(iv), i));
-    }
-    return b;
-  }
-};
-
 // Logits a row does not see to -inf; those it sees of a bad block to NaN.
 __device__ __forceinline__ void mask16(f32x16& x, int qp, int blk, int half, int window, int sinks, bool bad) {
 #pragma unroll
