@@ -6,7 +6,7 @@
 // are one or two column tiles of the matrix products, so every cached byte is
 // read once for all of them.  The step is a stream over the cache.
 //
-// Per 32-token block: S^T = K Q^T (keys as rows), one running maximum and sum per
+// Per 32-token block: S^T = K Q^T (keys as rows), running references and sum per
 // row, O^T += V^T P^T.  With keys as rows a lane's eight weights are one row's at
 // tokens {4g + r, 16 + 4g + r}, which is the order of the tokens in the cache's V
 // part: P^T needs no exchange between lanes, and K and V units go from memory to
@@ -89,7 +89,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   // stream over the cache (165.8 us with either).
   constexpr int WP = EB == 2 && NP == 1 ? 2 : NP;
   __shared__ float sh_o[4][16][LD];
-  __shared__ float sh_m[4][MT * 16], sh_l[4][MT * 16];
+  __shared__ float sh_m[4][MT * 16], sh_n[4][MT * 16], sh_l[4][MT * 16];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, col = lane & 15;
   const int item = blockIdx.x % (a.b.n * a.c.H), sp = blockIdx.x / (a.b.n * a.c.H);
@@ -159,10 +159,10 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   }
 
   f32x4 acc[MT][DT];
-  float m[MT], l[MT];
+  float m[MT], n[MT], l[MT];  // references of acc and (int8) of l
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
-    m[mt] = kNegInf;
+    m[mt] = n[mt] = kNegInf;
     l[mt] = 0.f;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt) acc[mt][dt] = zero4();
@@ -234,7 +234,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       const float c = qc[mt] * bs.c;
       float x[8], mx = kNegInf;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = __builtin_fmaf(s[mt][e >> 2][e & 3], c, bs.lv);
+      for (int e = 0; e < 8; ++e) x[e] = s[mt][e >> 2][e & 3] * c;
       if (!full) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -246,25 +246,32 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) mx = fmaxf(mx, x[e]);
-      mx = group_max(mx);
-      const bool grow = mx > m[mt] + kSlack;
-      if (__any(grow)) {
+      const float nx = group_max(mx);
+      mx = nx + bs.lv;
+      const bool grow = mx > m[mt] + kSlack, ngrow = EB == 1 && nx > n[mt] + kSlack;
+      if (__any(grow || ngrow)) {
         const float mn = grow ? mx : m[mt], al = grow ? decay(m[mt], mn) : 1.f;
         m[mt] = mn;
-        l[mt] *= al;
+        if constexpr (EB == 1) {
+          const float nn = ngrow ? nx : n[mt];
+          l[mt] *= ngrow ? decay(n[mt], nn) : 1.f;
+          n[mt] = nn;
+        } else {
+          l[mt] *= al;
+        }
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) acc[mt][dt] *= al;
       }
-      const float mu = (m[mt] == kNegInf ? 0.f : m[mt]) - Op::kLift;
-      float sum = 0.f;
+      const float sub = bs.lv + Op::kLift - (m[mt] == kNegInf ? 0.f : m[mt]);
+      const float to_n = EB == 1 ? to_normaliser<8>(x, 1.f, sub, n[mt], l[mt]) : 1.f;
+      float w[8], sum = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        x[e] = exp2_f(x[e] - mu);
-        sum += x[e];
+        w[e] = exp2_f(x[e] + sub);
+        sum += w[e];
       }
-      if (EB == 1) l[mt] += sum * bs.iv;
-      else l[mt] += sum;
-      split8<EB, WP>(x, pf[mt]);
+      l[mt] = __builtin_fmaf(sum, to_n, l[mt]);
+      split8<EB, WP>(w, pf[mt]);
     }
     if constexpr (EB == 2) {
       if (!full) {
@@ -308,8 +315,10 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 #pragma unroll
   for (int mt = 0; mt < MT; ++mt) {
     l[mt] = group_sum(l[mt]);
+    m[mt] -= Op::kLift;  // what acc is in units of
     if (g == 0) {
       sh_m[wv][16 * mt + col] = m[mt];
+      sh_n[wv][16 * mt + col] = EB == 1 ? n[mt] : m[mt];
       sh_l[wv][16 * mt + col] = l[mt];
     }
   }
@@ -328,18 +337,19 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       const int row = i / (D / 4), d = 4 * (i % (D / 4)), rr = 16 * mt + row;
       if (rr >= M) continue;
       f32x4 y = zero4();
-      float mm = kNegInf, ll = 0.f;
+      float mm = kNegInf, nm = kNegInf, ll = 0.f;
 #pragma unroll
       for (int w = 0; w < 4; ++w) {
         y += *reinterpret_cast<const f32x4*>(&sh_o[w][row][d]);
         mm = fmaxf(mm, sh_m[w][rr]);
+        nm = fmaxf(nm, sh_n[w][rr]);
       }
 #pragma unroll
-      for (int w = 0; w < 4; ++w) ll += sh_l[w][rr] * decay(sh_m[w][rr], mm);
+      for (int w = 0; w < 4; ++w) ll += sh_l[w][rr] * decay(sh_n[w][rr], nm);
       const int64_t at = (int64_t)(req * a.b.tokens + rr / a.G) * a.Hq + h * a.G + rr % a.G;
       if (ch.used == 1) {
         // ll is 0 only where nothing was seen, and every row sees itself
-        const float inv = 1.f / ll;
+        const float inv = decay(mm, nm) / ll;
         if (a.out_bf16)
           *reinterpret_cast<u16x4*>(reinterpret_cast<uint16_t*>(a.o) + at * D + d) =
               pack_bf16x4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
@@ -348,8 +358,10 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       } else {
         *reinterpret_cast<f32x4*>(a.part_o + (at * a.splits + sp) * D + d) = y;
         if (d == 0) {
-          a.part_ml[2 * (at * a.splits + sp)] = mm;
-          a.part_ml[2 * (at * a.splits + sp) + 1] = ll;
+          float* to = a.part_mnl + 3 * (at * a.splits + sp);
+          to[0] = mm;
+          to[1] = nm;
+          to[2] = ll;
         }
       }
     }
@@ -372,17 +384,23 @@ template <int D, int W> __global__ __launch_bounds__(256) void attn_join_kernel(
   const Reach reach = reach_of(sq.start + t0 / a.G, sq.start + (t1 - 1) / a.G, a.window, a.sinks);
   const int used = chunk_of(reach.count(), a.splits, a.min_blocks, 0).used;
   if (used == 1) return;
-  const float* ml = a.part_ml + 2 * at * a.splits;
+  const float* mnl = a.part_mnl + 3 * at * a.splits;
   const float* po = a.part_o + at * a.splits * D + C * lane;
-  float mm = kNegInf;
-  for (int s = lane; s < used; s += 64) mm = fmaxf(mm, ml[2 * s]);
+  float mm = kNegInf, nm = kNegInf;
+  for (int s = lane; s < used; s += 64) {
+    mm = fmaxf(mm, mnl[3 * s]);
+    nm = fmaxf(nm, mnl[3 * s + 1]);
+  }
 #pragma unroll
-  for (int x = 1; x < 64; x <<= 1) mm = fmaxf(mm, __shfl_xor(mm, x));
+  for (int x = 1; x < 64; x <<= 1) {
+    mm = fmaxf(mm, __shfl_xor(mm, x));
+    nm = fmaxf(nm, __shfl_xor(nm, x));
+  }
   float ll = 0.f, y[C] = {};
 #pragma unroll 8
   for (int s = part; s < used; s += W) {
-    const float w = decay(ml[2 * s], mm);
-    ll += w * ml[2 * s + 1];
+    const float w = decay(mnl[3 * s], mm);
+    ll += decay(mnl[3 * s + 1], nm) * mnl[3 * s + 2];
 #pragma unroll
     for (int i = 0; i < C; ++i) y[i] += w * po[(int64_t)s * D + i];
   }
@@ -402,7 +420,7 @@ template <int D, int W> __global__ __launch_bounds__(256) void attn_join_kernel(
       for (int i = 0; i < C; ++i) y[i] += sh[v][C * lane + i];
     }
   }
-  const float inv = 1.f / ll;
+  const float inv = decay(mm, nm) / ll;
 #pragma unroll
   for (int i = 0; i < C; ++i) {
     const int64_t o = at * D + C * lane + i;

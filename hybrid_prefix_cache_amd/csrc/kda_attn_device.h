@@ -8,12 +8,14 @@
 // its products run in fp16, where the weights keep 11 bits instead of 8:
 //   - q rows are brought to [2^7, 2^8) by a power of two, undone in the logit's
 //     factor, so that no bf16 or fp32 q leaves fp16's range;
-//   - the block's value scale goes into the weight, w' = exp2(x + log2 vs - m'),
-//     m' the running reference of x + log2 vs, so that w' is bounded whatever the
-//     scales; the normaliser sums w' / vs.  w' carries a factor 2^6, which with
-//     the slack below stays in fp16's range and leaves 30 binary orders of
-//     weights above its smallest number.
-// The reference is the running maximum, or up to 2^kSlack below it: the sums are
+//   - the block's value scale goes into the weight, w' = exp2(x + log2 vs - m),
+//     m the running reference of x + log2 vs, so that w' is bounded whatever the
+//     scales.  w' carries a factor 2^6, which with the slack below stays in fp16's
+//     range and leaves 30 binary orders of weights above its smallest number.
+//   - the normaliser has a reference of its own, n of the plain logits x, and is summed
+//     in fp32: a block of small values has small weights w', which may all round to 0,
+//     and its full share of the softmax.
+// A reference is the running maximum, or up to 2^kSlack below it: the sums are
 // rescaled only where a row's maximum passes its reference by more.
 // fp32 queries (and their weights) are split into parts that add up to 22 bits
 // (two fp16) or 24 (three bf16), one product each: the cached operand is exact
@@ -109,7 +111,7 @@ __device__ __forceinline__ float decay(float m, float mn) { return m == kNegInf 
 // A block's factors.  A scale that is not finite makes its block `bad`: NaN to every
 // row that sees it, nothing to the others.
 template <int EB> struct BlockScale {
-  float c = 1.f, lv = 0.f, iv = 1.f;  // logit factor, log2 of the value scale and its inverse
+  float c = 1.f, lv = 0.f;  // logit factor, log2 of the value scale
   bool bad = false;
   __device__ __forceinline__ void set(float ks, float vs, bool bad_page) {
     bad = bad_page;
@@ -119,7 +121,6 @@ template <int EB> struct BlockScale {
       vs = vs == 0.f ? 1.f : vs < 0x1p-120f ? 0x1p-120f : vs;
       c = ks;
       lv = __builtin_amdgcn_logf(vs);
-      iv = __builtin_amdgcn_rcpf(vs);
     }
   }
   // Lane i's factors, to the whole wave.
@@ -129,11 +130,27 @@ template <int EB> struct BlockScale {
     if constexpr (EB == 1) {
       b.c = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(c), i));
       b.lv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(lv), i));
-      b.iv = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(iv), i));
     }
     return b;
   }
 };
+
+// The factor that brings the sum of a block's weights, exp2(x_i c + sub), to the
+// normaliser's reference n.  Where the value scale is so small that the weights may have
+// left fp32's range, l receives the block's exp2(x_i c - n) here, and the factor is 0.
+// Row by row, so that a row's bits do not depend on its neighbours'.
+constexpr float kFar = 60.f;
+template <int N, typename X> __device__ __forceinline__ float to_normaliser(const X& x, float c, float sub, float n, float& l) {
+  const float ref = n == kNegInf ? 0.f : n, e = -(sub + ref);
+  const bool far = e > kFar;
+  if (__any(far)) {
+    float sum = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum += exp2_f(__builtin_fmaf(x[i], c, -ref));
+    l += far ? sum : 0.f;
+  }
+  return far ? 0.f : exp2_f(e);
+}
 
 // The power of two that brings amax to [2^7, 2^8), and its inverse.
 __device__ __forceinline__ float fit_f16(float amax, float* inverse) {

@@ -49,12 +49,6 @@ template <int N> __device__ __forceinline__ void to_lds(const uint8_t* src, uint
 }
 
 // Sum of an operand's eight weights, added to l.
-__device__ __forceinline__ float add8(f16x8 w, float l) {
-  const f16x2 one = {(_Float16)1.f, (_Float16)1.f};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) l = __builtin_amdgcn_fdot2(f16x2{w[2 * i], w[2 * i + 1]}, one, l, false);
-  return l;
-}
 __device__ __forceinline__ float add8(bf16x8 w, float l) {
   const bf16x2_t one = {static_cast<__bf16>(1.f), static_cast<__bf16>(1.f)};
 #pragma unroll
@@ -131,46 +125,54 @@ __device__ __forceinline__ void mask16(f32x16& x, int qp, int blk, int half, int
   }
 }
 
-// The block's weights from its logits, as operands of WP parts; m, l and the sums acc
-// follow.
+// The block's weights from its logits, as operands of WP parts; the references m and n
+// (of the weights and, int8, of the normaliser), l and the sums acc follow.
 template <int EB, int WP, int DT>
-__device__ __forceinline__ void weigh16(const f32x16& x, float qc, const BlockScale<EB>& b, f32x16* acc, float& m, float& l,
-                                        typename AttnOp<EB>::Frag (*pf)[WP]) {
+__device__ __forceinline__ void weigh16(const f32x16& x, float qc, const BlockScale<EB>& b, f32x16* acc, float& m, float& n,
+                                        float& l, typename AttnOp<EB>::Frag (*pf)[WP]) {
   const float c = EB == 1 ? fmaxf(qc * b.c, 0x1p-126f) : qc;  // above 0, so that -inf stays -inf
-  float mx = kNegInf;
+  float top = kNegInf;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) mx = fmaxf(mx, x[e]);
-  mx = __builtin_fmaf(half_max(mx), c, b.lv);
-  // the reference of the weights follows the maximum once it is kSlack behind, row by
-  // row, so that a row's bits do not depend on its neighbours'
-  const bool grow = mx > m + kSlack;
-  if (__any(grow)) {
+  for (int e = 0; e < 16; ++e) top = fmaxf(top, x[e]);
+  top = half_max(top);
+  const float mx = __builtin_fmaf(top, c, b.lv), nx = top * c;
+  // a reference follows its maximum once it is kSlack behind, row by row, so that a
+  // row's bits do not depend on its neighbours'
+  const bool grow = mx > m + kSlack, ngrow = EB == 1 && nx > n + kSlack;
+  if (__any(grow || ngrow)) {
     const float mn = grow ? mx : m, al = grow ? decay(m, mn) : 1.f;
     m = mn;
-    l *= al;
+    if constexpr (EB == 1) {
+      const float nn = ngrow ? nx : n;
+      l *= ngrow ? decay(n, nn) : 1.f;
+      n = nn;
+    } else {
+      l *= al;
+    }
 #pragma unroll
     for (int d = 0; d < DT; ++d) acc[d] *= al;
   }
   const float sub = b.lv + AttnOp<EB>::kLift - (m == kNegInf ? 0.f : m);
+  const float to_n = EB == 1 ? to_normaliser<16>(x, c, sub, n, l) : 1.f;
   float w[16], sum = 0.f;
 #pragma unroll
   for (int e = 0; e < 16; ++e) w[e] = exp2_f(__builtin_fmaf(x[e], c, sub));
   split8<EB, WP>(w, pf[0]);
   split8<EB, WP>(w + 8, pf[1]);
-  if constexpr (WP == 1) {
-    sum = add8(pf[1][0], add8(pf[0][0], 0.f));
+  if constexpr (EB == 2 && WP == 1) {
+    sum = add8(pf[1][0], add8(pf[0][0], 0.f));  // the rounded weights, whose range is fp32's
   } else {
 #pragma unroll
     for (int e = 0; e < 16; ++e) sum += w[e];
   }
-  l = __builtin_fmaf(sum, b.iv, l);
+  l = __builtin_fmaf(sum, to_n, l);
 }
 
 // The lane's row of a finished tile (or of its split) to o (or the partial results).
 template <int DT> __device__ __forceinline__ void store_row(const AttnArgs& a, int64_t out, int sp, int used, int half,
-                                                             const f32x16* acc, float m, float ll) {
+                                                             const f32x16* acc, float m, float n, float ll) {
   constexpr int D = 32 * DT;
-  const float inv = used == 1 ? 1.f / ll : 1.f;
+  const float inv = used == 1 ? decay(m, n) / ll : 1.f;
   float* po = a.part_o + (out * a.splits + sp) * D;
 #pragma unroll
   for (int d = 0; d < DT; ++d)
@@ -183,8 +185,10 @@ template <int DT> __device__ __forceinline__ void store_row(const AttnArgs& a, i
       else *reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.o) + out * D + ch) = y;
     }
   if (used > 1 && half == 0) {
-    a.part_ml[2 * (out * a.splits + sp)] = m;
-    a.part_ml[2 * (out * a.splits + sp) + 1] = ll;
+    float* to = a.part_mnl + 3 * (out * a.splits + sp);
+    to[0] = m;
+    to[1] = n;
+    to[2] = ll;
   }
 }
 

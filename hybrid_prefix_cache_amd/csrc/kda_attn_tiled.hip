@@ -56,7 +56,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
   const float qc = load_queries<D, EB, NP>(a, wr.q + 8 * half, qf);
 
   f32x16 acc[DT];
-  float m = kNegInf, l = 0.f;
+  float m = kNegInf, n = kNegInf, l = 0.f;
 #pragma unroll
   for (int d = 0; d < DT; ++d) acc[d] = zero16();
 
@@ -170,7 +170,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
       for (int p = 0; p < NP; ++p) x = Op::mma32(kf[ks], qf[ks][p], x);
     if (!full) mask16(x, wr.qp, blk, half, a.window, a.sinks, bs.bad);
     Frag pf[2][WP];
-    weigh16<EB, WP, DT>(x, qc, bs, acc, m, l, pf);
+    weigh16<EB, WP, DT>(x, qc, bs, acc, m, n, l, pf);
     Frag vf[2 * DT];
 #pragma unroll
     for (int i = 0; i < 2 * DT; ++i) vf[i] = *reinterpret_cast<const Frag*>(kb + voff + (i % DT) * 2048 + (i / DT) * 512);
@@ -207,7 +207,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
   int c = threadIdx.x & 31;
   asm volatile("" : "+v"(c));  // where the row goes is worked out again: kept, it would cost the loop registers
   const WaveRows to = wave_rows(a, s, h, row0 + 32 * wv, c, D);
-  if (to.live) store_row<DT>(a, to.out, sp, ch.used, half, acc, m, ll);
+  if (to.live) store_row<DT>(a, to.out, sp, ch.used, half, acc, m - Op::kLift, EB == 1 ? n : m, ll);
 }
 
 template <int D, int EB, int NP>

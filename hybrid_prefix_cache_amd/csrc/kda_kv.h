@@ -75,7 +75,7 @@ struct AttnArgs {
   const void* q;
   void* o;
   float* part_o;   // [rows][Hq][splits][D]
-  float* part_ml;  // [rows][Hq][splits][2]: running maximum and sum
+  float* part_mnl;  // [rows][Hq][splits][3]: references (log2) of part_o and of the sum, the sum
   int64_t q_ld;
   int32_t Hq, G;
   float scale_log2;

@@ -320,7 +320,7 @@ int64_t reach_blocks(int64_t end, int64_t len, int32_t window, int32_t sinks) {
 }
 
 size_t partial_bytes(const kda_kv_pool* p, int32_t Hq, int64_t rows, int64_t splits) {
-  return splits == 1 ? 0 : (size_t)(rows * Hq * splits * (p->head_dim + 2) * 4);
+  return splits == 1 ? 0 : (size_t)(rows * Hq * splits * (p->head_dim + 3) * 4);
 }
 
 // The decode kernel: its partial results are small beside the cache it reads, so the
@@ -332,7 +332,7 @@ void split_decode(AttnPlan* pl, const kda_kv_pool* p, int32_t Hq, int64_t rows, 
   pl->bytes = partial_bytes(p, Hq, rows, pl->splits);
 }
 
-// The tiled kernel's partial results are 66 KB a tile and share (d = 128), so the
+// The tiled kernel's partial results are 67 KB a tile and share (d = 128), so the
 // number of shares is weighed, at the numbers that give every CU one, two or three
 // workgroups: the farthest-reaching tile's blocks, one after the other, at what a
 // block takes beside that many workgroups, or all blocks (`steps`) at three; and for
@@ -398,7 +398,7 @@ AttnArgs attn_args(const kda_kv_pool* p, const void* q, int64_t q_ld, void* o, k
   a.q = q;
   a.o = o;
   a.part_o = static_cast<float*>(partial);
-  a.part_ml = a.part_o + rows * Hq * pl.splits * p->head_dim;
+  a.part_mnl = a.part_o + rows * Hq * pl.splits * p->head_dim;
   a.q_ld = q_ld;
   a.Hq = Hq;
   a.G = Hq / p->num_heads;

@@ -555,6 +555,9 @@ kda_status kda_kv_read(const kda_kv_pool* pool, void* k_out, void* v_out, kda_dt
  * all their tokens share.
  * A KDA_INT8 value scale in (0, 2^-120) counts as 2^-120 (an error of o below
  * 2^-113); a block with a scale that is not finite is NaN to the rows that see it.
+ * Beside a KDA_INT8 cache w_j times the value scale s_j is rounded to fp16 (in two
+ * parts for fp32 q): off by 2^-11 (2^-22) of itself, or by 2^-31 of the row's largest
+ * w s where that is more.  The sum of the w_j is kept apart from the scales, in fp32.
  * workspace: kda_attn_prefill_workspace_bytes with the same metadata.  Two calls
  * that may overlap (streams, captured graphs) need one each, here and wherever
  * this section takes a workspace.
