@@ -109,7 +109,9 @@ __device__ __forceinline__ float exp2_f(float x) { return __builtin_amdgcn_exp2f
 __device__ __forceinline__ float decay(float m, float mn) { return m == kNegInf ? 0.f : exp2_f(m - mn); }
 
 // A block's factors.  A scale that is not finite makes its block `bad`: NaN to every
-// row that sees it, nothing to the others.
+// row that sees it, nothing to the others.  A value scale of 0 (a block of zeros) has
+// the logarithm -inf: its weights w' are 0 and leave the reference m alone, which would
+// otherwise take the other blocks' weights out of fp16's range; the normaliser has them.
 template <int EB> struct BlockScale {
   float c = 1.f, lv = 0.f;  // logit factor, log2 of the value scale
   bool bad = false;
@@ -118,9 +120,8 @@ template <int EB> struct BlockScale {
     if constexpr (EB == 1) {
       bad = bad || !(ks < __builtin_inff() && vs < __builtin_inff());
       if (bad) ks = vs = 1.f;
-      vs = vs == 0.f ? 1.f : vs < 0x1p-120f ? 0x1p-120f : vs;
       c = ks;
-      lv = __builtin_amdgcn_logf(vs);
+      lv = vs == 0.f ? kNegInf : __builtin_amdgcn_logf(fmaxf(vs, 0x1p-120f));
     }
   }
   // Lane i's factors, to the whole wave.
