@@ -502,7 +502,9 @@ int64_t kda_kv_workspace_bytes(int32_t num_seqs);
  * change.  Values must be finite: one that is not makes its block's scale
  * non-finite, and every read of the block NaN.
  * Only the slots of the call's tokens (and, on growth, the older codes of the
- * first block) are changed; two sequences must not share a written page's block.
+ * first block) are changed.  A page holds tokens of one request: two sequences of a
+ * call must not write one page (a shared written block is a race; KDA_VALIDATE=1
+ * refuses any shared written page with KDA_ERR_PAGE_ALIAS).
  */
 kda_status kda_kv_append(const kda_kv_pool* pool, const kda_rope* rope, const void* q,
                          const void* k, const void* v, kda_dtype in_dtype, int64_t q_ld,
