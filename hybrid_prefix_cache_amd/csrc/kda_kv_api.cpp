@@ -218,9 +218,9 @@ kda_status check_step(const char* what, const int32_t* pos, int32_t n, int32_t t
   return KDA_OK;
 }
 
-// The tensors of an append; rows of the call are `rows`.
-kda_status check_append(const kda_kv_pool* p, const kda_rope* rope, const void* q, const void* k, const void* v,
-                        kda_dtype dt, int64_t q_ld, int64_t k_ld, int64_t v_ld, const void* q_out, int32_t Hq) {
+// The descriptors of an append; its tensors are checked once the call's rows are known.
+kda_status check_append(const kda_kv_pool* p, const kda_rope* rope, const void* q, kda_dtype dt, const void* q_out,
+                        int32_t Hq) {
   kda_status s = check_kv_pool(p);
   if (s != KDA_OK) return s;
   if (!valid_dtype(dt)) return fail(KDA_ERR_DTYPE, "unknown dtype code %d", (int)dt);
@@ -468,7 +468,7 @@ kda_status kda_kv_append(const kda_kv_pool* pool, const kda_rope* rope, const vo
                          const int32_t* page_table, int32_t max_pages, void* workspace, size_t workspace_bytes,
                          void* stream) {
   return guarded([&]() -> kda_status {
-    kda_status s = check_append(pool, rope, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads);
+    kda_status s = check_append(pool, rope, q, in_dtype, q_out, num_q_heads);
     if (s != KDA_OK) return s;
     if (num_seqs == 0) return ok();
     s = check_table(pool, page_table, max_pages);
@@ -503,7 +503,7 @@ kda_status kda_kv_append_step(const kda_kv_pool* pool, const kda_rope* rope, con
                               void* q_out, int32_t num_q_heads, int32_t n, int32_t tokens, const int32_t* pos,
                               const int32_t* page_table, int32_t max_pages, void* stream) {
   return guarded([&]() -> kda_status {
-    kda_status s = check_append(pool, rope, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads);
+    kda_status s = check_append(pool, rope, q, in_dtype, q_out, num_q_heads);
     if (s != KDA_OK) return s;
     s = check_step("kda_kv_append_step", pos, n, tokens);
     if (s != KDA_OK || n == 0) return s == KDA_OK ? ok() : s;
