@@ -18,9 +18,9 @@
 // depends on the call's arguments alone.
 //
 // Bound by memory: 256 int8 requests of 512 to 8191 tokens (8 heads of 128, 2.34 GB)
-// take 390 us, 6.0 TB/s; a million tokens of one request (2.15 GB, split 192 ways)
-// 335 us with the join, 6.4 TB/s; 256 bf16 requests with a window of 1024 (1.0 GB)
-// 166 us, 6.1 TB/s.  A large copy reaches 6.6 TB/s.  Tiles go from memory to
+// take 394 us, 5.9 TB/s (fp32 queries 406); a million tokens of one request (2.15 GB,
+// split 192 ways) 338 us with the join, 6.35 TB/s; 256 bf16 requests with a window of
+// 1024 (1.0 GB) 166 us, 6.1 TB/s.  A large copy reaches 6.6 TB/s.  Tiles go from memory to
 // registers one block ahead, with three workgroups a CU (int8): LDS staging would
 // add a barrier to a stream that shares nothing between waves.
 #include "kda_attn_device.h"

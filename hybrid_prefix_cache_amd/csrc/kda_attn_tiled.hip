@@ -19,12 +19,12 @@
 // like a decode step, and joined by the same kernel.
 //
 // Bound by the matrix and vector units together, and by the power they draw: an
-// 8192-token prompt of 32 heads over 8 (550 GFLOP) takes 563 to 589 us over an int8
-// cache, by the card (933 to 977 TFLOP/s), and 517 us over a bf16 one (1064); with a
-// cache and queries of zeros the same instructions take 453 and 374 us.  The largest
-// library products of random bf16 matrices reach 1.31-1.34 PFLOP/s on this part
-// (1.8 of zeros).  Of a block's 1100 SIMD cycles the matrix unit has 512, vector
-// instructions 510 (bf16) or 680 (int8).  Taken for it: one 32-token block a step and
+// 8192-token prompt of 32 heads over 8 (550 GFLOP) takes 564 to 598 us over an int8
+// cache, by the card (920 to 975 TFLOP/s), and 517 to 534 us over a bf16 one (1030 to
+// 1064); with a bf16 cache and queries of zeros the same instructions take 374 us.  The
+// largest library products of random bf16 matrices reach 1.31-1.34 PFLOP/s on this part
+// (1.8 of zeros).  Of a block's SIMD cycles, 930 (bf16) or 1130 (int8), the matrix unit
+// has 512, vector instructions 505 or 760.  Taken for it: one 32-token block a step and
 // three workgroups a CU, whose waves fill each other's waits (int8, when this took 594
 // us: 64-token steps and two workgroups a CU 686; 256 rows and eight waves in one step
 // 613; eight waves in two groups a phase apart 835).
@@ -230,8 +230,9 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   // to 1.55 times over few.  Sequences of few rows, which leave half of a tile's waves
   // without any, have a second part instead (error 1.00; 256 sequences of 8 tokens and 4
   // heads over 1000: 207 us with either, 64 of 16 tokens over 2000: 102 us, so 123).  For
-  // a long prompt it would be half of all products again (247 us, 333).  By the sequence:
-  // a row's bits do not depend on the rest of the call.
+  // a long prompt it would be half of all products again (247 us, 333).  By the sequence,
+  // so that it has the same parts in any batch; a resumed suffix of few rows has two where
+  // the whole prompt has one.
   if constexpr (EB == 2 && NP == 1) {
     if (s.len * a.G <= kFewRows) {
       attend_tile<D, EB, NP, 2>(a, s, req, h, sp, row0, lds);

@@ -10,9 +10,9 @@
 // registers between the load, the block's maximum and the code; codes (not
 // values) cross LDS into the block's element order, 16 bytes a thread from there.
 // 8192 tokens of 32 + 2 * 8 heads of 128, bf16 to int8 with rotation, 188 MB:
-// 35.5 us, 5.3 TB/s (a large copy: 6.6), the vector unit busy 47% of it (the
-// 64-bit rotation, whose pairs are taken one after the other: all at once they hold 120
-// registers instead of 61, and a CU half the waves).
+// 35.5 to 36.7 us, 5.1 to 5.3 TB/s (a large copy: 6.6), the vector unit busy half of it
+// (the 64-bit rotation, whose pairs are taken one after the other: all at once they hold
+// 120 registers instead of 61, and a CU half the waves).
 #include "kda_device.h"
 #include "kda_kv.h"
 

@@ -26,10 +26,13 @@ constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;  // workgroups of 256 thr
 // million-token request: 399 us at 2048, a third round nearly empty, 335 us at 1536; a
 // third of it past 16 rows, whose workgroups are two a CU).
 constexpr int64_t kDecodeTarget = 1536;
-// What the shares of the tiled kernel are weighed by, measured at 128 channels: us a
-// block takes a workgroup with one, two or three on the CU; us of the join's launch;
-// bytes of partial results a us.  Filling the card whatever it cost, prompts of 1024,
-// 2048 and 3000 tokens (32 heads, bf16 cache) took 43, 86 and 135 us; weighed, 31, 60 and 95.
+// What the shares of the tiled kernel are weighed by: us a block takes a workgroup with
+// one, two or three on the CU; us of the join's launch; bytes of partial results a us.
+// Measured with bf16 queries over a bf16 cache of 128 channels, and taken for the other
+// types and 64 channels too, whose steps take from two thirds of it (64 channels) to
+// over twice (fp32 queries): there another number of shares may be faster.  Filling the
+// card whatever it cost, prompts of 1024, 2048 and 3000 tokens (32 heads, bf16 cache)
+// took 43, 86 and 135 us; weighed, 31, 60 and 95.
 constexpr int64_t kCUs = 256;
 constexpr double kStepUs[4] = {0, 1.1, 1.15, 1.71}, kJoinUs = 4.0, kPartialRate = 5e6;
 

@@ -438,7 +438,8 @@ kda_status kda_short_conv_update(const kda_conv_pool* cpool, const void* x, cons
  * append has two for a block of a head and, with q, at most one for two rows, a
  * read one for a block of a head, an attention call one for a key/value head and
  * 128 (step form: request or 128) of its rows, times the workgroups that share
- * the cache where there are few of them.
+ * the cache where there are few of them; an attention call also if its rows times
+ * num_q_heads pass 2^30.
  */
 typedef struct {
   void* base;
@@ -554,12 +555,19 @@ kda_status kda_kv_read(const kda_kv_pool* pool, void* k_out, void* v_out, kda_dt
  * Pages that no row of the call sees are not read and may have been freed.
  * What slots past a request's tokens, and tokens a row does not see, hold
  * (NaN included) does not reach that row, but for KDA_INT8 blocks, whose scale
- * all their tokens share.
+ * all their tokens share.  A row that sees an infinite or NaN bf16 value is
+ * infinite or NaN in its channel, either of them.
  * A KDA_INT8 value scale in (0, 2^-120) counts as 2^-120 (an error of o below
  * 2^-113); a block with a scale that is not finite is NaN to the rows that see it.
  * Beside a KDA_INT8 cache w_j times the value scale s_j is rounded to fp16 (in two
  * parts for fp32 q): off by 2^-11 (2^-22) of itself, or by 2^-31 of the row's largest
  * w s where that is more.  The sum of the w_j is kept apart from the scales, in fp32.
+ * Beside a KDA_BF16 cache w_j is rounded to bf16: for bf16 q to one number (2^-8)
+ * where a sequence brings more than 64 rows (a token and query head) a key/value
+ * head, else to the sum of two (2^-16); for fp32 q to the sum of three.
+ * A result depends on the call's arguments alone, but a row's bits may differ between
+ * calls of different shapes (resumed and whole prompts, step and packed forms): the
+ * parts above, and the number of workgroups that share its cache, follow the call.
  * workspace: kda_attn_prefill_workspace_bytes with the same metadata.  Two calls
  * that may overlap (streams, captured graphs) need one each, here and wherever
  * this section takes a workspace.
