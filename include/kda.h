@@ -556,7 +556,9 @@ kda_status kda_kv_read(const kda_kv_pool* pool, void* k_out, void* v_out, kda_dt
  * What slots past a request's tokens, and tokens a row does not see, hold
  * (NaN included) does not reach that row, but for KDA_INT8 blocks, whose scale
  * all their tokens share.  A row that sees an infinite or NaN bf16 value is
- * infinite or NaN in its channel, either of them.
+ * infinite or NaN in its channel, either of them.  The sums over a KDA_BF16 cache are
+ * held in fp32 before they are divided, up to 256 times the values each: values of
+ * 2^119 / tokens and more may overflow.
  * A KDA_INT8 value scale in (0, 2^-120) counts as 2^-120 (an error of o below
  * 2^-113); a block with a scale that is not finite is NaN to the rows that see it.
  * Beside a KDA_INT8 cache w_j times the value scale s_j is rounded to fp16 (in two
