@@ -45,6 +45,10 @@ EXPORTS = ("kda_version", "kda_last_error", "kda_pool_check", "kda_state_offset"
            "kda_kv_pool_check", "kda_kv_head_bytes", "kda_kv_workspace_bytes", "kda_kv_append",
            "kda_kv_append_step", "kda_kv_read", "kda_attn_prefill_workspace_bytes", "kda_attn_prefill",
            "kda_attn_decode_workspace_bytes", "kda_attn_decode",
+           "kda_decode_tree", "kda_decode_commit", "kda_short_conv_tree", "kda_short_conv_commit",
+           "kda_kv_append_tree", "kda_attn_tree_workspace_bytes", "kda_attn_tree", "kda_kv_commit",
+           "kda_page_map_check", "kda_pages_workspace_bytes", "kda_pages_reserve", "kda_pages_free", "kda_pages_fork",
+           "kda_pages_compact", "kda_kv_copy_pages",
            "kda_xxh64", "kda_chain_hashes", "kda_ckpt_plan", "kda_index_create",
            "kda_index_destroy", "kda_index_register_pages", "kda_index_register_ckpt",
            "kda_index_mark_ready", "kda_index_lookup", "kda_index_release", "kda_index_evict_page",
@@ -85,6 +89,13 @@ class kda_rope(ctypes.Structure):
                 ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
+class kda_page_map(ctypes.Structure):
+    device = None  # of the tensors it was made from
+
+    _fields_ = [("refs", ctypes.c_void_p), ("table", ctypes.c_void_p), ("num_pages", ctypes.c_int32),
+                ("rows", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32)]
+
+
 class kda_hit(ctypes.Structure):
     _fields_ = [("boundary", ctypes.c_int64), ("mla_tokens", ctypes.c_int64),
                 ("num_pages", ctypes.c_int32), ("pad", ctypes.c_int32),
@@ -104,6 +115,7 @@ _lib = ctypes.CDLL(LIB_PATH)
 _P, _i32, _i64, _sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 _PP = ctypes.POINTER(kda_pool)
 _PKV, _PR = ctypes.POINTER(kda_kv_pool), ctypes.POINTER(kda_rope)
+_PC, _PM = ctypes.POINTER(kda_conv_pool), ctypes.POINTER(kda_page_map)
 _sig = {
     "kda_version": (_i32, []),
     "kda_last_error": (ctypes.c_char_p, []),
@@ -145,6 +157,23 @@ _sig = {
     "kda_attn_decode_workspace_bytes": (_sz, [_PKV, _i32, _i32, _i32, _i32, _i32, _i32]),
     "kda_attn_decode": (ctypes.c_int, [_PKV, _P, ctypes.c_int, _i64, _P, ctypes.c_int, _i32, ctypes.c_float,
                                        _i32, _i32, _i32, _i32, _P, _P, _i32, _P, _sz, _P]),
+    "kda_decode_tree": (ctypes.c_int, [_PP, _P, _P, _P, _P, _P, ctypes.c_int, _P, ctypes.c_int, _i32, _i32, _P, _P, _P]),
+    "kda_decode_commit": (ctypes.c_int, [_PP, _P, _P, _P, _P, ctypes.c_int, _i32, _i32, _P, _P, _P, _P, _P]),
+    "kda_short_conv_tree": (ctypes.c_int, [_PC, _P, _P, _P, ctypes.c_int, _i32, _i32, _P, _P, _P]),
+    "kda_short_conv_commit": (ctypes.c_int, [_PC, _P, _i32, _i32, _P, _P, _P, _P, _P]),
+    "kda_kv_append_tree": (ctypes.c_int, [_PKV, _PR, _P, _P, _P, ctypes.c_int, _i64, _i64, _i64, _P, _i32,
+                                          _i32, _i32, _P, _P, _P, _i32, _P]),
+    "kda_attn_tree_workspace_bytes": (_sz, [_PKV, _i32, _i32, _i32, _i32, _i32, _i32]),
+    "kda_attn_tree": (ctypes.c_int, [_PKV, _P, ctypes.c_int, _i64, _P, ctypes.c_int, _i32, ctypes.c_float,
+                                     _i32, _i32, _i32, _i32, _P, _P, _P, _i32, _P, _sz, _P]),
+    "kda_kv_commit": (ctypes.c_int, [_PKV, _i32, _i32, _P, _P, _P, _P, _i32, _P]),
+    "kda_page_map_check": (ctypes.c_int, [_PM]),
+    "kda_pages_workspace_bytes": (_sz, [_PM]),
+    "kda_pages_reserve": (ctypes.c_int, [_PM, _P, _P, _P, _P, _sz, _P]),
+    "kda_pages_free": (ctypes.c_int, [_PM, _P, _P, _P]),
+    "kda_pages_fork": (ctypes.c_int, [_PM, _i32, _P, _P, _P, _P, _P, _P, _P, _P, _sz, _P]),
+    "kda_pages_compact": (ctypes.c_int, [_PM, _P, _P, _P, _sz, _P]),
+    "kda_kv_copy_pages": (ctypes.c_int, [_PKV, _i32, _P, _P, _P, _P]),
     "kda_xxh64": (ctypes.c_uint64, [_P, _i64, ctypes.c_uint64]),
     "kda_chain_hashes": (_i64, [_P, _i64, _i32, ctypes.c_uint64, _P, _i64]),
     "kda_ckpt_plan": (_i64, [_i64, _i64, _i32]),
@@ -636,6 +665,182 @@ def kda_attn_decode(pool, q, o, tokens, pos, page_table, *, scale, window=0, sin
     _check(_lib.kda_attn_decode(ctypes.byref(pool), qp, _dtype_code(q), ql, op, _dtype_code(o), hq, scale, window,
                                 sinks, n, tokens, _ints("pos", pos, n, 1, dev), tp, page_table.shape[1], wp, wb,
                                 _on(stream, dev)))
+
+
+# ---- trees of drafted tokens ----------------------------------------------------
+def _tree(parent, dev):
+    """(pointer, requests, entries) of an int32 device tensor [n, tokens]."""
+    return _ints("parent", parent, parent.shape[0], 2, dev), parent.shape[0], parent.shape[1]
+
+
+def _path(path, count, dev):
+    ptr, n, tokens = _ints("path", path, path.shape[0], 2, dev), path.shape[0], path.shape[1]
+    return ptr, _ints("count", count, n, 1, dev), n, tokens
+
+
+def _same(name, x, shape, dtype, dev):
+    """Pointer of a contiguous tensor of device `dev` with this shape (and type, if one is given)."""
+    if x.get_device() != dev or not x.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of the current device")
+    if tuple(x.shape) != shape or (dtype is not None and x.dtype != dtype):
+        raise ValueError(f"{name} must be {list(shape)}{'' if dtype is None else f' of {dtype}'} (got {tuple(x.shape)} of {x.dtype})")
+    return x.data_ptr()
+
+
+def _tokens_of(pool, rows, k, v, g, beta, dev):
+    """Pointers of a recurrence's k, v, g and beta, and their type."""
+    shape, dt = (rows, pool.num_heads, pool.d_k), k.dtype
+    return (_same("k", k, shape, None, dev), _same("v", v, shape, dt, dev), _same("g", g, shape, dt, dev),
+            _same("beta", beta, shape[:2], dt, dev), _dtype_code(k))
+
+
+def kda_decode_tree(pool, q, k, v, g, beta, o, parent, page_in, *, stream=None):
+    """The recurrence along trees: q, k, g, v, o [n * tokens, H, d], beta [n * tokens, H]; parent int32
+    [n, tokens]; page_in int32 [n] (device tensors).  Writes o alone."""
+    dev = torch.cuda.current_device()
+    tp, n, tokens = _tree(parent, dev)
+    kp, vp, gp, bp, dt = _tokens_of(pool, n * tokens, k, v, g, beta, dev)
+    qp, op = _same("q", q, tuple(k.shape), k.dtype, dev), _same("o", o, tuple(k.shape), None, dev)
+    _check(_lib.kda_decode_tree(ctypes.byref(pool), qp, kp, vp, gp, bp, dt, op, _dtype_code(o), n, tokens, tp,
+                                _ints("page_in", page_in, n, 1, dev), _on(stream, dev)))
+
+
+def kda_decode_commit(pool, k, v, g, beta, path, count, page_in, page_out, *, stream=None):
+    """The state after the accepted path (path int32 [n, tokens], count int32 [n]) of page_in[r], to page_out[r]."""
+    dev = torch.cuda.current_device()
+    pp, cp, n, tokens = _path(path, count, dev)
+    kp, vp, gp, bp, dt = _tokens_of(pool, n * tokens, k, v, g, beta, dev)
+    _check(_lib.kda_decode_commit(ctypes.byref(pool), kp, vp, gp, bp, dt, n, tokens, pp, cp, _ints("page_in", page_in, n, 1, dev),
+                                  _ints("page_out", page_out, n, 1, dev), _on(stream, dev)))
+
+
+def _conv_dtype(cpool):
+    return torch.bfloat16 if cpool.dtype == KDA_BF16 else torch.float32
+
+
+def kda_short_conv_tree(cpool, x, w, y, parent, page_in, *, stream=None):
+    """The short convolution along trees: x, y [n * tokens, C], w [C, W] fp32, parent int32 [n, tokens], page_in
+    int32 [n] (device tensors).  Writes y alone."""
+    dev = torch.cuda.current_device()
+    tp, n, tokens = _tree(parent, dev)
+    shape = (n * tokens, cpool.channels)
+    _check(_lib.kda_short_conv_tree(ctypes.byref(cpool), _same("x", x, shape, _conv_dtype(cpool), dev),
+                                    _same("w", w, (cpool.channels, cpool.width), torch.float32, dev),
+                                    _same("y", y, shape, None, dev), _dtype_code(y), n, tokens, tp,
+                                    _ints("page_in", page_in, n, 1, dev), _on(stream, dev)))
+
+
+def kda_short_conv_commit(cpool, x, path, count, page_in, page_out, *, stream=None):
+    """The window after the accepted path of page_in[r], to page_out[r]."""
+    dev = torch.cuda.current_device()
+    pp, cp, n, tokens = _path(path, count, dev)
+    _check(_lib.kda_short_conv_commit(ctypes.byref(cpool), _same("x", x, (n * tokens, cpool.channels), _conv_dtype(cpool), dev),
+                                      n, tokens, pp, cp, _ints("page_in", page_in, n, 1, dev),
+                                      _ints("page_out", page_out, n, 1, dev), _on(stream, dev)))
+
+
+def kda_kv_append_tree(pool, q, k, v, q_out, parent, pos, page_table, *, rope=None, stream=None):
+    """kda_kv_append_step for trees (parent int32 [n, tokens]): entry t at slot pos[r] + t, rotated by
+    pos[r] + its depth."""
+    dev = _here(pool, torch.cuda.current_device())
+    pp, n, tokens = _tree(parent, dev)
+    qp, kp, vp, dt, ql, kl, vl, op, hq, rp = _append_tensors(pool, q, k, v, q_out, n * tokens, rope, dev)
+    tp = _ints("page_table", page_table, n, 2, dev)
+    _check(_lib.kda_kv_append_tree(ctypes.byref(pool), rp, qp, kp, vp, dt, ql, kl, vl, op, hq, n, tokens,
+                                   _ints("pos", pos, n, 1, dev), pp, tp, page_table.shape[1], _on(stream, dev)))
+
+
+def kda_attn_tree_workspace_bytes(pool, num_q_heads: int, n: int, tokens: int, max_pages: int, *, window: int = 0,
+                                  sinks: int = 0) -> int:
+    return int(_lib.kda_attn_tree_workspace_bytes(ctypes.byref(pool), num_q_heads, n, tokens, max_pages, window, sinks))
+
+
+def kda_attn_tree(pool, q, o, parent, pos, page_table, *, scale, window=0, sinks=0, workspace=None, stream=None):
+    """kda_attn_decode for trees (parent int32 [n, tokens]): q, o [n * tokens, Hq, d] device tensors; a node
+    sees the tokens cached before pos[r] and the nodes on its way."""
+    dev, hq = _here(pool, torch.cuda.current_device()), _heads(q, pool.head_dim)
+    pp, n, tokens = _tree(parent, dev)
+    qp, ql = _rows("q", q, n * tokens, hq, pool.head_dim, None, dev)
+    op = _out("o", o, n * tokens, hq, pool.head_dim, None, dev)
+    tp = _ints("page_table", page_table, n, 2, dev)
+    wp, wb = _ws(workspace, dev)
+    _check(_lib.kda_attn_tree(ctypes.byref(pool), qp, _dtype_code(q), ql, op, _dtype_code(o), hq, scale, window, sinks,
+                              n, tokens, _ints("pos", pos, n, 1, dev), pp, tp, page_table.shape[1], wp, wb,
+                              _on(stream, dev)))
+
+
+def kda_kv_commit(pool, path, count, pos, page_table, *, stream=None):
+    """Moves the keys and values of slot pos[r] + path[r, i] to slot pos[r] + i, for i < count[r]."""
+    dev = _here(pool, torch.cuda.current_device())
+    pp, cp, n, tokens = _path(path, count, dev)
+    tp = _ints("page_table", page_table, n, 2, dev)
+    _check(_lib.kda_kv_commit(ctypes.byref(pool), n, tokens, _ints("pos", pos, n, 1, dev), pp, cp, tp,
+                              page_table.shape[1], _on(stream, dev)))
+
+
+# ---- upkeep of pages ------------------------------------------------------------
+def make_page_map(refs, table, page_tokens: int):
+    """Page map over int32 device tensors refs [num_pages] and table [rows, max_pages], which it keeps alive."""
+    dev = refs.get_device()
+    rp, tp = _ints("refs", refs, refs.numel(), 1, dev), _ints("table", table, table.shape[0], 2, dev)
+    if dev < 0:
+        raise ValueError("expected device tensors")
+    m = kda_page_map(rp, tp, refs.numel(), table.shape[0], table.shape[1], int(page_tokens))
+    m.device, m.tensors = dev, (refs, table)
+    return m
+
+
+def kda_page_map_check(page_map) -> int:
+    return int(_lib.kda_page_map_check(ctypes.byref(page_map)))
+
+
+def kda_pages_workspace_bytes(page_map) -> int:
+    return int(_lib.kda_pages_workspace_bytes(ctypes.byref(page_map)))
+
+
+def kda_pages_reserve(page_map, first, last, status, *, workspace=None, stream=None):
+    """Pages for the tokens [first[r], last[r]) of each row; status[r]: entries that found none (int32 device
+    tensors [rows])."""
+    dev, n = _here(page_map, torch.cuda.current_device()), page_map.rows
+    wp, wb = _ws(workspace, dev)
+    _check(_lib.kda_pages_reserve(ctypes.byref(page_map), _ints("first", first, n, 1, dev), _ints("last", last, n, 1, dev),
+                                  _ints("status", status, n, 1, dev), wp, wb, _on(stream, dev)))
+
+
+def kda_pages_free(page_map, first, last, *, stream=None):
+    """Lets go of the pages whose tokens all lie in [first[r], last[r]) of row r (int32 device tensors [rows])."""
+    dev, n = _here(page_map, torch.cuda.current_device()), page_map.rows
+    _check(_lib.kda_pages_free(ctypes.byref(page_map), _ints("first", first, n, 1, dev), _ints("last", last, n, 1, dev),
+                               _on(stream, dev)))
+
+
+def kda_pages_fork(page_map, src_row, dst_row, tokens, copy_src, copy_dst, copy_tokens, status, *, workspace=None,
+                   stream=None):
+    """Row dst_row[i] becomes the first tokens[i] tokens of row src_row[i]; the copies to make in each layer's
+    pool go to copy_src, copy_dst, copy_tokens (all int32 device tensors [n])."""
+    dev, n = _here(page_map, torch.cuda.current_device()), src_row.numel()
+    arrays = [_ints(name, x, n, 1, dev) for name, x in (
+        ("src_row", src_row), ("dst_row", dst_row), ("tokens", tokens), ("copy_src", copy_src), ("copy_dst", copy_dst),
+        ("copy_tokens", copy_tokens), ("status", status))]
+    wp, wb = _ws(workspace, dev)
+    _check(_lib.kda_pages_fork(ctypes.byref(page_map), n, *arrays, wp, wb, _on(stream, dev)))
+
+
+def kda_pages_compact(page_map, copy_src, copy_dst, *, workspace=None, stream=None):
+    """Moves pages to low numbers; the copies to make in each layer's pool go to copy_src, copy_dst (int32
+    device tensors [num_pages])."""
+    dev, n = _here(page_map, torch.cuda.current_device()), page_map.num_pages
+    wp, wb = _ws(workspace, dev)
+    _check(_lib.kda_pages_compact(ctypes.byref(page_map), _ints("copy_src", copy_src, n, 1, dev),
+                                  _ints("copy_dst", copy_dst, n, 1, dev), wp, wb, _on(stream, dev)))
+
+
+def kda_kv_copy_pages(pool, src, dst, *, tokens=None, stream=None):
+    """Pages src[i] to dst[i] (none where src[i] is negative): whole, or the blocks with their first tokens[i]
+    tokens (int32 device tensors of one length)."""
+    dev, n = _here(pool, torch.cuda.current_device()), src.numel()
+    _check(_lib.kda_kv_copy_pages(ctypes.byref(pool), n, _ints("src", src, n, 1, dev), _ints("dst", dst, n, 1, dev),
+                                  None if tokens is None else _ints("tokens", tokens, n, 1, dev), _on(stream, dev)))
 
 
 # ---- host prefix index (include/kda_index.h) --------------------------------

@@ -158,6 +158,23 @@ void host_set_error(const char* msg) { g_err = msg; }
 void host_clear_error() { g_err.clear(); }
 }  // namespace kda
 
+kda_status kda::check_conv_pool(const kda_conv_pool* p) {
+  if (!p) return fail(KDA_ERR_NULL, "kda_short_conv: conv pool descriptor is NULL");
+  if (!p->base) return fail(KDA_ERR_POOL, "kda_short_conv: conv pool base is NULL");
+  if (!aligned(p->base, 256)) return fail(KDA_ERR_POOL, "kda_short_conv: conv pool base must be 256-byte aligned");
+  if (p->num_pages < 1) return fail(KDA_ERR_POOL, "kda_short_conv: conv pool needs num_pages >= 1");
+  if (p->width < 2 || p->width > 4) return fail(KDA_ERR_SHAPE, "kda_short_conv: width %d not in {2, 3, 4}", p->width);
+  if (!valid_dtype(p->dtype)) return fail(KDA_ERR_DTYPE, "kda_short_conv: unknown dtype code %d", p->dtype);
+  const int vec = p->dtype == KDA_BF16 ? 8 : 4;
+  if (p->channels < vec || p->channels % vec != 0 || p->channels > (1 << 24))
+    return fail(KDA_ERR_SHAPE, "kda_short_conv: channels %d must be a positive multiple of %d", p->channels, vec);
+  const int64_t need = (int64_t)(p->width - 1) * p->channels * (p->dtype == KDA_BF16 ? 2 : 4);
+  if (p->page_bytes < need || p->page_bytes % 256 != 0)
+    return fail(KDA_ERR_POOL, "kda_short_conv: page_bytes %lld must be a multiple of 256 and >= %lld",
+                (long long)p->page_bytes, (long long)need);
+  return KDA_OK;
+}
+
 extern "C" {
 
 int32_t kda_version(void) { return (1 << 16) | 0; }
@@ -519,23 +536,6 @@ kda_status kda_checkpoint_restore(const kda_pool* pool, const int32_t* src_ckpt,
 int64_t kda_conv_workspace_bytes(int32_t num_seqs, int32_t num_ckpts) {
   if (num_seqs < 0 || num_ckpts < 0) return -1;
   return meta_layout(num_seqs, num_ckpts).inter_off;
-}
-
-static kda_status check_conv_pool(const kda_conv_pool* p) {
-  if (!p) return fail(KDA_ERR_NULL, "kda_short_conv: conv pool descriptor is NULL");
-  if (!p->base) return fail(KDA_ERR_POOL, "kda_short_conv: conv pool base is NULL");
-  if (!aligned(p->base, 256)) return fail(KDA_ERR_POOL, "kda_short_conv: conv pool base must be 256-byte aligned");
-  if (p->num_pages < 1) return fail(KDA_ERR_POOL, "kda_short_conv: conv pool needs num_pages >= 1");
-  if (p->width < 2 || p->width > 4) return fail(KDA_ERR_SHAPE, "kda_short_conv: width %d not in {2, 3, 4}", p->width);
-  if (!valid_dtype(p->dtype)) return fail(KDA_ERR_DTYPE, "kda_short_conv: unknown dtype code %d", p->dtype);
-  const int vec = p->dtype == KDA_BF16 ? 8 : 4;
-  if (p->channels < vec || p->channels % vec != 0 || p->channels > (1 << 24))
-    return fail(KDA_ERR_SHAPE, "kda_short_conv: channels %d must be a positive multiple of %d", p->channels, vec);
-  const int64_t need = (int64_t)(p->width - 1) * p->channels * (p->dtype == KDA_BF16 ? 2 : 4);
-  if (p->page_bytes < need || p->page_bytes % 256 != 0)
-    return fail(KDA_ERR_POOL, "kda_short_conv: page_bytes %lld must be a multiple of 256 and >= %lld",
-                (long long)p->page_bytes, (long long)need);
-  return KDA_OK;
 }
 
 kda_status kda_short_conv(const kda_conv_pool* cpool, const void* x, const float* w, void* y,

@@ -78,7 +78,9 @@ __device__ __forceinline__ void spread_nonfinite(u32x4_t& v, const bf16x8* seen,
     }
 }
 
-template <int D, int EB, int NP, int MT>
+// TREE: the rows are the nodes of a drafted tree, at slots p0 + t; a row sees the cached
+// tokens before p0 by its position, p0 + depth, and of the slots from p0 on its way.
+template <int D, int EB, int NP, int MT, bool TREE>
 __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   typedef AttnOp<EB> Op;
   typedef typename Op::Frag Frag;
@@ -109,9 +111,17 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     return;
   }
   const Reach reach = reach_of(p0, p1, a.window, a.sinks);
-  const Whole whole = whole_of(p0, p1, a.window, a.sinks);
+  const Whole whole = whole_of(TREE ? p0 - 1 : p0, p1, a.window, a.sinks);
   const Chunk ch = chunk_of(reach.count(), a.splits, a.min_blocks, sp);
   if (ch.begin >= ch.end) return;
+  TreeNode tree;
+  uint64_t sight = 0, nodes = 0, bad = 0, see_way[MT];  // of the lane's entry; of all; of the lane's rows
+  if constexpr (TREE) {
+    tree = tree_node(a.parent + (int64_t)req * a.b.tokens, a.b.tokens);
+    sight = tree_sight(tree, p0, a.b.tokens, a.window, a.sinks);
+    nodes = __ballot(tree.node);
+    bad = __ballot(tree.bad);
+  }
 
   // ---- queries: lane (g, col) holds row col's channels of k-group g
   Frag qf[MT][KS][NP];
@@ -122,6 +132,10 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     const int row = 16 * mt + col;
     const bool live = row < M;
     qp[mt] = p0 + (live ? row / a.G : 0);
+    if constexpr (TREE) {
+      qp[mt] = p0 + __shfl(tree.depth, live ? row / a.G : 0);
+      see_way[mt] = shfl64(sight, live ? row / a.G : 0);
+    }
     const int64_t at = (int64_t)(req * a.b.tokens + (live ? row / a.G : 0)) * a.q_ld +
                        (int64_t)(h * a.G + (live ? row % a.G : 0)) * D;
     float x[KS][8], amax = 0.f;
@@ -236,10 +250,16 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] = s[mt][e >> 2][e & 3] * c;
       if (!full) {
+        uint32_t in_tree = 0;
+        if constexpr (TREE) in_tree = tree_bits(see_way[mt], blk * kKvBlock - (int)p0);
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const int64_t j = (int64_t)blk * kKvBlock + 16 * (e >> 2) + 4 * g + (e & 3);
-          const bool see = sees(qp[mt], j, a.window, a.sinks);
+          bool see;
+          if constexpr (TREE)
+            see = j < p0 ? sees(qp[mt], j, a.window, a.sinks) : in_tree >> (16 * (e >> 2) + 4 * g + (e & 3)) & 1;
+          else
+            see = sees(qp[mt], j, a.window, a.sinks);
           x[e] = !see ? kNegInf : bs.bad ? __builtin_nanf("") : x[e];
           seen[mt][e] = static_cast<__bf16>(see ? 1.f : 0.f);
         }
@@ -346,6 +366,15 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
       }
 #pragma unroll
       for (int w = 0; w < 4; ++w) ll += sh_l[w][rr] * decay(sh_n[w][rr], nm);
+      if constexpr (TREE) {  // no node: 0; a bad one: NaN, through the join too
+        const int tok = rr / a.G;
+        if (!(nodes >> tok & 1) || (bad >> tok & 1)) {
+          const float v = nodes >> tok & 1 ? __builtin_nanf("") : 0.f;
+          y = f32x4{v, v, v, v};
+          mm = nm = 0.f;
+          ll = 1.f;
+        }
+      }
       const int64_t at = (int64_t)(req * a.b.tokens + rr / a.G) * a.Hq + h * a.G + rr % a.G;
       if (ch.used == 1) {
         // ll is 0 only where nothing was seen, and every row sees itself
@@ -381,7 +410,8 @@ template <int D, int W> __global__ __launch_bounds__(256) void attn_join_kernel(
   if (sq.start < 0 || (int64_t)sq.start + sq.len > (int64_t)a.c.max_pages * a.c.page_tokens) return;
   // the reach of the row's tile, as the attention kernel divided it
   const int t0 = ((row - sq.row) * a.G + g) / a.tile_rows * a.tile_rows, t1 = min(sq.len * a.G, t0 + a.tile_rows);
-  const Reach reach = reach_of(sq.start + t0 / a.G, sq.start + (t1 - 1) / a.G, a.window, a.sinks);
+  const Reach reach = a.parent ? reach_of(sq.start, sq.start + sq.len - 1, a.window, a.sinks)
+                               : reach_of(sq.start + t0 / a.G, sq.start + (t1 - 1) / a.G, a.window, a.sinks);
   const int used = chunk_of(reach.count(), a.splits, a.min_blocks, 0).used;
   if (used == 1) return;
   const float* mnl = a.part_mnl + 3 * at * a.splits;
@@ -429,10 +459,14 @@ template <int D, int W> __global__ __launch_bounds__(256) void attn_join_kernel(
   }
 }
 
-template <int D, int EB, int NP> static void launch_mt(const AttnArgs& a, hipStream_t st) {
+template <int D, int EB, int NP, bool TREE> static void launch_tr(const AttnArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.b.n * a.c.H * a.splits)), block(256);
-  if (a.b.tokens * a.G <= 16) hipLaunchKernelGGL((attn_decode_kernel<D, EB, NP, 1>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((attn_decode_kernel<D, EB, NP, 2>), grid, block, 0, st, a);
+  if (a.b.tokens * a.G <= 16) hipLaunchKernelGGL((attn_decode_kernel<D, EB, NP, 1, TREE>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((attn_decode_kernel<D, EB, NP, 2, TREE>), grid, block, 0, st, a);
+}
+template <int D, int EB, int NP> static void launch_mt(const AttnArgs& a, hipStream_t st) {
+  if (a.parent) launch_tr<D, EB, NP, true>(a, st);
+  else launch_tr<D, EB, NP, false>(a, st);
 }
 template <int D> static void launch_dd(bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st) {
   if (int8) {

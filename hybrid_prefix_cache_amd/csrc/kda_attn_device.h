@@ -23,6 +23,7 @@
 #pragma once
 #include "kda_device.h"
 #include "kda_kv.h"
+#include "kda_tree.h"
 
 namespace kda {
 
@@ -188,6 +189,13 @@ __device__ __forceinline__ Whole whole_of(int first, int last, int window, int s
 }
 __device__ __forceinline__ bool sees(int p, int j, int window, int sinks) {  // positions below 2^30
   return j <= p && (!window || j > p - window || j < sinks);
+}
+
+// The part of a row's sight of a tree that lies in a 32-token block, whose first slot is
+// the tree's slot `first` (negative where the tree begins inside the block).
+__device__ __forceinline__ uint32_t tree_bits(uint64_t see, int first) {
+  if (first <= -kKvBlock || first >= kMaxTree) return 0;
+  return (uint32_t)(first < 0 ? see << -first : see >> first);
 }
 
 // How the blocks a tile sees are divided among `splits` workgroups: chunks of at

@@ -124,6 +124,17 @@ __device__ __forceinline__ void mask16(f32x16& x, int qp, int blk, int half, int
     x[e] = !sees(qp, j, window, sinks) ? kNegInf : bad ? __builtin_nanf("") : x[e];
   }
 }
+// The same for a node of a drafted tree that begins at slot p0.
+__device__ __forceinline__ void mask16_tree(f32x16& x, int qp, int p0, uint64_t see, int blk, int half, int window, int sinks,
+                                            bool bad) {
+  const uint32_t in_tree = tree_bits(see, blk * kKvBlock - p0);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int t = token_of(e >> 2, half, e & 3), j = blk * kKvBlock + t;
+    const bool sees_it = j < p0 ? sees(qp, j, window, sinks) : in_tree >> t & 1;
+    x[e] = !sees_it ? kNegInf : bad ? __builtin_nanf("") : x[e];
+  }
+}
 
 // The block's weights from its logits, as operands of WP parts; the references m and n
 // (of the weights and, int8, of the normaliser), l and the sums acc follow.

@@ -28,6 +28,7 @@
 // L2), which only wins when x is already cached.
 #include "kda_device.h"
 #include "kda_launch.h"
+#include "kda_tree.h"
 
 namespace kda {
 
@@ -260,6 +261,135 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvUpdateArgs a) {
     for (int j = 0; j < W - 1; ++j)
       *reinterpret_cast<u32x4_t*>(dp + (int64_t)j * C * sizeof(In)) = rows[q][j + 1];
   }
+}
+
+// Along a tree of drafted tokens: node t's inputs are its own row of x and those of the
+// nodes before it on its way, then the window's (page_in[r]).  A thread takes a 16-byte
+// channel group of kConvTreeNodes nodes of a request; its taps stay in registers.  Rows
+// of parents are read again by their children, mostly from the caches.  Same taps and
+// summation order as conv_kernel.
+constexpr int kConvTreeNodes = 8;
+
+template <typename In, int W>
+__global__ __launch_bounds__(256) void conv_tree_kernel(ConvTreeArgs a) {
+  using CV = ConvVec<In>;
+  constexpr int N = CV::N, K = kConvTreeNodes;
+  const int parts = (a.tokens + K - 1) / K, r = blockIdx.x / parts, t0 = blockIdx.x % parts * K;
+  const int64_t row0 = (int64_t)r * a.tokens, C = a.C;
+  const TreeNode tree = tree_node(a.parent + row0, a.tokens);
+  const uint64_t good = __ballot(tree.good()), node = __ballot(tree.node);
+  const int up = tree.good() ? a.parent[row0 + (threadIdx.x & 63)] : -1;  // of the lane's entry
+  const int pin = a.page_in[r];
+  const bool page = pin >= 0 && pin < a.num_pages;
+  const int c0 = (blockIdx.y * 256 + threadIdx.x) * N;
+  const bool live = c0 < a.C;
+  const In* x = reinterpret_cast<const In*>(a.x) + row0 * C + c0;
+  const In* win = reinterpret_cast<const In*>(a.cpool + (int64_t)(page ? pin : 0) * a.cpage_bytes) + c0;
+  float wt[W][N];
+  if (live) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int j = 0; j < W; ++j) wt[j][i] = a.w[(int64_t)(c0 + i) * W + j];
+  }
+  u32x4_t rows[K][W];
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int t = t0 + i;
+    if (t >= a.tokens || !(good >> t & 1) || !page) continue;
+    int at = t, back = 0;  // the node, or (at < 0) how many inputs before the tree
+#pragma unroll
+    for (int j = W - 1; j >= 0; --j) {
+      if (live) rows[i][j] = CV::raw(at >= 0 ? x + at * C : win + (int64_t)(W - 1 - back) * C);
+      if (at >= 0) at = __builtin_amdgcn_readlane(up, at);
+      if (at < 0) ++back;
+    }
+  }
+  if (!live) return;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    const int t = t0 + i;
+    if (t >= a.tokens) continue;
+    float yv[N];
+#pragma unroll
+    for (int e = 0; e < N; ++e) yv[e] = 0.f;
+    if (!(node >> t & 1) && page) {
+    } else if ((good >> t & 1) && page) {
+#pragma unroll
+      for (int j = 0; j < W; ++j) {
+        float xv[N];
+        CV::unpack(rows[i][j], xv);
+#pragma unroll
+        for (int e = 0; e < N; ++e) yv[e] = fmaf(wt[j][e], xv[e], yv[e]);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e) yv[e] = __builtin_nanf("");
+    }
+    const int64_t yo = (row0 + t) * C + c0;
+    if (a.out_bf16) {
+      u32x4_t qv;
+#pragma unroll
+      for (int e = 0; e < N / 2; ++e) qv[e] = pack_bf16x2(yv[2 * e], yv[2 * e + 1]);
+      if constexpr (N == 8) {
+        __builtin_nontemporal_store(qv, reinterpret_cast<u32x4_t*>(reinterpret_cast<uint16_t*>(a.y) + yo));
+      } else {
+        __builtin_nontemporal_store(u32x2_t{qv[0], qv[1]},
+                                    reinterpret_cast<u32x2_t*>(reinterpret_cast<uint16_t*>(a.y) + yo));
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; e += 4)
+        __builtin_nontemporal_store(f32x4{yv[e], yv[e + 1], yv[e + 2], yv[e + 3]},
+                                    reinterpret_cast<f32x4*>(reinterpret_cast<float*>(a.y) + yo + e));
+    }
+  }
+}
+
+// The window after each request's accepted path: of the entering window followed by the
+// path's inputs, the last W - 1, as copies of 16-byte words.  All are read before the
+// first is written, so page_out[r] may equal page_in[r].
+template <int W> __global__ __launch_bounds__(256) void conv_commit_kernel(ConvCommitArgs a) {
+  const int r = blockIdx.x;
+  const int pin = a.page_in[r], po = a.page_out[r], count = __builtin_amdgcn_readfirstlane(a.count[r]);
+  const TreePath path = tree_path(a.path + (int64_t)r * a.tokens, count, a.tokens);
+  if (pin < 0 || pin >= a.num_pages || po < 0 || po >= a.num_pages || !path.valid) return;
+  const int64_t c = 16 * (blockIdx.y * 256 + (int64_t)threadIdx.x);
+  const uint8_t* win = a.cpool + (int64_t)pin * a.cpage_bytes + c;
+  const uint8_t* x = reinterpret_cast<const uint8_t*>(a.x) + (int64_t)r * a.tokens * a.row_bytes + c;
+  const uint8_t* from[W - 1];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) {
+    const int e = count + j;  // of the inputs in a row
+    from[j] = e < W - 1 ? win + (int64_t)e * a.row_bytes
+                        : x + (int64_t)__builtin_amdgcn_readlane(path.node, e - (W - 1)) * a.row_bytes;
+  }
+  if (c >= a.row_bytes) return;
+  u32x4_t rows[W - 1];
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) rows[j] = *reinterpret_cast<const u32x4_t*>(from[j]);
+  uint8_t* dp = a.cpool + (int64_t)po * a.cpage_bytes + c;
+#pragma unroll
+  for (int j = 0; j < W - 1; ++j) *reinterpret_cast<u32x4_t*>(dp + (int64_t)j * a.row_bytes) = rows[j];
+}
+
+template <typename In> static hipError_t launch_conv_tree_t(const ConvTreeArgs& a, hipStream_t st) {
+  constexpr int N = ConvVec<In>::N;
+  const dim3 grid((unsigned)(a.n * ((a.tokens + kConvTreeNodes - 1) / kConvTreeNodes)), (unsigned)((a.C / N + 255) / 256));
+  if (a.W == 2) hipLaunchKernelGGL((conv_tree_kernel<In, 2>), grid, dim3(256), 0, st, a);
+  else if (a.W == 3) hipLaunchKernelGGL((conv_tree_kernel<In, 3>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((conv_tree_kernel<In, 4>), grid, dim3(256), 0, st, a);
+  return hipGetLastError();
+}
+hipError_t launch_conv_tree(const ConvTreeArgs& a, hipStream_t st) {
+  return a.in_bf16 ? launch_conv_tree_t<uint16_t>(a, st) : launch_conv_tree_t<float>(a, st);
+}
+hipError_t launch_conv_commit(const ConvCommitArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)a.n, (unsigned)((a.row_bytes / 16 + 255) / 256));
+  if (a.W == 2) hipLaunchKernelGGL((conv_commit_kernel<2>), grid, dim3(256), 0, st, a);
+  else if (a.W == 3) hipLaunchKernelGGL((conv_commit_kernel<3>), grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((conv_commit_kernel<4>), grid, dim3(256), 0, st, a);
+  return hipGetLastError();
 }
 
 template <typename In>

@@ -19,6 +19,11 @@ kda_status hip_fail(hipError_t e, const char* what);
 inline bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool valid_dtype(int d) { return d == KDA_F32 || d == KDA_BF16; }
 
+// KDA_VALIDATE=1: device tables are read back and checked before a call.
+bool validating();
+
+kda_status check_conv_pool(const kda_conv_pool* p);
+
 // Copies a host table into the workspace through kernel arguments.
 kda_status ship_metadata(uint8_t* ws, const std::vector<uint8_t>& blob, hipStream_t st);
 

@@ -56,6 +56,7 @@ struct KvAppendArgs {
   int32_t Hq;
   int32_t kv_wgs;  // workgroups of the key/value part
   int32_t rows;
+  const int32_t* parent;  // [n][tokens]: the rows of a request are a tree's nodes
   KvBatch b;
 };
 static_assert(sizeof(KvAppendArgs) <= 4096, "kernel argument budget");
@@ -83,9 +84,19 @@ struct AttnArgs {
   int32_t rows, units, tile_rows;
   int32_t splits, min_blocks;  // workgroups that share the blocks a tile sees; a share's least
   int32_t out_bf16;
+  const int32_t* parent;  // [n][tokens]: the rows of a request are a tree's nodes
   KvBatch b;
 };
 static_assert(sizeof(AttnArgs) <= 4096, "kernel argument budget");
+
+// The accepted paths of drafted trees, kept.
+struct KvCommitArgs {
+  KvCache c;
+  const int32_t* pos;
+  const int32_t* path;   // [n][tokens]
+  const int32_t* count;  // [n]
+  int32_t n, tokens;
+};
 
 constexpr int kTileRows = 128;   // rows of a tile of the tiled kernel
 constexpr int kFewRows = 64;     // rows of a sequence and head that are few to it
@@ -99,6 +110,7 @@ hipError_t launch_attn_tiled(int D, bool in_bf16, bool int8, const AttnArgs& a, 
 hipError_t launch_attn_join(int D, const AttnArgs& a, hipStream_t st);
 // one: the one-token step's kernel (b.pos set, b.tokens == 1)
 hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st);
+hipError_t launch_kv_commit(int D, bool int8, const KvCommitArgs& a, hipStream_t st);
 hipError_t launch_kv_read(int D, bool bf16, bool int8, const KvReadArgs& a, int64_t units, hipStream_t st);
 
 // ---- device side --------------------------------------------------------------

@@ -15,6 +15,7 @@
 // 120 registers instead of 61, and a CU half the waves).
 #include "kda_device.h"
 #include "kda_kv.h"
+#include "kda_tree.h"
 
 namespace kda {
 
@@ -120,17 +121,28 @@ __device__ __forceinline__ uint32_t codes_word(const float* x, float s, float in
 }
 __device__ __forceinline__ uint32_t top_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
-template <int D, int WAVES, typename In> __device__ __forceinline__ void rotate_q(const KvAppendArgs& a, int tid) {
+// TREE, here and below: a request's rows are the nodes of a drafted tree, at slots
+// start + t, rotated at position start + depth.
+template <int D, int WAVES, typename In, bool TREE = false>
+__device__ __forceinline__ void rotate_q(const KvAppendArgs& a, int tid) {
   constexpr int SL = D / 16, HG = 64 / SL;  // slots of a row; heads a wave holds at a time
   const int row = uni((blockIdx.x - a.kv_wgs) * WAVES + (tid >> 6));  // a wave each
   if (row >= a.rows) return;
   const KvSeq s = kv_seq_uniform(a.b, uni(kv_find_row(a.b, row)));
-  const int64_t pos = (int64_t)s.start + (row - s.row);
+  int64_t pos = (int64_t)s.start + (row - s.row);
+  bool none = false, bad = false;  // the row is no node, or a bad one
+  if constexpr (TREE) {
+    const TreeNode tree = tree_node(a.parent + s.row, s.len);
+    const int t = row - s.row;
+    pos = (int64_t)s.start + __builtin_amdgcn_readlane(tree.depth, t);
+    none = !(__ballot(tree.node) >> t & 1);
+    bad = __ballot(tree.bad) >> t & 1;
+  }
   const int i = tid % SL, hg = (tid / SL) % HG;
   const Slot sl = slot_of(a, i);
   const In* q = reinterpret_cast<const In*>(a.q) + row * a.q_ld;
   In* out = reinterpret_cast<In*>(a.q_out) + (int64_t)row * a.Hq * D;
-  const bool off = s.start < 0, lost = !off && a.cos && pos >= a.num_pos;
+  const bool off = s.start < 0 || none, lost = !off && (bad || (a.cos && pos >= a.num_pos));
   float co[8], si[8];
   if (sl.turns && !off && !lost) {
     load8(a.cos + pos * (a.rot >> 1) + 8 * i, co);
@@ -154,14 +166,15 @@ template <int D, int WAVES, typename In> __device__ __forceinline__ void rotate_
   }
 }
 
-template <int D, typename In, int EB> __global__ __launch_bounds__(2 * D, 8) void kv_append_kernel(KvAppendArgs a) {
+template <int D, typename In, int EB, bool TREE>
+__global__ __launch_bounds__(2 * D, 8) void kv_append_kernel(KvAppendArgs a) {
   constexpr int SL = D / 16, PART = kKvBlock * D * EB, NE = 16 / EB, NT = 2 * D;
   constexpr int NU = PART / 16 / NT;  // 16-byte units of the part a thread moves
   __shared__ __align__(16) uint8_t blk[PART];
   __shared__ uint32_t top[NT / 64];
   const int tid = threadIdx.x;
   if ((int)blockIdx.x >= a.kv_wgs) {
-    rotate_q<D, NT / 64, In>(a, tid);
+    rotate_q<D, NT / 64, In, TREE>(a, tid);
     return;
   }
   const int p = blockIdx.x & 1, h = (blockIdx.x >> 1) % a.c.H, unit = (blockIdx.x >> 1) / a.c.H;
@@ -170,7 +183,7 @@ template <int D, typename In, int EB> __global__ __launch_bounds__(2 * D, 8) voi
   if (s.start < 0) return;
   const int bi = s.start / kKvBlock + (unit - s.unit);
   int64_t hi = min((int64_t)s.start + s.len, (int64_t)a.c.max_pages * a.c.page_tokens);
-  if (a.cos) hi = min(hi, a.num_pos);
+  if (!TREE && a.cos) hi = min(hi, a.num_pos);
   const int64_t p0 = (int64_t)bi * kKvBlock;
   const int t0 = max(s.start - (int)p0, 0), t1 = (int)min(hi - p0, (int64_t)kKvBlock);
   if (t1 <= t0) return;
@@ -196,22 +209,31 @@ template <int D, typename In, int EB> __global__ __launch_bounds__(2 * D, 8) voi
   const int kt = tid / SL, vt = tid / (D / 4) * 4, vc = tid % (D / 4) * 4;
   const Slot sl = slot_of(a, tid % SL);
   const bool kin = p == 0 && kt >= t0 && kt < t1;
+  const int node0 = (int)p0 - s.start;  // tree entry of the block's token 0
+  uint64_t good = ~0ull;                // entries that are stored; the others' slots are zeros
+  int64_t at = p0 + kt;                 // the key's position
+  if constexpr (TREE) {
+    const TreeNode tree = tree_node(a.parent + s.row, s.len);
+    good = __ballot(tree.good() && !(a.cos && (int64_t)s.start + tree.depth >= a.num_pos));
+    at = (int64_t)s.start + __shfl(tree.depth, max(node0 + kt, 0) & 63);
+  }
+  auto stored = [&](int t) { return !TREE || (good >> (node0 + t) & 1); };  // of a block's token that the call brings
   if (p == 0) {
-    if (kin) {
+    if (kin && stored(kt)) {
       const In* from = reinterpret_cast<const In*>(a.k) + (row0 + kt) * a.k_ld + h * D;
       load8(from + 8 * sl.a, x[0]);
       load8(from + 8 * sl.b, x[2]);
       if (sl.turns) {
         float co[8], si[8];
-        load8(a.cos + (p0 + kt) * (a.rot >> 1) + 8 * (tid % SL), co);
-        load8(a.sin + (p0 + kt) * (a.rot >> 1) + 8 * (tid % SL), si);
+        load8(a.cos + at * (a.rot >> 1) + 8 * (tid % SL), co);
+        load8(a.sin + at * (a.rot >> 1) + 8 * (tid % SL), si);
         rotate_slot(a.interleaved, co, si, x[0], x[2]);
       }
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (vt + j >= t0 && vt + j < t1)
+      if (vt + j >= t0 && vt + j < t1 && stored(vt + j))
         load4(reinterpret_cast<const In*>(a.v) + (row0 + vt + j) * a.v_ld + h * D + vc, x[j]);
   }
   bool grown = false;
@@ -458,10 +480,114 @@ template <int D, typename Out, int EB> __global__ __launch_bounds__(256) void kv
   }
 }
 
+// Keeps the accepted path of a tree: the row of slot pos + path[i] goes to slot pos + i.
+// A workgroup takes the K or the V part of one head of a request: the up to three blocks
+// a tree touches go to LDS, and the 16-byte units that change are put together from
+// there, so nothing is overwritten before it is read.  Int8: a block takes the largest
+// scale of the blocks its rows come from (its own, where it holds older rows, among them);
+// rows of that scale keep their codes.
+// Bound by the chain of loads (position, path, page, block) and by launching.
+template <int D, int EB> __global__ __launch_bounds__(256) void kv_commit_kernel(KvCommitArgs a) {
+  constexpr int PART = kKvBlock * D * EB, NU = PART / 16, NE = 16 / EB, NB = 3;
+  __shared__ __align__(16) uint8_t blk[NB][PART];
+  __shared__ uint8_t from[NB * kKvBlock];  // the slot (from the first block on) a slot's row comes from
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int p = blockIdx.x & 1, h = (blockIdx.x >> 1) % a.c.H, req = (blockIdx.x >> 1) / a.c.H;
+  const int pos = uni(a.pos[req]), count = uni(a.count[req]);
+  if (pos < 0 || count <= 0) return;
+  const TreePath path = tree_path(a.path + (int64_t)req * a.tokens, count, a.tokens);
+  if (!path.valid || (int64_t)pos + a.tokens > (int64_t)a.c.max_pages * a.c.page_tokens) return;
+  if (!__any(lane < count && path.node != lane)) return;  // every row is in its place
+  const int b0 = pos / kKvBlock, o = pos % kKvBlock;
+  const int last = __builtin_amdgcn_readlane(path.node, count - 1), nb = (o + last) / kKvBlock + 1;  // blocks read
+  const int nw = (o + count - 1) / kKvBlock + 1;                                                    // blocks written
+  uint8_t* block[NB] = {};
+  float* scale[NB] = {};
+  float so[NB] = {}, sn[NB] = {};
+  bool bad = false;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    // a block between two that hold accepted rows may hold none: its page need not exist
+    const bool used = b < nb && (b < nw || __any(lane < count && (o + path.node) / kKvBlock == b));
+    if (!used) continue;
+    block[b] = kv_block<D, EB>(a.c, req, b0 + b, h, &scale[b]);
+    bad |= !block[b];
+  }
+  if (bad) return;
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (!block[b]) continue;
+    block[b] += p * PART;
+    if constexpr (EB == 1) so[b] = scale[b][p];
+    for (int u = tid; u < NU; u += 256) *reinterpret_cast<u32x4_t*>(&blk[b][16 * u]) = *reinterpret_cast<const u32x4_t*>(block[b] + 16 * u);
+  }
+  for (int i = tid; i < NB * kKvBlock; i += 256) from[i] = (uint8_t)i;
+  __syncthreads();
+  if (tid < 64 && lane < count) from[o + lane] = (uint8_t)(o + path.node);
+  if constexpr (EB == 1) {
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      // bits: a NaN is larger than any number
+      uint32_t top = b == 0 && o ? __float_as_uint(so[0]) : 0u;
+#pragma unroll
+      for (int f = 0; f < NB; ++f)
+        if (__any(lane < count && (o + lane) / kKvBlock == b && (o + path.node) / kKvBlock == f)) top = max(top, __float_as_uint(so[f]));
+      sn[b] = __uint_as_float(top);
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int b = 0; b < NB; ++b) {
+    if (b >= nw) continue;
+    const bool grown = EB == 1 && __float_as_uint(sn[b]) != __float_as_uint(so[b]);
+    for (int u = tid; u < NU; u += 256) {
+      // tokens of the unit: one (keys), or 4 g .. and 16 + 4 g .. (values)
+      const int first = p == 0 ? u / (D * EB) * 16 + u % 16 : u / 16 % 4 * 4;
+      u32x4_t w = *reinterpret_cast<const u32x4_t*>(&blk[b][16 * u]);
+      bool some = false;
+#pragma unroll
+      for (int e = 0; e < NE; ++e) {
+        const int t = p == 0 ? first : first + (e & 3) + 16 * ((e & 7) >> 2), slot = b * kKvBlock + t;
+        const int src = from[slot], sb = src / kKvBlock, stk = src % kKvBlock;
+        if (slot >= o + count || (src == slot && !grown)) continue;
+        some = true;
+        // the same channel of the source's token: its unit and place in it
+        const int su = p == 0 ? u / 16 % (D * EB / 16) * 16 + (stk >> 4) * (D * EB) + (stk & 15)
+                              : u / 64 * 64 + ((stk & 15) >> 2) * 16 + u % 16;
+        const int se = p == 0 ? e : (e & ~7) + (stk & 3) + 4 * (stk >> 4);
+        if constexpr (EB == 1) {
+          uint32_t c = blk[sb][16 * su + se];
+          const float s = sb == 0 ? so[0] : sb == 1 ? so[1] : so[2];
+          if (__float_as_uint(s) != __float_as_uint(sn[b])) c = (uint32_t)quant((float)(int8_t)c * s, sn[b]) & 255u;
+          w[e / 4] = (w[e / 4] & ~(255u << (8 * (e % 4)))) | c << (8 * (e % 4));
+        } else {
+          const uint32_t c = *reinterpret_cast<const uint16_t*>(&blk[sb][16 * su + 2 * se]);
+          w[e / 2] = (w[e / 2] & ~(0xffffu << (16 * (e % 2)))) | c << (16 * (e % 2));
+        }
+      }
+      if (some) *reinterpret_cast<u32x4_t*>(block[b] + 16 * u) = w;
+    }
+    if (EB == 1 && tid == 0 && grown) scale[b][p] = sn[b];
+  }
+}
+
+hipError_t launch_kv_commit(int D, bool int8, const KvCommitArgs& a, hipStream_t st) {
+  const dim3 g((unsigned)(a.n * a.c.H * 2)), b(256);
+  if (D == 128) {
+    if (int8) hipLaunchKernelGGL((kv_commit_kernel<128, 1>), g, b, 0, st, a);
+    else hipLaunchKernelGGL((kv_commit_kernel<128, 2>), g, b, 0, st, a);
+  } else {
+    if (int8) hipLaunchKernelGGL((kv_commit_kernel<64, 1>), g, b, 0, st, a);
+    else hipLaunchKernelGGL((kv_commit_kernel<64, 2>), g, b, 0, st, a);
+  }
+  return hipGetLastError();
+}
+
 template <int D, typename In, int EB>
 static void launch_append_t(const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st) {
-  if (one) hipLaunchKernelGGL((kv_append_one_kernel<D, In, EB>), dim3((unsigned)wgs), dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((kv_append_kernel<D, In, EB>), dim3((unsigned)wgs), dim3(2 * D), 0, st, a);
+  if (a.parent) hipLaunchKernelGGL((kv_append_kernel<D, In, EB, true>), dim3((unsigned)wgs), dim3(2 * D), 0, st, a);
+  else if (one) hipLaunchKernelGGL((kv_append_one_kernel<D, In, EB>), dim3((unsigned)wgs), dim3(256), 0, st, a);
+  else hipLaunchKernelGGL((kv_append_kernel<D, In, EB, false>), dim3((unsigned)wgs), dim3(2 * D), 0, st, a);
 }
 template <int D>
 static void launch_append_d(bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st) {

@@ -156,11 +156,6 @@ kda_status ship_seqs(const std::vector<KvSeq>& seqs, void* ws, KvBatch* b, hipSt
   return ship_metadata(static_cast<uint8_t*>(ws), blob, st);
 }
 
-bool validating() {
-  const char* v = std::getenv("KDA_VALIDATE");
-  return v && v[0] == '1';
-}
-
 // KDA_VALIDATE=1: the pages a call needs, read back and checked.  `write`: the
 // pages that receive tokens have to be distinct between requests.
 kda_status check_pages(const kda_kv_pool* p, const int32_t* table, int32_t max_pages,
@@ -273,10 +268,10 @@ KvAppendArgs append_args(const kda_kv_pool* p, const kda_rope* rope, const void*
 // workgroup of 2 d threads takes a part (K or V) of a block.  q takes a wave a row.
 kda_status run_append(const kda_kv_pool* p, kda_dtype in, KvAppendArgs* a, int64_t units, hipStream_t st) {
   const int32_t d = p->head_dim, H = p->num_heads;
-  const bool one = a->b.pos && a->b.tokens == 1;
+  const bool one = a->b.pos && a->b.tokens == 1 && !a->parent;
   a->kv_wgs = (int32_t)(one ? a->b.n * (((int64_t)H * d + 1023) / 1024) : units * H * 2);
   const int64_t waves = one ? 4 : 2 * d / 64, wgs = a->kv_wgs + (a->Hq ? (a->rows + waves - 1) / waves : 0);
-  Launch L("kda_kv_append", st);
+  Launch L(a->parent ? "kda_kv_append_tree" : "kda_kv_append", st);
   const hipError_t e = launch_kv_append(d, in == KDA_BF16, p->dtype == KDA_INT8, *a, wgs, one, st);
   return e == hipSuccess ? ok() : hip_fail(e, "append launch");
 }
@@ -443,7 +438,103 @@ template <typename F> kda_status guarded(F f) {
   }
 }
 
+// The slots a request's tree takes, read back: up to its last node.
+kda_status tree_seqs(const int32_t* pos, const int32_t* parent, int32_t n, int32_t tokens, std::vector<KvSeq>* seqs,
+                     hipStream_t st) {
+  kda_status s = step_seqs(pos, n, tokens, seqs, st);
+  if (s != KDA_OK) return s;
+  std::vector<int32_t> p((size_t)n * tokens);
+  hipError_t e = hipMemcpyAsync(p.data(), parent, p.size() * 4, hipMemcpyDeviceToHost, st);
+  if (e == hipSuccess) e = hipStreamSynchronize(st);
+  if (e != hipSuccess) return hip_fail(e, "tree read-back");
+  for (int32_t i = 0; i < n; ++i) {
+    KvSeq& q = (*seqs)[i];
+    std::vector<bool> good(tokens, false);
+    for (int32_t t = 0; t < tokens; ++t) {
+      const int32_t up = p[(size_t)i * tokens + t];
+      if (up < -1) continue;
+      if (up >= t || (up >= 0 && !good[up]))
+        return fail(KDA_ERR_SEQ, "request %d: parent[%d] = %d is not a node before it", i, t, up);
+      good[t] = true;
+      q.len = t + 1;
+    }
+    if (!good[q.len - 1]) q.len = 0;
+  }
+  return KDA_OK;
+}
+
+// The attention step over n requests of `tokens` rows each; parent: the rows are a tree.
+kda_status attend_step(const char* what, const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld,
+                       void* o, kda_dtype out_dtype, int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
+                       int32_t n, int32_t tokens, const int32_t* pos, const int32_t* parent, bool tree,
+                       const int32_t* page_table, int32_t max_pages, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+  kda_status s = check_attn(pool, in_dtype, out_dtype, num_q_heads, scale, window, sinks);
+  if (s != KDA_OK) return s;
+  s = check_step(what, pos, n, tokens);
+  if (s != KDA_OK || n == 0) return s == KDA_OK ? ok() : s;
+  if (tree && !parent) return fail(KDA_ERR_NULL, "%s: parent is NULL", what);
+  s = check_table(pool, page_table, max_pages);
+  if (s != KDA_OK) return s;
+  const int64_t rows = (int64_t)n * tokens;
+  s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
+  if (s != KDA_OK) return s;
+  const AttnPlan pl = plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks);
+  if (pl.units * pool->num_heads * pl.splits > kMaxGroups || rows * num_q_heads > kMaxTokens)
+    return fail(KDA_ERR_SHAPE, "too much work for one call");
+  s = check_workspace(workspace, workspace_bytes, std::max<size_t>(256, pl.bytes));
+  if (s != KDA_OK) return s;
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (validating()) {
+    std::vector<KvSeq> seqs;
+    s = tree ? tree_seqs(pos, parent, n, tokens, &seqs, st) : step_seqs(pos, n, tokens, &seqs, st);
+    if (s == KDA_OK) s = check_pages(pool, page_table, max_pages, seqs, window, sinks, false, true, st);
+    if (s != KDA_OK) return s;
+  }
+  AttnArgs a = attn_args(pool, q, q_ld, o, out_dtype, num_q_heads, scale, window, sinks, page_table, max_pages, rows,
+                         pl, workspace);
+  a.b = step_batch(pos, n, tokens, (int32_t)(pl.units / n));
+  a.parent = parent;
+  return run_attn(pool, in_dtype, a, pl.decode, what, st);
+}
+
+// The append of n requests of `tokens` rows each; parent: the rows are a tree.
+kda_status append_step(const char* what, const kda_kv_pool* pool, const kda_rope* rope, const void* q, const void* k,
+                       const void* v, kda_dtype in_dtype, int64_t q_ld, int64_t k_ld, int64_t v_ld, void* q_out,
+                       int32_t num_q_heads, int32_t n, int32_t tokens, const int32_t* pos, const int32_t* parent,
+                       bool tree, const int32_t* page_table, int32_t max_pages, void* stream) {
+  kda_status s = check_append(pool, rope, q, in_dtype, q_out, num_q_heads);
+  if (s != KDA_OK) return s;
+  s = check_step(what, pos, n, tokens);
+  if (s != KDA_OK || n == 0) return s == KDA_OK ? ok() : s;
+  if (tree && !parent) return fail(KDA_ERR_NULL, "%s: parent is NULL", what);
+  s = check_table(pool, page_table, max_pages);
+  if (s != KDA_OK) return s;
+  const int64_t rows = (int64_t)n * tokens;
+  s = check_append_rows(pool, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads, rows);
+  if (s != KDA_OK) return s;
+  const int per = (tokens + kKvBlock - 2) / kKvBlock + 1;  // blocks `tokens` consecutive tokens can touch
+  if ((int64_t)n * per * pool->num_heads * 2 + (rows + 1) / 2 > kMaxGroups)
+    return fail(KDA_ERR_SHAPE, "too much work for one call");
+  hipStream_t st = reinterpret_cast<hipStream_t>(stream);
+  if (validating()) {
+    std::vector<KvSeq> seqs;
+    s = tree ? tree_seqs(pos, parent, n, tokens, &seqs, st) : step_seqs(pos, n, tokens, &seqs, st);
+    if (s == KDA_OK) s = check_pages(pool, page_table, max_pages, seqs, 0, 0, true, false, st);
+    if (s != KDA_OK) return s;
+  }
+  KvAppendArgs a = append_args(pool, rope, q, k, v, q_ld, k_ld, v_ld, q_out, num_q_heads, page_table, max_pages, rows);
+  a.b = step_batch(pos, n, tokens, per);
+  a.parent = parent;
+  return run_append(pool, in_dtype, &a, (int64_t)n * per, st);
+}
+
 }  // namespace
+
+bool kda::validating() {
+  const char* v = std::getenv("KDA_VALIDATE");
+  return v && v[0] == '1';
+}
 
 extern "C" {
 
@@ -506,29 +597,58 @@ kda_status kda_kv_append_step(const kda_kv_pool* pool, const kda_rope* rope, con
                               void* q_out, int32_t num_q_heads, int32_t n, int32_t tokens, const int32_t* pos,
                               const int32_t* page_table, int32_t max_pages, void* stream) {
   return guarded([&]() -> kda_status {
-    kda_status s = check_append(pool, rope, q, in_dtype, q_out, num_q_heads);
+    return append_step("kda_kv_append_step", pool, rope, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads, n,
+                       tokens, pos, nullptr, false, page_table, max_pages, stream);
+  });
+}
+
+kda_status kda_kv_append_tree(const kda_kv_pool* pool, const kda_rope* rope, const void* q, const void* k,
+                              const void* v, kda_dtype in_dtype, int64_t q_ld, int64_t k_ld, int64_t v_ld,
+                              void* q_out, int32_t num_q_heads, int32_t n, int32_t tokens, const int32_t* pos,
+                              const int32_t* parent, const int32_t* page_table, int32_t max_pages, void* stream) {
+  return guarded([&]() -> kda_status {
+    return append_step("kda_kv_append_tree", pool, rope, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads, n,
+                       tokens, pos, parent, true, page_table, max_pages, stream);
+  });
+}
+
+kda_status kda_kv_commit(const kda_kv_pool* pool, int32_t n, int32_t tokens, const int32_t* pos, const int32_t* path,
+                         const int32_t* count, const int32_t* page_table, int32_t max_pages, void* stream) {
+  return guarded([&]() -> kda_status {
+    kda_status s = check_kv_pool(pool);
     if (s != KDA_OK) return s;
-    s = check_step("kda_kv_append_step", pos, n, tokens);
+    s = check_step("kda_kv_commit", pos, n, tokens);
     if (s != KDA_OK || n == 0) return s == KDA_OK ? ok() : s;
+    if (!path || !count) return fail(KDA_ERR_NULL, "kda_kv_commit: path or count is NULL");
     s = check_table(pool, page_table, max_pages);
     if (s != KDA_OK) return s;
-    const int64_t rows = (int64_t)n * tokens;
-    s = check_append_rows(pool, q, k, v, in_dtype, q_ld, k_ld, v_ld, q_out, num_q_heads, rows);
-    if (s != KDA_OK) return s;
-    const int per = (tokens + kKvBlock - 2) / kKvBlock + 1;  // blocks `tokens` consecutive tokens can touch
-    if ((int64_t)n * per * pool->num_heads * 2 + (rows + 1) / 2 > kMaxGroups)
-      return fail(KDA_ERR_SHAPE, "too much work for one call");
+    if ((int64_t)n * pool->num_heads * 2 > kMaxGroups) return fail(KDA_ERR_SHAPE, "too much work for one call");
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (validating()) {
+      std::vector<int32_t> c((size_t)n), p((size_t)n * tokens);
+      hipError_t e = hipMemcpyAsync(c.data(), count, c.size() * 4, hipMemcpyDeviceToHost, st);
+      if (e == hipSuccess) e = hipMemcpyAsync(p.data(), path, p.size() * 4, hipMemcpyDeviceToHost, st);
+      if (e == hipSuccess) e = hipStreamSynchronize(st);
+      if (e != hipSuccess) return hip_fail(e, "path read-back");
       std::vector<KvSeq> seqs;
       s = step_seqs(pos, n, tokens, &seqs, st);
-      if (s == KDA_OK) s = check_pages(pool, page_table, max_pages, seqs, 0, 0, true, false, st);
+      if (s != KDA_OK) return s;
+      for (int32_t i = 0; i < n; ++i) {
+        if (c[i] < 0 || c[i] > tokens) return fail(KDA_ERR_SEQ, "request %d: count %d outside [0, tokens]", i, c[i]);
+        for (int32_t j = 0, before = -1; j < c[i]; ++j) {
+          const int32_t t = p[(size_t)i * tokens + j];
+          if (t <= before || t >= tokens) return fail(KDA_ERR_SEQ, "request %d: path[%d] = %d", i, j, t);
+          before = t;
+        }
+        seqs[i].len = c[i] ? p[(size_t)i * tokens + c[i] - 1] + 1 : 0;
+      }
+      s = check_pages(pool, page_table, max_pages, seqs, 0, 0, true, false, st);
       if (s != KDA_OK) return s;
     }
-    KvAppendArgs a = append_args(pool, rope, q, k, v, q_ld, k_ld, v_ld, q_out, num_q_heads, page_table, max_pages,
-                                 rows);
-    a.b = step_batch(pos, n, tokens, per);
-    return run_append(pool, in_dtype, &a, (int64_t)n * per, st);
+    const KvCommitArgs a{cache_of(pool, page_table, max_pages), pos, path, count, n, tokens};
+    Launch L("kda_kv_commit", st);
+    const hipError_t e = launch_kv_commit(pool->head_dim, pool->dtype == KDA_INT8, a, st);
+    return e == hipSuccess ? ok() : hip_fail(e, "commit launch");
   });
 }
 
@@ -645,31 +765,24 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
                            int32_t n, int32_t tokens, const int32_t* pos, const int32_t* page_table,
                            int32_t max_pages, void* workspace, size_t workspace_bytes, void* stream) {
   return guarded([&]() -> kda_status {
-    kda_status s = check_attn(pool, in_dtype, out_dtype, num_q_heads, scale, window, sinks);
-    if (s != KDA_OK) return s;
-    s = check_step("kda_attn_decode", pos, n, tokens);
-    if (s != KDA_OK || n == 0) return s == KDA_OK ? ok() : s;
-    s = check_table(pool, page_table, max_pages);
-    if (s != KDA_OK) return s;
-    const int64_t rows = (int64_t)n * tokens;
-    s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
-    if (s != KDA_OK) return s;
-    const AttnPlan pl = plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks);
-    if (pl.units * pool->num_heads * pl.splits > kMaxGroups || rows * num_q_heads > kMaxTokens)
-      return fail(KDA_ERR_SHAPE, "too much work for one call");
-    s = check_workspace(workspace, workspace_bytes, std::max<size_t>(256, pl.bytes));
-    if (s != KDA_OK) return s;
-    hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-    if (validating()) {
-      std::vector<KvSeq> seqs;
-      s = step_seqs(pos, n, tokens, &seqs, st);
-      if (s == KDA_OK) s = check_pages(pool, page_table, max_pages, seqs, window, sinks, false, true, st);
-      if (s != KDA_OK) return s;
-    }
-    AttnArgs a = attn_args(pool, q, q_ld, o, out_dtype, num_q_heads, scale, window, sinks, page_table, max_pages,
-                           rows, pl, workspace);
-    a.b = step_batch(pos, n, tokens, (int32_t)(pl.units / n));
-    return run_attn(pool, in_dtype, a, pl.decode, "kda_attn_decode", st);
+    return attend_step("kda_attn_decode", pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, scale, window, sinks, n,
+                       tokens, pos, nullptr, false, page_table, max_pages, workspace, workspace_bytes, stream);
+  });
+}
+
+size_t kda_attn_tree_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n, int32_t tokens,
+                                     int32_t max_pages, int32_t window, int32_t sinks) {
+  return kda_attn_decode_workspace_bytes(pool, num_q_heads, n, tokens, max_pages, window, sinks);
+}
+
+kda_status kda_attn_tree(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld, void* o,
+                         kda_dtype out_dtype, int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
+                         int32_t n, int32_t tokens, const int32_t* pos, const int32_t* parent,
+                         const int32_t* page_table, int32_t max_pages, void* workspace, size_t workspace_bytes,
+                         void* stream) {
+  return guarded([&]() -> kda_status {
+    return attend_step("kda_attn_tree", pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, scale, window, sinks, n,
+                       tokens, pos, parent, true, page_table, max_pages, workspace, workspace_bytes, stream);
   });
 }
 

@@ -216,6 +216,80 @@ struct ConvUpdateArgs {
   int32_t out_bf16;
 };
 
+// The recurrence along the trees of n requests: row r * tokens + t is entry t of request
+// r's tree, parent its parents.
+struct TreeArgs {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  void* o;
+  const int32_t* parent;   // device [n][tokens]
+  const int32_t* page_in;  // device [n]
+  const uint8_t* pool;
+  int64_t page_bytes;
+  int32_t num_pages;
+  int32_t H;
+  int32_t out_bf16;
+  int32_t n;
+  int32_t tokens;
+};
+
+// The state after each request's accepted path.
+struct StateCommitArgs {
+  const void* k;
+  const void* v;
+  const void* g;
+  const void* beta;
+  const int32_t* path;      // device [n][tokens]
+  const int32_t* count;     // device [n]
+  const int32_t* page_in;   // device [n]
+  const int32_t* page_out;  // device [n]
+  uint8_t* pool;
+  int64_t page_bytes;
+  int32_t num_pages;
+  int32_t H;
+  int32_t n;
+  int32_t tokens;
+};
+
+// The convolution along the trees of n requests, and the window after their accepted paths.
+struct ConvTreeArgs {
+  const void* x;
+  const float* w;
+  void* y;
+  const int32_t* parent;  // device [n][tokens]
+  const int32_t* page_in;
+  const uint8_t* cpool;
+  int64_t cpage_bytes;
+  int32_t num_pages;
+  int32_t n;
+  int32_t tokens;
+  int32_t C;
+  int32_t W;
+  int32_t in_bf16;
+  int32_t out_bf16;
+};
+struct ConvCommitArgs {
+  const void* x;
+  const int32_t* path;   // device [n][tokens]
+  const int32_t* count;  // device [n]
+  const int32_t* page_in;
+  const int32_t* page_out;
+  uint8_t* cpool;
+  int64_t cpage_bytes;
+  int32_t num_pages;
+  int32_t n;
+  int32_t tokens;
+  int32_t row_bytes;  // of an input
+  int32_t W;
+};
+
+hipError_t launch_tree(int D, bool bf16, const TreeArgs& a, hipStream_t st);
+hipError_t launch_state_commit(int D, bool bf16, const StateCommitArgs& a, hipStream_t st);
+hipError_t launch_conv_tree(const ConvTreeArgs& a, hipStream_t st);
+hipError_t launch_conv_commit(const ConvCommitArgs& a, hipStream_t st);
 hipError_t launch_copy(const CopyArgs& a, hipStream_t st);
 hipError_t launch_conv(const ConvArgs& a, int32_t total_chunks, hipStream_t st);
 hipError_t launch_conv_update(const ConvUpdateArgs& a, hipStream_t st);

@@ -602,6 +602,216 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
                            void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Trees of drafted tokens: verification in one step of several continuations that
+ * share prefixes, instead of one chain (kda_decode_verify, kda_attn_decode with tokens
+ * > 1).  A request drafts `tokens` entries (1..64; a fixed number for a call, so that a
+ * captured step follows its trees):
+ *   parent : int32 DEVICE array [n][tokens].  Entry t of a request is a node if
+ *            parent[t] is -1 (it follows the last cached token; a tree may have several
+ *            such roots) or an earlier entry s < t that is a node (it follows node s).
+ *            Below -1 there is no node (-2 is usual, for requests that drafted fewer):
+ *            its input rows are not read and its output rows are 0.  Device-side: a
+ *            parent that is not before its child, or no node, makes the child and all
+ *            that follow it bad: NaN in their output rows, and nothing is stored of them.
+ *            With KDA_VALIDATE=1 the attention, append and commit calls check the trees
+ *            (paths) on the host and refuse bad ones with KDA_ERR_SEQ.
+ * A node's way is the nodes from its root to itself; its depth is their number less
+ * one.  Row r * tokens + t of a tensor is entry t of request r.
+ *
+ * A step verifies a tree with kda_short_conv_tree and kda_decode_tree in the recurrent
+ * layers (which leave window and state pages as they are) and kda_kv_append_tree and
+ * kda_attn_tree in the softmax layers.  The tokens then accepted are a way, from the
+ * root on, given to the commits:
+ *   path   : int32 DEVICE array [n][tokens], its first count[r] entries are the accepted
+ *            nodes of request r in order (so they ascend); the rest is not read.
+ *   count  : int32 DEVICE array [n], 0..tokens.
+ * Device-side: a count outside [0, tokens], or a path that does not ascend within the
+ * tree, leaves the request's pages as they are.
+ */
+
+/*
+ * The recurrence along trees: o of every node, as if the tokens of its way had been
+ * decoded one after the other from the state page_in[r] (kda_decode_step's formulas).
+ * No state is written; the entering one is read once, whatever the number of nodes.
+ *   q, k, g : [n*tokens, H, d_k]; v, o : [n*tokens, H, d_v]; beta : [n*tokens, H]; q, k,
+ *   v, g and o 16-byte aligned, o not overlapping an input; page_in : [n] int32 DEVICE.
+ * Numerics: a node is a triangular system over its way instead of a chain of states, in
+ * fp32 (products on fp32 matrix instructions; for bf16 inputs those with the state and the
+ * gated rows in two bf16 parts each, good to 2^-15 of the terms), so rows equal a
+ * chain's to rounding, not to the bit.  g >= -104 counts, below it as -104 (whose
+ * exponential is 0 in fp32).  A node with a k, v or beta that is infinite or NaN, or a g
+ * that is NaN or +inf, is NaN in every channel, and so are the nodes that follow it;
+ * other nodes are not touched by it.
+ * Device-side: a request whose page index is outside [0, num_pages) gets NaN rows.
+ */
+kda_status kda_decode_tree(const kda_pool* pool, const void* q, const void* k, const void* v,
+                           const void* g, const void* beta, kda_dtype in_dtype, void* o,
+                           kda_dtype out_dtype, int32_t n, int32_t tokens, const int32_t* parent,
+                           const int32_t* page_in, void* stream);
+
+/*
+ * The state after the accepted path, to page_out[r] (which may equal page_in[r]): the
+ * bits that kda_decode_step gives for the path's tokens one by one.  Tensors as in
+ * kda_decode_tree.  A count of 0 copies the state.  The page_out entries are distinct
+ * and no page_out[r] equals page_in[r'] for r' != r (KDA_VALIDATE=1 checks).
+ * Device-side: a request with a page index outside [0, num_pages) touches no page.
+ */
+kda_status kda_decode_commit(const kda_pool* pool, const void* k, const void* v, const void* g,
+                             const void* beta, kda_dtype in_dtype, int32_t n, int32_t tokens,
+                             const int32_t* path, const int32_t* count, const int32_t* page_in,
+                             const int32_t* page_out, void* stream);
+
+/*
+ * The short convolution along trees: y of every node from its own input, those of its
+ * way and the window page_in[r], the bits of kda_short_conv_update for the tokens of its
+ * way one by one.  x : [n*tokens, C] (cpool->dtype), w : [C][W] fp32, y : [n*tokens, C]
+ * (out_dtype, not overlapping x), 16-byte aligned.  No window is written.  A request
+ * whose page index is outside [0, num_pages) gets NaN rows.
+ */
+kda_status kda_short_conv_tree(const kda_conv_pool* cpool, const void* x, const float* w, void* y,
+                               kda_dtype out_dtype, int32_t n, int32_t tokens,
+                               const int32_t* parent, const int32_t* page_in, void* stream);
+
+/* The window after the accepted path, to page_out[r]; rules as in kda_decode_commit. */
+kda_status kda_short_conv_commit(const kda_conv_pool* cpool, const void* x, int32_t n,
+                                 int32_t tokens, const int32_t* path, const int32_t* count,
+                                 const int32_t* page_in, const int32_t* page_out, void* stream);
+
+/*
+ * kda_kv_append_step for trees: entry t goes to cache slot pos[r] + t, rotated (with
+ * its q row) by its position, pos[r] + depth.  Entries that are no nodes, bad ones and
+ * nodes at positions past rope->num_pos store zeros in their slots (q_out: 0, NaN,
+ * NaN).  The slots from pos[r] on hold the draft until kda_kv_commit.  In a KDA_INT8
+ * cache all nodes count for the scale of the block that they share with older tokens,
+ * as in kda_kv_append, whether they are accepted or not.
+ */
+kda_status kda_kv_append_tree(const kda_kv_pool* pool, const kda_rope* rope, const void* q,
+                              const void* k, const void* v, kda_dtype in_dtype, int64_t q_ld,
+                              int64_t k_ld, int64_t v_ld, void* q_out, int32_t num_q_heads,
+                              int32_t n, int32_t tokens, const int32_t* pos,
+                              const int32_t* parent, const int32_t* page_table,
+                              int32_t max_pages, void* stream);
+
+/*
+ * kda_attn_decode for trees: node t, at position p = pos[r] + depth, sees the tokens
+ * cached before pos[r] and the nodes of its way (at their positions), by the rule of
+ * kda_attn_prefill (window and sinks count positions).  What the slots of other nodes
+ * hold does not reach it, as that section says of tokens a row does not see.  Rows of a
+ * request whose pos[r] + tokens passes max_pages * page_tokens are NaN; pos[r] < 0: 0.
+ * Weights are rounded as in kda_attn_decode.  workspace: kda_attn_tree_workspace_bytes.
+ */
+size_t kda_attn_tree_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n,
+                                     int32_t tokens, int32_t max_pages, int32_t window,
+                                     int32_t sinks);
+
+kda_status kda_attn_tree(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld,
+                         void* o, kda_dtype out_dtype, int32_t num_q_heads, float scale,
+                         int32_t window, int32_t sinks, int32_t n, int32_t tokens,
+                         const int32_t* pos, const int32_t* parent, const int32_t* page_table,
+                         int32_t max_pages, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Keeps the accepted path in the cache: the keys and values of slot pos[r] + path[i]
+ * move to slot pos[r] + i, for i < count[r].  Slots from pos[r] + count[r] on are left
+ * with what they hold.  KDA_BF16: values are copied.  KDA_INT8, per block and part: the
+ * block's scale becomes the largest of the scales of the blocks that its tokens up to
+ * pos[r] + count[r] come from; tokens of that scale keep their codes c, the others
+ * become clamp(round_half_even(c * scale_before / scale), -127, 127).
+ * Device-side: a request with pos[r] < 0, with pos[r] + tokens past max_pages *
+ * page_tokens, or with a bad page among those that the path touches is left as it is.
+ * Two requests must not share a page that is written.
+ */
+kda_status kda_kv_commit(const kda_kv_pool* pool, int32_t n, int32_t tokens, const int32_t* pos,
+                         const int32_t* path, const int32_t* count, const int32_t* page_table,
+                         int32_t max_pages, void* stream);
+
+/*
+ * Upkeep of a cache's pages on the device, so that a captured serving step can fork
+ * samples, take pages for its next tokens and let go of them without the host.  One map
+ * serves all layers, whose pools hold a page's keys and values under one number; copies
+ * (kda_kv_copy_pages) are made in each pool.
+ *   refs  : int32 DEVICE array [num_pages], the holders of each page: table entries, and
+ *           whatever else the caller counts (pages that a prefix index keeps, say).  A page
+ *           with refs <= 0 is free.
+ *   table : int32 DEVICE array [rows][max_pages], as the cache's calls take it: entry j of
+ *           a row is the page of its tokens [j * page_tokens, (j + 1) * page_tokens), or
+ *           negative.
+ * Where a call takes pages, it takes the free ones of lowest number, in the order of its
+ * rows (forks) and entries; results do not depend on the run.  Device-side: entries and
+ * rows out of range are passed over.  Calls on one map are ordered by the caller (one
+ * stream); each call on it that takes a workspace may use the same one
+ * (kda_pages_workspace_bytes, 256-byte aligned).
+ */
+typedef struct {
+  int32_t* refs;
+  int32_t* table;
+  int32_t num_pages;    /* 1 .. 2^24 */
+  int32_t rows;         /* rows * max_pages at most 2^30 */
+  int32_t max_pages;
+  int32_t page_tokens;  /* max_pages * page_tokens at most 2^30 */
+} kda_page_map;
+
+kda_status kda_page_map_check(const kda_page_map* map);
+size_t kda_pages_workspace_bytes(const kda_page_map* map);
+
+/*
+ * Room for tokens: every entry of row r that overlaps the tokens [first[r], last[r]) and
+ * holds no page gets one (refs 1).  first, last, status : int32 DEVICE arrays [rows];
+ * status[r] is the number of entries for which there was none left (they stay as they
+ * are, and so do all later ones of the call).  first >= last: nothing.
+ */
+kda_status kda_pages_reserve(const kda_page_map* map, const int32_t* first, const int32_t* last,
+                             int32_t* status, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/*
+ * Lets go of the pages of row r whose tokens all lie in [first[r], last[r]): the entry
+ * becomes -1 and the page loses a holder.  (0, max_pages * page_tokens) ends a request;
+ * (length, max_pages * page_tokens) cuts it back; (sinks, position - window + 1) drops
+ * what a sliding window has passed.
+ */
+kda_status kda_pages_free(const kda_page_map* map, const int32_t* first, const int32_t* last,
+                          void* stream);
+
+/*
+ * Forks: row dst_row[i] becomes the first tokens[i] tokens of row src_row[i].  Whole pages
+ * are shared (one more holder); the page in which the tokens end, if they do, gets a free
+ * page in its place, to be filled by kda_kv_copy_pages in each layer with the list
+ * that the call writes: copy_src, copy_dst, copy_tokens, int32 DEVICE arrays [n], the
+ * copies first, in the order of the forks, then -1, -1, 0.  Entries of src_row without a
+ * page stay without one.  All arrays int32 DEVICE [n], n <= rows.
+ *   status[i] : 0 done; 1 no free page (the row stays empty); 2 a row out of range,
+ *               src_row = dst_row, a dst_row that holds pages, or too many tokens.
+ * tokens[i] < 0: fork i takes no part.  A dst_row appears once and is no src_row of the
+ * call (KDA_VALIDATE=1 checks).  A source may appear many times.
+ */
+kda_status kda_pages_fork(const kda_page_map* map, int32_t n, const int32_t* src_row,
+                          const int32_t* dst_row, const int32_t* tokens, int32_t* copy_src,
+                          int32_t* copy_dst, int32_t* copy_tokens, int32_t* status,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Moves pages to low numbers, so that the pool's end is free: the page of highest number
+ * that only table entries hold (refs equals the entries with it) goes to the free page of
+ * lowest number, and so on while the free one is lower.  Table and refs are rewritten;
+ * the moves are written to copy_src, copy_dst (int32 DEVICE arrays [num_pages], -1 past the
+ * last), for kda_kv_copy_pages in each layer before the cache is used again.  Pages with
+ * other holders stay where they are.
+ */
+kda_status kda_pages_compact(const kda_page_map* map, int32_t* copy_src, int32_t* copy_dst,
+                             void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Copies pages of a key/value pool: src[i] to dst[i], i < n (src, dst : int32 DEVICE
+ * arrays [n]).  tokens (int32 DEVICE [n] or NULL): only the 32-token blocks that hold
+ * the page's first tokens[i] tokens; NULL: whole pages.  Pairs with a negative src[i]
+ * and pairs out of range are passed over; the destinations of the others are distinct
+ * and none of their sources (KDA_VALIDATE=1 checks, and refuses pairs out of range).
+ */
+kda_status kda_kv_copy_pages(const kda_kv_pool* pool, int32_t n, const int32_t* src,
+                             const int32_t* dst, const int32_t* tokens, void* stream);
+
+/*
  * Optional per-kernel timing (tracing aid).  When enabled, every kernel the
  * library launches is bracketed by a pair of HIP events on its own stream;
  * kda_profile_read synchronises those events and returns, per kernel name, the
