@@ -33,10 +33,8 @@
 namespace kda {
 
 // One tile: rows row0 .. of sequence s (request req) and head h, share sp of what they
-// see.  WP: parts of a weight.  TREE: the rows are the nodes of a drafted tree, at slots
-// s.start + t, which see the cached tokens before s.start by their position and of the
-// slots from it on their way.
-template <int D, int EB, int NP, int WP, bool TREE>
+// see.  WP: parts of a weight.
+template <int D, int EB, int NP, int WP>
 __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, int req, int h, int sp, int row0,
                                             uint8_t (*lds)[4 * kKvBlock * D]) {
   typedef AttnOp<EB> Op;
@@ -46,24 +44,14 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
   constexpr int RAW = kKvBlock * D * EB;    // bytes of a part in the cache
   const int lane = threadIdx.x & 63, wv = uni(threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31, rows = s.len * a.G;
-  const int tp0 = TREE ? s.start : s.start + row0 / a.G;
-  const int tp1 = TREE ? s.start + s.len - 1 : s.start + (min(rows, row0 + ROWS) - 1) / a.G;
+  const int tp0 = s.start + row0 / a.G, tp1 = s.start + (min(rows, row0 + ROWS) - 1) / a.G;
   const Reach reach = reach_of(tp0, tp1, a.window, a.sinks);
-  const Whole tile_sees = whole_of(TREE ? tp0 - 1 : tp0, tp1, a.window, a.sinks);
+  const Whole tile_sees = whole_of(tp0, tp1, a.window, a.sinks);
   const Chunk ch = chunk_of(reach.count(), a.splits, a.min_blocks, sp);
   if (ch.begin >= ch.end) return;
 
-  WaveRows wr = wave_rows(a, s, h, row0 + 32 * wv, col, D);
-  const Whole wave_sees = TREE ? tile_sees : whole_of(wr.p0, wr.p1, a.window, a.sinks);
-  uint64_t see_way = 0, nodes = 0, bad = 0;  // the lane's row's sight of the tree; all entries
-  if constexpr (TREE) {
-    const TreeNode tree = tree_node(a.parent + (int64_t)req * s.len, s.len);
-    const int tok = wr.qp - s.start;  // of the lane's row
-    wr.qp = s.start + __shfl(tree.depth, tok);
-    see_way = shfl64(tree_sight(tree, s.start, s.len, a.window, a.sinks), tok);
-    nodes = __ballot(tree.node);
-    bad = __ballot(tree.bad);
-  }
+  const WaveRows wr = wave_rows(a, s, h, row0 + 32 * wv, col, D);
+  const Whole wave_sees = whole_of(wr.p0, wr.p1, a.window, a.sinks);
   Frag qf[KS][NP];
   const float qc = load_queries<D, EB, NP>(a, wr.q + 8 * half, qf);
 
@@ -145,9 +133,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
     if (!wr.idle) {
 #pragma unroll 1
       for (int t = 0; t < kKvBlock; ++t) {
-        const int j = blk * kKvBlock + t;
-        const bool see = TREE && j >= s.start ? tree_bits(see_way, blk * kKvBlock - s.start) >> t & 1
-                                              : sees(wr.qp, j, a.window, a.sinks);
+        const bool see = sees(wr.qp, blk * kKvBlock + t, a.window, a.sinks);
         const uint8_t* vt = v + 16 * (16 * ((t & 15) >> 2) + 4 * half) + 2 * ((t & 3) + 4 * (t >> 4));
 #pragma unroll
         for (int d = 0; d < DT; ++d)
@@ -182,10 +168,7 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
     for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
       for (int p = 0; p < NP; ++p) x = Op::mma32(kf[ks], qf[ks][p], x);
-    if (!full) {
-      if constexpr (TREE) mask16_tree(x, wr.qp, s.start, see_way, blk, half, a.window, a.sinks, bs.bad);
-      else mask16(x, wr.qp, blk, half, a.window, a.sinks, bs.bad);
-    }
+    if (!full) mask16(x, wr.qp, blk, half, a.window, a.sinks, bs.bad);
     Frag pf[2][WP];
     weigh16<EB, WP, DT>(x, qc, bs, acc, m, n, l, pf);
     Frag vf[2 * DT];
@@ -216,31 +199,18 @@ __device__ __forceinline__ void attend_tile(const AttnArgs& a, const KvSeq& s, i
     if constexpr (EB == 2) {
       if (bs.bad || !tile_sees.has(blk)) purify(buf, blk);
     }
-    if (wr.idle || (!TREE && blk * kKvBlock > wr.p1)) continue;  // no rows, or past every row of the wave
+    if (wr.idle || blk * kKvBlock > wr.p1) continue;  // no rows, or past every row of the wave
     step(&lds[buf][0], blk, !bs.bad && wave_sees.has(blk), bs);
   }
 
-  float ll = half_sum(l);
+  const float ll = half_sum(l);
   int c = threadIdx.x & 31;
   asm volatile("" : "+v"(c));  // where the row goes is worked out again: kept, it would cost the loop registers
   const WaveRows to = wave_rows(a, s, h, row0 + 32 * wv, c, D);
-  if constexpr (TREE) {  // no node: 0; a bad one: NaN, through the join too
-    const int tok = to.qp - s.start;
-    if (!(nodes >> tok & 1) || (bad >> tok & 1)) {
-      const float v = nodes >> tok & 1 ? __builtin_nanf("") : 0.f;
-#pragma unroll
-      for (int d = 0; d < DT; ++d)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) acc[d][e] = v;
-      m = Op::kLift;
-      n = 0.f;
-      ll = 1.f;
-    }
-  }
   if (to.live) store_row<DT>(a, to.out, sp, ch.used, half, acc, m - Op::kLift, EB == 1 ? n : m, ll);
 }
 
-template <int D, int EB, int NP, bool TREE>
+template <int D, int EB, int NP>
 __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled_kernel(AttnArgs a) {
   __shared__ __align__(1024) uint8_t lds[2][4 * kKvBlock * D];  // two blocks: K part | V part, 16 bits
   // heads fastest: the workgroups of one head share an XCD's L2 where 8 divides the
@@ -265,17 +235,15 @@ __global__ __launch_bounds__(256, NP == 3 ? 1 : NP == 2 ? 2 : 3) void attn_tiled
   // the whole prompt has one.
   if constexpr (EB == 2 && NP == 1) {
     if (s.len * a.G <= kFewRows) {
-      attend_tile<D, EB, NP, 2, TREE>(a, s, req, h, sp, row0, lds);
+      attend_tile<D, EB, NP, 2>(a, s, req, h, sp, row0, lds);
       return;
     }
   }
-  attend_tile<D, EB, NP, NP, TREE>(a, s, req, h, sp, row0, lds);
+  attend_tile<D, EB, NP, NP>(a, s, req, h, sp, row0, lds);
 }
 
 template <int D, int EB, int NP> static void launch_t(const AttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.units * a.c.H * a.splits));
-  if (a.parent) hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP, true>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP, false>), grid, dim3(256), 0, st, a);
+  hipLaunchKernelGGL((attn_tiled_kernel<D, EB, NP>), dim3((unsigned)(a.units * a.c.H * a.splits)), dim3(256), 0, st, a);
 }
 template <int D> static void launch_d(bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st) {
   if (int8) {

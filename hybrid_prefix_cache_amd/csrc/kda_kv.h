@@ -98,6 +98,7 @@ struct KvCommitArgs {
   int32_t n, tokens;
 };
 
+constexpr int kCUs = 256;
 constexpr int kTileRows = 128;   // rows of a tile of the tiled kernel
 constexpr int kFewRows = 64;     // rows of a sequence and head that are few to it
 // Rows per request and key/value head the decode kernel takes.  Beyond, column
@@ -107,6 +108,8 @@ constexpr int kDecodeRows = 32;
 
 hipError_t launch_attn_decode(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_tiled(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
+// trees past the decode kernel's rows
+hipError_t launch_attn_tree(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_join(int D, const AttnArgs& a, hipStream_t st);
 // one: the one-token step's kernel (b.pos set, b.tokens == 1)
 hipError_t launch_kv_append(int D, bool bf16, bool int8, const KvAppendArgs& a, int64_t wgs, bool one, hipStream_t st);

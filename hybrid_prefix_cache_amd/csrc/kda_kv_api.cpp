@@ -33,7 +33,6 @@ constexpr int64_t kDecodeTarget = 1536;
 // over twice (fp32 queries): there another number of shares may be faster.  Filling the
 // card whatever it cost, prompts of 1024, 2048 and 3000 tokens (32 heads, bf16 cache)
 // took 43, 86 and 135 us; weighed, 31, 60 and 95.
-constexpr int64_t kCUs = 256;
 constexpr double kStepUs[4] = {0, 1.1, 1.15, 1.71}, kJoinUs = 4.0, kPartialRate = 5e6;
 
 kda_status check_kv_pool(const kda_kv_pool* p) {
@@ -342,7 +341,7 @@ void split_tiles(AttnPlan* pl, const kda_kv_pool* p, int32_t Hq, int64_t rows, i
   double best = 0;
   pl->splits = 0;
   for (int fill = 0; fill <= 3; ++fill) {
-    const int64_t s = std::max<int64_t>(1, std::min(most, fill * kCUs / wgs));
+    const int64_t s = std::max<int64_t>(1, std::min(most, (int64_t)fill * kCUs / wgs));
     const int64_t beside = std::min<int64_t>(3, (wgs * s + kCUs - 1) / kCUs);
     double us = std::max((double)((blocks + s - 1) / s) * kStepUs[beside], steps * kStepUs[3] / (3 * kCUs));
     if (s > 1) us += kJoinUs + 2 * (double)partial_bytes(p, Hq, rows, s) / kPartialRate;
@@ -364,6 +363,23 @@ AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens
   const int64_t blocks = reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks);
   if (pl.decode) split_decode(&pl, p, Hq, (int64_t)n * tokens, blocks, rows);
   else split_tiles(&pl, p, Hq, (int64_t)n * tokens, blocks, (double)pl.units * p->num_heads * blocks);
+  return pl;
+}
+
+// Trees.  Past the decode kernel's rows a tile's blocks are shared only where the tiles
+// leave half of the card's workgroups without one.
+AttnPlan plan_tree(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens, int32_t max_pages, int32_t window,
+                   int32_t sinks) {  // the same for every type of q: the workspace is asked for without it
+  AttnPlan pl = plan_decode(p, Hq, n, tokens, max_pages, window, sinks);
+  if (pl.decode) return pl;
+  const int64_t rows = (int64_t)tokens * (Hq / p->num_heads);
+  pl.tile_rows = rows <= kFewRows ? kFewRows : kTileRows;
+  pl.units = (int64_t)n * ((rows + pl.tile_rows - 1) / pl.tile_rows);
+  const int64_t slots = rows <= kFewRows ? 2 * kCUs : kCUs, tiles = std::max<int64_t>(1, pl.units * p->num_heads);
+  const int64_t blocks = reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks);
+  pl.min_blocks = 16;
+  pl.splits = std::max<int64_t>(1, std::min(slots / tiles, blocks / pl.min_blocks));
+  pl.bytes = partial_bytes(p, Hq, (int64_t)n * tokens, pl.splits);
   return pl;
 }
 
@@ -414,11 +430,11 @@ AttnArgs attn_args(const kda_kv_pool* p, const void* q, int64_t q_ld, void* o, k
 
 kda_status run_attn(const kda_kv_pool* p, kda_dtype in, const AttnArgs& a, bool decode, const char* name,
                     hipStream_t st) {
+  const auto launch = decode ? launch_attn_decode : a.parent ? launch_attn_tree : launch_attn_tiled;
   hipError_t e;
   {
     Launch L(name, st);
-    e = decode ? launch_attn_decode(p->head_dim, in == KDA_BF16, p->dtype == KDA_INT8, a, st)
-               : launch_attn_tiled(p->head_dim, in == KDA_BF16, p->dtype == KDA_INT8, a, st);
+    e = launch(p->head_dim, in == KDA_BF16, p->dtype == KDA_INT8, a, st);
   }
   if (e == hipSuccess && a.splits > 1) {
     Launch L("kda_attn_join", st);
@@ -436,6 +452,12 @@ template <typename F> kda_status guarded(F f) {
   } catch (...) {
     return fail(KDA_ERR_HIP, "unexpected host error");
   }
+}
+
+bool step_sizes_ok(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n, int32_t tokens, int32_t max_pages,
+                   int32_t window, int32_t sinks) {
+  return check_attn(pool, KDA_BF16, KDA_BF16, num_q_heads, 1.f, window, sinks) == KDA_OK && n >= 0 && tokens >= 1 &&
+         tokens <= 64 && max_pages >= 1 && n <= 1 << 24 && (int64_t)max_pages * pool->page_tokens <= kMaxTokens;
 }
 
 // The slots a request's tree takes, read back: up to its last node.
@@ -479,7 +501,8 @@ kda_status attend_step(const char* what, const kda_kv_pool* pool, const void* q,
   const int64_t rows = (int64_t)n * tokens;
   s = check_attn_rows(pool, q, in_dtype, q_ld, o, out_dtype, num_q_heads, rows);
   if (s != KDA_OK) return s;
-  const AttnPlan pl = plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks);
+  const AttnPlan pl = tree ? plan_tree(pool, num_q_heads, n, tokens, max_pages, window, sinks)
+                           : plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks);
   if (pl.units * pool->num_heads * pl.splits > kMaxGroups || rows * num_q_heads > kMaxTokens)
     return fail(KDA_ERR_SHAPE, "too much work for one call");
   s = check_workspace(workspace, workspace_bytes, std::max<size_t>(256, pl.bytes));
@@ -753,11 +776,8 @@ kda_status kda_attn_prefill(const kda_kv_pool* pool, const void* q, kda_dtype in
 
 size_t kda_attn_decode_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n, int32_t tokens,
                                        int32_t max_pages, int32_t window, int32_t sinks) {
-  if (check_attn(pool, KDA_BF16, KDA_BF16, num_q_heads, 1.f, window, sinks) != KDA_OK || n < 0 || tokens < 1 ||
-      tokens > 64 || max_pages < 1 || n > 1 << 24 || (int64_t)max_pages * pool->page_tokens > kMaxTokens)
-    return 0;
-  if (n == 0) return 256;
-  return std::max<size_t>(256, plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks).bytes);
+  if (!step_sizes_ok(pool, num_q_heads, n, tokens, max_pages, window, sinks)) return 0;
+  return n == 0 ? 256 : std::max<size_t>(256, plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks).bytes);
 }
 
 kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld, void* o,
@@ -772,7 +792,8 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
 
 size_t kda_attn_tree_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n, int32_t tokens,
                                      int32_t max_pages, int32_t window, int32_t sinks) {
-  return kda_attn_decode_workspace_bytes(pool, num_q_heads, n, tokens, max_pages, window, sinks);
+  if (!step_sizes_ok(pool, num_q_heads, n, tokens, max_pages, window, sinks)) return 0;
+  return n == 0 ? 256 : std::max<size_t>(256, plan_tree(pool, num_q_heads, n, tokens, max_pages, window, sinks).bytes);
 }
 
 kda_status kda_attn_tree(const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld, void* o,
