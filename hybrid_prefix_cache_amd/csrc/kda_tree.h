@@ -20,10 +20,10 @@ struct TreeNode {
   __device__ __forceinline__ bool good() const { return node && !bad; }
 };
 
-// The whole wave calls it.  Six steps, each of which doubles the way that an entry knows.
-__device__ __forceinline__ TreeNode tree_node(const int32_t* parent, int tokens) {
+// p: the lane's entry, -2 past the tree.  The whole wave calls it.  Six steps, each of which
+// doubles the way that an entry knows.
+__device__ __forceinline__ TreeNode tree_node_of(int p) {
   const int t = threadIdx.x & 63;
-  const int p = t < tokens ? parent[t] : -2;
   const bool wrong = p >= t;
   int up = wrong ? -1 : max(p, -1);
   uint32_t lo = t < 32 ? 1u << t : 0u, hi = t < 32 ? 0u : 1u << (t - 32);
@@ -43,6 +43,10 @@ __device__ __forceinline__ TreeNode tree_node(const int32_t* parent, int tokens)
   x.bad = x.node && (x.way & rotten) != 0;
   x.depth = __popcll(x.way) - 1;
   return x;
+}
+__device__ __forceinline__ TreeNode tree_node(const int32_t* parent, int tokens) {
+  const int t = threadIdx.x & 63;
+  return tree_node_of(t < tokens ? parent[t] : -2);
 }
 
 // The nodes on the lane's way that its own node at position pos + depth sees through a

@@ -44,6 +44,96 @@ __device__ __forceinline__ f32x4 mma1(float a, float b, f32x4 c) { return __buil
 
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin_inff(); }
 
+// A and Q pair by pair, up the way of each of the wave's nodes, the gates between summed as
+// it goes; a lane takes channels lane, lane + 64.  Rare, and slow: 64 nodes in a chain take
+// 64 * 65 / 2 such steps.
+template <int D, typename In>
+__device__ __forceinline__ void tree_pairs(const TreeArgs& a, const uint64_t* way, const int* odd, uint64_t good, int64_t row0,
+                                           int h, int N, int LN, int waves, float* am, float* wm) {
+  const int lane = threadIdx.x & 63;
+  const uint64_t spoilt = __ballot(odd[lane] != 0);
+  auto in = [&](const void* p, int64_t at) { return load_as_f(reinterpret_cast<const In*>(p) + at); };
+  auto place = [&](int t) { return (row0 + t) * a.H + h; };
+  for (int t = threadIdx.x >> 6; t < N; t += waves) {
+    if (lane < N) am[t * LN + lane] = wm[t * LN + lane] = 0.f;
+    if (!(good >> t & 1) || (way[t] & spoilt)) continue;
+    float kt[D / 64], q[D / 64], x[D / 64] = {};
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      kt[j] = in(a.k, place(t) * D + lane + 64 * j);
+      q[j] = in(a.q, place(t) * D + lane + 64 * j);
+    }
+    for (uint64_t m = way[t]; m;) {
+      const int s = 63 - __builtin_clzll(m);
+      m &= ~(1ull << s);
+      float sa = 0.f, sq = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 64; ++j) {
+        const float ks = in(a.k, place(s) * D + lane + 64 * j) * __expf(x[j]);
+        sa = __builtin_fmaf(kt[j], ks, sa);
+        sq = __builtin_fmaf(q[j], ks, sq);
+        x[j] += fmaxf(in(a.g, place(s) * D + lane + 64 * j), -104.f);
+      }
+#pragma unroll
+      for (int i = 1; i < 64; i <<= 1) {
+        sa += __shfl_xor(sa, i);
+        sq += __shfl_xor(sq, i);
+      }
+      const float beta = in(a.beta, place(s));
+      if (lane == 0) {
+        if (s != t) am[t * LN + s] = beta * sa;
+        wm[t * LN + s] = beta * sq;
+      }
+    }
+  }
+}
+
+// The diagonal tiles of I + A, inverted in place: lane c of a wave takes column c.
+template <int NT> __device__ __forceinline__ void invert_diagonal(float* am, int LN, int wv, int lane) {
+  if (wv >= NT || lane >= 16) return;
+  float* d = am + 16 * wv * LN + 16 * wv;
+  float x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    f32x4 row[4];
+#pragma unroll
+    for (int j = 0; j < (i + 3) / 4; ++j) row[j] = lds4(d + i * LN + 4 * j);
+    float y = i == lane ? 1.f : 0.f;
+#pragma unroll
+    for (int j = 0; j < i; ++j) y = __builtin_fmaf(-row[j >> 2][j & 3], x[j], y);
+    x[i] = y;  // 0 above the diagonal
+  }
+#pragma unroll
+  for (int i = 0; i < 16; ++i) d[i * LN + lane] = x[i];
+}
+
+// W = Q (I + A)^-1, a wave for each tile row, its tiles from the last to the first:
+// W_j = (Q_j - sum_{i > j} W_i A_ij) (I + A_jj)^-1
+template <int LN> __device__ __forceinline__ void solve_row(const float* am, float* wm, int wv, int g, int col) {
+  float* w = wm + 16 * wv * LN;
+  for (int j = wv; j >= 0; --j) {
+    f32x4 acc;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc[e] = w[(4 * g + e) * LN + 16 * j + col];
+    for (int i = j + 1; i <= wv; ++i) {
+      const f32x4 x = lds4(w + col * LN + 16 * i + 4 * g);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) acc = mma1(-x[e], am[(16 * i + 4 * g + e) * LN + 16 * j + col], acc);
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[(4 * g + e) * LN + 16 * j + col] = acc[e];
+    __builtin_amdgcn_wave_barrier();
+    const f32x4 x = lds4(w + col * LN + 16 * j + 4 * g);
+    acc = zero4();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc = mma1(x[e], am[(16 * j + 4 * g + e) * LN + 16 * j + col], acc);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[(4 * g + e) * LN + 16 * j + col] = acc[e];
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 template <int D, typename In, int NT>
 __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeArgs a) {
   using SH = TreeShape<D, NT>;
@@ -78,24 +168,7 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
     }
     return;
   }
-  // ---- the wave's columns of the state, asked for at once: row 16 kb + 4 g + i
   const int c0 = CPL * (16 * wv + col);
-  const float* s0 = reinterpret_cast<const float*>(a.pool + pin * a.page_bytes) + (int64_t)h * D * D + c0;
-  float st[D / 4][CPL];
-#pragma unroll
-  for (int kb = 0; kb < D / 16; ++kb)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float* p = s0 + (16 * kb + 4 * g + i) * D;
-      if constexpr (CPL == 2) {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        st[4 * kb + i][0] = x.x;
-        st[4 * kb + i][1] = x.y;
-      } else {
-        st[4 * kb + i][0] = *p;
-      }
-    }
-
   const TreeNode tree = tree_node(a.parent + row0, T);
   const uint64_t good = __ballot(tree.good());
   if (tid < 64) {
@@ -166,6 +239,24 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
       }
     }
   }
+  // ---- the wave's columns of the state, asked for here, behind all else that is asked for: row
+  // 16 kb + 4 g + i
+  const float* s0 = reinterpret_cast<const float*>(a.pool + pin * a.page_bytes) + (int64_t)h * D * D + c0;
+  float st[D / 4][CPL];
+#pragma unroll
+  for (int kb = 0; kb < D / 16; ++kb)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float* p = s0 + (16 * kb + 4 * g + i) * D;
+      if constexpr (CPL == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        st[4 * kb + i][0] = x.x;
+        st[4 * kb + i][1] = x.y;
+      } else {
+        st[4 * kb + i][0] = *p;
+      }
+    }
+
   far = __syncthreads_or(far);
 
   // ---- A and Q, tile by tile of the lower triangle; in registers until every wave has
@@ -207,89 +298,13 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
       }
     }
   } else {
-    // pair by pair, up the way of each of the wave's nodes, the gates between summed as it
-    // goes; a lane takes channels lane, lane + 64.  Rare, and slow: 64 nodes in a chain take
-    // 64 * 65 / 2 such steps.
-    for (int t = wv; t < N; t += WAVES) {
-      if (lane < N) am[t * LN + lane] = wm[t * LN + lane] = 0.f;
-      if (!(good >> t & 1)) continue;
-      float kt[D / 64], q[D / 64], x[D / 64] = {};
-#pragma unroll
-      for (int j = 0; j < D / 64; ++j) {
-        kt[j] = in(a.k, place(t) * D + lane + 64 * j);
-        q[j] = in(a.q, place(t) * D + lane + 64 * j);
-      }
-      for (uint64_t m = way[t]; m;) {
-        const int s = 63 - __builtin_clzll(m);
-        m &= ~(1ull << s);
-        float sa = 0.f, sq = 0.f;
-#pragma unroll
-        for (int j = 0; j < D / 64; ++j) {
-          const float ks = in(a.k, place(s) * D + lane + 64 * j) * __expf(x[j]);
-          sa = __builtin_fmaf(kt[j], ks, sa);
-          sq = __builtin_fmaf(q[j], ks, sq);
-          x[j] += fmaxf(in(a.g, place(s) * D + lane + 64 * j), -104.f);
-        }
-#pragma unroll
-        for (int i = 1; i < 64; i <<= 1) {
-          sa += __shfl_xor(sa, i);
-          sq += __shfl_xor(sq, i);
-        }
-        const float beta = in(a.beta, place(s));
-        if (lane == 0 && !odd[s]) {
-          if (s != t) am[t * LN + s] = beta * sa;
-          wm[t * LN + s] = beta * sq;
-        }
-      }
-    }
+    tree_pairs<D, In>(a, way, odd, good, row0, h, N, LN, WAVES, am, wm);
   }
   __syncthreads();
 
-  // ---- the diagonal tiles of I + A, inverted in place: lane c of a wave takes column c
-  if (wv < NT && lane < 16) {
-    float* d = am + 16 * wv * LN + 16 * wv;
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      f32x4 row[4];
-#pragma unroll
-      for (int j = 0; j < (i + 3) / 4; ++j) row[j] = lds4(d + i * LN + 4 * j);
-      float y = i == lane ? 1.f : 0.f;
-#pragma unroll
-      for (int j = 0; j < i; ++j) y = __builtin_fmaf(-row[j >> 2][j & 3], x[j], y);
-      x[i] = y;  // 0 above the diagonal
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) d[i * LN + lane] = x[i];
-  }
+  invert_diagonal<NT>(am, LN, wv, lane);
   __syncthreads();
-
-  // ---- W = Q (I + A)^-1, a wave for each tile row, its tiles from the last to the first:
-  // W_j = (Q_j - sum_{i > j} W_i A_ij) (I + A_jj)^-1
-  if (wv < NT) {
-    float* w = wm + 16 * wv * LN;
-    for (int j = wv; j >= 0; --j) {
-      f32x4 acc;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[e] = w[(4 * g + e) * LN + 16 * j + col];
-      for (int i = j + 1; i <= wv; ++i) {
-        const f32x4 x = lds4(w + col * LN + 16 * i + 4 * g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc = mma1(-x[e], am[(16 * i + 4 * g + e) * LN + 16 * j + col], acc);
-      }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[(4 * g + e) * LN + 16 * j + col] = acc[e];
-      __builtin_amdgcn_wave_barrier();
-      const f32x4 x = lds4(w + col * LN + 16 * j + 4 * g);
-      acc = zero4();
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc = mma1(x[e], am[(16 * j + 4 * g + e) * LN + 16 * j + col], acc);
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int e = 0; e < 4; ++e) w[(4 * g + e) * LN + 16 * j + col] = acc[e];
-      __builtin_amdgcn_wave_barrier();
-    }
-  }
+  if (wv < NT) solve_row<LN>(am, wm, wv, g, col);
   __syncthreads();
 
   // ---- Qhat - W Khat, in place
@@ -341,6 +356,401 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
 #pragma unroll
       for (int j = 0; j < CPL; ++j) y[j] = !node ? 0.f : ok ? acc[j][e] : __builtin_nanf("");
       put(t, c0, y);
+    }
+  }
+}
+
+// ---- bf16 inputs ---------------------------------------------------------------
+// The same steps on bf16 matrix instructions: an operand that is not bf16 by itself is the
+// sum of two bf16 parts, and a product is three (the parts' lower halves left out), good to
+// 2^-16 of its terms, with a fifth of the fp32 instructions' time.
+//
+// A wave takes CT column tiles of the gates, keys and queries, transposed (rows are
+// channels): a lane then holds four channels of one node, which is 8 bytes of a row of an
+// operand and of the inputs.  It keeps its Khat and Qhat in registers: Khat goes to LDS
+// twice, by rows for A and Q, then by columns for W Khat.
+template <int D, int NT> struct TreeShape16 {
+  static constexpr int WAVES = D == 128 && NT > 2 ? 8 : 4;
+  static constexpr int THREADS = 64 * WAVES;
+  static constexpr int N = 16 * NT;
+  static constexpr int CT = D / 16 / WAVES;      // column tiles of a wave
+  static constexpr int CPL = D / (16 * WAVES);   // columns of the state a lane holds of each row
+  static constexpr int LC = D + 8, LS = N + 8;   // strides of rows of channels, of nodes (bf16)
+  static constexpr int LN = N + 4;               // of rows of nodes (fp32)
+  static constexpr int ROWS = 2 * N * LC;        // two parts by rows
+  static constexpr int COLS = 2 * D * LS;        // by columns
+  static constexpr int KB = ROWS > COLS ? ROWS : COLS;            // Khat by rows, then by columns
+  static constexpr int XB = ROWS > 4 * N * LN ? ROWS : 4 * N * LN;  // beta k exp(-G), then A and W (fp32)
+  static constexpr int GB = D * LS > 2 * N * LS ? D * LS : 2 * N * LS;  // gates by columns, then W
+};
+
+struct Parts {
+  bf16x8 hi, lo;
+};
+__device__ __forceinline__ bf16x8 lds8(const uint16_t* p) { return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u16x8*>(p)); }
+__device__ __forceinline__ f32x4 mma8(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
+__device__ __forceinline__ bf16x8 none8() { return __builtin_bit_cast(bf16x8, u16x8{0, 0, 0, 0, 0, 0, 0, 0}); }
+// Four values as parts, to two places 8 bytes long.
+__device__ __forceinline__ void put_parts(uint16_t* hi, uint16_t* lo, const f32x4& x) {
+  const u16x4 h = pack_bf16x4(x[0], x[1], x[2], x[3]);
+  *reinterpret_cast<u16x4*>(hi) = h;
+  *reinterpret_cast<u16x4*>(lo) = pack_bf16x4(x[0] - bf16_to_f32(h[0]), x[1] - bf16_to_f32(h[1]), x[2] - bf16_to_f32(h[2]), x[3] - bf16_to_f32(h[3]));
+}
+__device__ __forceinline__ uint16_t part_hi(float x, uint16_t* lo) {
+  const uint16_t h = f32_to_bf16(x);
+  *lo = f32_to_bf16(x - bf16_to_f32(h));
+  return h;
+}
+
+template <int D, int NT>
+__global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kernel(TreeArgs a) {
+  using SH = TreeShape16<D, NT>;
+  constexpr int N = SH::N, LC = SH::LC, LS = SH::LS, LN = SH::LN, CPL = SH::CPL, CT = SH::CT, WAVES = SH::WAVES;
+  constexpr int KD = D / 32, KN = (N + 31) / 32;  // matrix steps over channels, over nodes
+  __shared__ __align__(16) uint16_t kb[SH::KB], qb[SH::ROWS], xb[SH::XB], gb[SH::GB];
+  __shared__ uint64_t way[64];
+  __shared__ int odd[64];  // a node has a value that is not finite
+  float* const am = reinterpret_cast<float*>(xb);
+  float* const wm = am + N * LN;
+  const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int g = lane >> 4, col = lane & 15;
+  const int r = blockIdx.x / a.H, h = blockIdx.x % a.H, T = a.tokens;
+  const int pin = __builtin_amdgcn_readfirstlane(a.page_in[r]);
+  const int64_t row0 = (int64_t)r * T;
+  if (pin < 0 || pin >= a.num_pages) {
+    for (int i = tid; i < T * D; i += SH::THREADS) {
+      const int64_t at = ((row0 + i / D) * a.H + h) * D + i % D;
+      if (a.out_bf16) reinterpret_cast<uint16_t*>(a.o)[at] = 0x7fc0u;
+      else reinterpret_cast<float*>(a.o)[at] = __builtin_nanf("");
+    }
+    return;
+  }
+  const uint16_t* const gq = reinterpret_cast<const uint16_t*>(a.q);
+  const uint16_t* const gk = reinterpret_cast<const uint16_t*>(a.k);
+  const uint16_t* const gv = reinterpret_cast<const uint16_t*>(a.v);
+  const uint16_t* const gg = reinterpret_cast<const uint16_t*>(a.g);
+  const uint16_t* const gbeta = reinterpret_cast<const uint16_t*>(a.beta);
+  // (row, head); entries past the tree repeat its last one, whose values are then not used
+  auto place = [&](int t) { return (row0 + min(t, T - 1)) * a.H + h; };
+
+  // ---- everything a wave needs is asked for here, the state last: what is asked for is
+  // answered in order, and the state is needed last
+  const int c0 = CPL * (16 * wv + col);
+  const int parent = lane < T ? a.parent[row0 + lane] : -2;
+  constexpr int GU = (N * 2 + 63) / 64;  // 16-byte units of a column tile's gates a lane brings: node u / 2
+  u16x8 graw[CT][GU];
+  u16x4 kraw[CT][NT], qraw[CT][NT];
+  uint16_t braw[NT];
+  uint32_t vraw[KN][8];
+#pragma unroll
+  for (int i = 0; i < CT; ++i) {
+    const int c = 16 * (CT * wv + i);
+#pragma unroll
+    for (int u = 0; u < GU; ++u)
+      graw[i][u] = *reinterpret_cast<const u16x8*>(gg + place((64 * u + lane) >> 1) * D + c + 8 * (lane & 1));
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      kraw[i][t] = *reinterpret_cast<const u16x4*>(gk + place(16 * t + col) * D + c + 4 * g);
+      qraw[i][t] = *reinterpret_cast<const u16x4*>(gq + place(16 * t + col) * D + c + 4 * g);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < NT; ++t) braw[t] = gbeta[place(16 * t + col)];
+#pragma unroll
+  for (int k = 0; k < KN; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint16_t* p = gv + place(32 * k + 8 * g + i) * D + c0;
+      vraw[k][i] = CPL == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
+    }
+  __builtin_amdgcn_sched_barrier(0);
+  const float* s0 = reinterpret_cast<const float*>(a.pool + pin * a.page_bytes) + (int64_t)h * D * D + c0;
+  float st[KD][8][CPL];  // rows 32 k + 8 g + i
+#pragma unroll
+  for (int k = 0; k < KD; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float* p = s0 + (32 * k + 8 * g + i) * D;
+      if constexpr (CPL == 2) {
+        const float2 x = *reinterpret_cast<const float2*>(p);
+        st[k][i][0] = x.x;
+        st[k][i][1] = x.y;
+      } else {
+        st[k][i][0] = *p;
+      }
+    }
+  __builtin_amdgcn_sched_barrier(0);
+
+  const TreeNode tree = tree_node_of(parent);
+  const uint64_t good = __ballot(tree.good());
+  if (tid < 64) {
+    way[tid] = tree.way;
+    odd[tid] = 0;
+  }
+  // ---- gates by columns, a wave its own column tiles
+#pragma unroll
+  for (int i = 0; i < CT; ++i)
+#pragma unroll
+    for (int u = 0; u < GU; ++u) {
+      const int s = (64 * u + lane) >> 1, c = 16 * (CT * wv + i) + 8 * (lane & 1);
+      if (s >= N) continue;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        uint16_t x = graw[i][u][e];
+        if (!(good >> s & 1) || !(bf16_to_f32(x) < __builtin_inff())) x = 0;
+        else if (bf16_to_f32(x) < -104.f) x = 0xc2d0u;  // -104
+        gb[(c + e) * LS + s] = x;
+      }
+    }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < CT; ++i)
+#pragma unroll
+    for (int u = 0; u < GU; ++u) {
+      const int s = (64 * u + lane) >> 1;
+      bool bad = false;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) bad |= !(bf16_to_f32(graw[i][u][e]) < __builtin_inff());
+      if (s < N && (good >> s & 1) && bad) odd[s] = 1;
+    }
+  // ---- gates summed along the ways, as a product with the 0/1 matrix of ways; the factors
+  bool far = false;
+  f32x4 khat[CT][NT], qhat[CT][NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int node = 16 * t + col;
+    const uint64_t w = way[node];
+    bf16x8 on[KN];
+#pragma unroll
+    for (int k = 0; k < KN; ++k) {
+      const uint32_t bits = (uint32_t)(w >> (32 * k + 8 * g)) & 255u;
+      u16x8 x;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = bits >> e & 1 ? 0x3f80u : 0;
+      on[k] = __builtin_bit_cast(bf16x8, x);
+    }
+    const bool live = good >> node & 1;
+    const float beta = live ? bf16_to_f32(braw[t]) : 0.f;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      const int c = 16 * (CT * wv + i);
+      f32x4 G = zero4();
+#pragma unroll
+      for (int k = 0; k < KN; ++k)
+        if (32 * k <= 16 * t) {
+          const bf16x8 x = 32 * k + 8 * g < N ? lds8(gb + (c + col) * LS + 32 * k + 8 * g) : none8();
+          G = mma8(x, on[k], G);
+        }
+      f32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float k = live ? bf16_to_f32(kraw[i][t][e]) : 0.f;
+        const float q = live ? bf16_to_f32(qraw[i][t][e]) : 0.f;
+        if (!is_finite(k) || !is_finite(beta)) {
+          odd[node] = 1;
+          k = 0.f;
+        }
+        const float G1 = live ? G[e] : 0.f;
+        far |= fabsf(G1) > kFarGate<uint16_t>;
+        const float up = __expf(G1);
+        khat[i][t][e] = k * up;
+        qhat[i][t][e] = q * up;
+        x[e] = (is_finite(beta) ? beta : 0.f) * k * __expf(-G1);
+      }
+      const int to = node * LC + c + 4 * g;
+      put_parts(kb + to, kb + N * LC + to, khat[i][t]);
+      put_parts(qb + to, qb + N * LC + to, qhat[i][t]);
+      put_parts(xb + to, xb + N * LC + to, x);
+    }
+  }
+  // values of the wave's columns as an operand: nodes 32 k + 8 g + i
+  bf16x8 vf[KN][CPL];
+#pragma unroll
+  for (int k = 0; k < KN; ++k)
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+      u16x8 x;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int s = 32 * k + 8 * g + i;
+        x[i] = s < N && (good >> s & 1) ? (uint16_t)(vraw[k][i] >> (16 * j)) : 0;
+        if ((x[i] & 0x7f80u) == 0x7f80u) {
+          odd[s] = 1;
+          x[i] = 0;
+        }
+      }
+      vf[k][j] = __builtin_bit_cast(bf16x8, x);
+    }
+  far = __syncthreads_or(far);
+
+  // ---- A and Q, tile by tile of the lower triangle; in registers until every wave has
+  // read what they replace
+  constexpr int UNITS = NT * (NT + 1), MINE = (UNITS + WAVES - 1) / WAVES;  // a tile of A or of Q
+  f32x4 got[MINE];
+  auto tile_of = [](int u, int* ti, int* tj) {
+    const int tile = u >> 1;
+    *ti = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0;
+    *tj = tile - *ti * (*ti + 1) / 2;
+  };
+  if (!far) {
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) {
+      const int u = m * WAVES + wv;
+      if (u >= UNITS) continue;
+      int ti, tj;
+      tile_of(u, &ti, &tj);
+      const uint16_t* A = (u & 1 ? qb : kb) + (16 * ti + col) * LC + 8 * g;
+      const uint16_t* B = xb + (16 * tj + col) * LC + 8 * g;
+      f32x4 x = zero4(), y = zero4(), z = zero4();
+#pragma unroll
+      for (int k = 0; k < KD; ++k) {
+        const bf16x8 ah = lds8(A + 32 * k), al = lds8(A + N * LC + 32 * k), bh = lds8(B + 32 * k), bl = lds8(B + N * LC + 32 * k);
+        x = mma8(ah, bh, x);
+        y = mma8(al, bh, y);
+        z = mma8(ah, bl, z);
+      }
+      got[m] = x + (y + z);
+    }
+  }
+  __syncthreads();
+  // Khat by columns, in its own place
+#pragma unroll
+  for (int t = 0; t < NT; ++t)
+#pragma unroll
+    for (int i = 0; i < CT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int to = (16 * (CT * wv + i) + 4 * g + e) * LS + 16 * t + col;
+        uint16_t lo;
+        kb[to] = part_hi(khat[i][t][e], &lo);
+        kb[D * LS + to] = lo;
+      }
+  if (!far) {
+#pragma unroll
+    for (int m = 0; m < MINE; ++m) {
+      const int u = m * WAVES + wv;
+      if (u >= UNITS) continue;
+      int ti, tj;
+      tile_of(u, &ti, &tj);
+      float* to = u & 1 ? wm : am;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * ti + 4 * g + e, s = 16 * tj + col;
+        to[t * LN + s] = (way[t] >> s & 1) && ((u & 1) || s != t) ? got[m][e] : 0.f;
+      }
+    }
+  } else {
+    tree_pairs<D, uint16_t>(a, way, odd, good, row0, h, N, LN, WAVES, am, wm);
+  }
+  __syncthreads();
+  invert_diagonal<NT>(am, LN, wv, lane);
+  __syncthreads();
+  // ---- W = Q (I + A)^-1, and its parts
+  if (wv < NT) {
+    solve_row<LN>(am, wm, wv, g, col);
+    const float* w = wm + 16 * wv * LN;
+    uint16_t* to = gb + 16 * wv * LS;
+    for (int i = lane; i < 16 * 4 * (wv + 1); i += 64) {
+      const int t = i / (4 * (wv + 1)), s = i % (4 * (wv + 1)) * 4;
+      put_parts(to + t * LS + s, to + N * LS + t * LS + s, lds4(w + t * LN + s));
+    }
+  }
+  __syncthreads();
+
+  // ---- Qhat - W Khat, to where Qhat was
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    bf16x8 wh[KN], wl[KN];
+#pragma unroll
+    for (int k = 0; k < KN; ++k) {
+      const bool on = 32 * k + 8 * g < 16 * (t + 1);
+      const uint16_t* p = gb + (16 * t + col) * LS + 32 * k + 8 * g;
+      wh[k] = on ? lds8(p) : none8();
+      wl[k] = on ? lds8(p + N * LS) : none8();
+    }
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      const int c = 16 * (CT * wv + i);
+      f32x4 x = zero4();
+#pragma unroll
+      for (int k = 0; k < KN; ++k)
+        if (32 * k <= 16 * t) {
+          const bool on = 32 * k + 8 * g < N;
+          const uint16_t* p = kb + (c + col) * LS + 32 * k + 8 * g;
+          const bf16x8 kh = on ? lds8(p) : none8(), kl = on ? lds8(p + D * LS) : none8();
+          x = mma8(kh, wh[k], x);
+          x = mma8(kl, wh[k], x);
+          x = mma8(kh, wl[k], x);
+        }
+      const int to = (16 * t + col) * LC + c + 4 * g;
+      put_parts(qb + to, qb + N * LC + to, qhat[i][t] - x);
+    }
+  }
+  __syncthreads();
+
+  // ---- O = (Qhat - W Khat) S0 + W V
+  Parts sf[KD][CPL];
+#pragma unroll
+  for (int k = 0; k < KD; ++k)
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+      u16x8 hi, lo;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint16_t l;
+        hi[i] = part_hi(st[k][i][j], &l);
+        lo[i] = l;
+      }
+      sf[k][j] = Parts{__builtin_bit_cast(bf16x8, hi), __builtin_bit_cast(bf16x8, lo)};
+    }
+  const uint64_t spoilt = __ballot(odd[lane] != 0), nodes = __ballot(tree.node);
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (16 * t >= T) break;
+    f32x4 x[CPL], y[CPL], z[CPL];
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) x[j] = y[j] = z[j] = zero4();
+#pragma unroll
+    for (int k = 0; k < KN; ++k)
+      if (32 * k <= 16 * t) {
+        const bool on = 32 * k + 8 * g < 16 * (t + 1);
+        const uint16_t* p = gb + (16 * t + col) * LS + 32 * k + 8 * g;
+        const bf16x8 wh = on ? lds8(p) : none8(), wl = on ? lds8(p + N * LS) : none8();
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) {
+          x[j] = mma8(wh, vf[k][j], x[j]);
+          y[j] = mma8(wl, vf[k][j], y[j]);
+        }
+      }
+#pragma unroll
+    for (int k = 0; k < KD; ++k) {
+      const uint16_t* p = qb + (16 * t + col) * LC + 32 * k + 8 * g;
+      const bf16x8 qh = lds8(p), ql = lds8(p + N * LC);
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) {
+        x[j] = mma8(qh, sf[k][j].hi, x[j]);
+        y[j] = mma8(ql, sf[k][j].hi, y[j]);
+        z[j] = mma8(qh, sf[k][j].lo, z[j]);
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int node = 16 * t + 4 * g + e;
+      if (node >= T) continue;
+      const bool is_node = nodes >> node & 1, ok = (good >> node & 1) && !(way[node] & spoilt);
+      float o[CPL];
+#pragma unroll
+      for (int j = 0; j < CPL; ++j) o[j] = !is_node ? 0.f : ok ? x[j][e] + (y[j][e] + z[j][e]) : __builtin_nanf("");
+      const int64_t at = ((row0 + node) * a.H + h) * D + c0;
+      if (a.out_bf16) {
+        uint16_t* to = reinterpret_cast<uint16_t*>(a.o) + at;
+        if constexpr (CPL == 2) *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(o[0], o[1]);
+        else *to = f32_to_bf16(o[0]);
+      } else {
+        float* to = reinterpret_cast<float*>(a.o) + at;
+#pragma unroll
+        for (int j = 0; j < CPL; ++j) to[j] = o[j];
+      }
     }
   }
 }
@@ -434,9 +844,18 @@ __global__ __launch_bounds__((CommitShape<D>::NT), 4) void state_commit_kernel(S
     __builtin_nontemporal_store(s[i], reinterpret_cast<f32x4*>(dst + (rg + i * RS) * D + c0));
 }
 
-template <int D, typename In> static void launch_tree_t(const TreeArgs& a, hipStream_t st) {
+template <int D> static void launch_tree_f32(const TreeArgs& a, hipStream_t st) {
   const dim3 grid((unsigned)(a.n * a.H));
-#define KDA_TREE(NT) hipLaunchKernelGGL((tree_kernel<D, In, NT>), grid, dim3(TreeShape<D, NT>::THREADS), 0, st, a)
+#define KDA_TREE(NT) hipLaunchKernelGGL((tree_kernel<D, float, NT>), grid, dim3(TreeShape<D, NT>::THREADS), 0, st, a)
+  if (a.tokens <= 16) KDA_TREE(1);
+  else if (a.tokens <= 32) KDA_TREE(2);
+  else if (a.tokens <= 48) KDA_TREE(3);
+  else KDA_TREE(4);
+#undef KDA_TREE
+}
+template <int D> static void launch_tree_bf16(const TreeArgs& a, hipStream_t st) {
+  const dim3 grid((unsigned)(a.n * a.H));
+#define KDA_TREE(NT) hipLaunchKernelGGL((tree_bf16_kernel<D, NT>), grid, dim3(TreeShape16<D, NT>::THREADS), 0, st, a)
   if (a.tokens <= 16) KDA_TREE(1);
   else if (a.tokens <= 32) KDA_TREE(2);
   else if (a.tokens <= 48) KDA_TREE(3);
@@ -445,11 +864,11 @@ template <int D, typename In> static void launch_tree_t(const TreeArgs& a, hipSt
 }
 hipError_t launch_tree(int D, bool bf16, const TreeArgs& a, hipStream_t st) {
   if (D == 128) {
-    if (bf16) launch_tree_t<128, uint16_t>(a, st);
-    else launch_tree_t<128, float>(a, st);
+    if (bf16) launch_tree_bf16<128>(a, st);
+    else launch_tree_f32<128>(a, st);
   } else {
-    if (bf16) launch_tree_t<64, uint16_t>(a, st);
-    else launch_tree_t<64, float>(a, st);
+    if (bf16) launch_tree_bf16<64>(a, st);
+    else launch_tree_f32<64>(a, st);
   }
   return hipGetLastError();
 }
