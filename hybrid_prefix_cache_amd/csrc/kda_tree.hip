@@ -387,19 +387,29 @@ template <int D, int NT> struct TreeShape16 {
 struct Parts {
   bf16x8 hi, lo;
 };
-__device__ __forceinline__ bf16x8 lds8(const uint16_t* p) { return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u16x8*>(p)); }
+__device__ __forceinline__ bf16x8 lds8(const uint16_t* p) { return __builtin_bit_cast(bf16x8, *reinterpret_cast<const u32x4_t*>(p)); }
 __device__ __forceinline__ f32x4 mma8(bf16x8 a, bf16x8 b, f32x4 c) { return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0); }
-__device__ __forceinline__ bf16x8 none8() { return __builtin_bit_cast(bf16x8, u16x8{0, 0, 0, 0, 0, 0, 0, 0}); }
+__device__ __forceinline__ bf16x8 none8() { return __builtin_bit_cast(bf16x8, u32x4_t{0u, 0u, 0u, 0u}); }
+// Two bf16 in a word: their values; two values as a word of upper and one of lower parts.
+__device__ __forceinline__ float low_of(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float high_of(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+__device__ __forceinline__ uint32_t split2(float x, float y, uint32_t* lo) {
+  const uint32_t h = pack_bf16x2(x, y);
+  *lo = pack_bf16x2(x - low_of(h), y - high_of(h));
+  return h;
+}
+// Bits 15 and 31 are set where the word's bf16 values are infinite or NaN.
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
 // Four values as parts, to two places 8 bytes long.
 __device__ __forceinline__ void put_parts(uint16_t* hi, uint16_t* lo, const f32x4& x) {
-  const u16x4 h = pack_bf16x4(x[0], x[1], x[2], x[3]);
-  *reinterpret_cast<u16x4*>(hi) = h;
-  *reinterpret_cast<u16x4*>(lo) = pack_bf16x4(x[0] - bf16_to_f32(h[0]), x[1] - bf16_to_f32(h[1]), x[2] - bf16_to_f32(h[2]), x[3] - bf16_to_f32(h[3]));
-}
-__device__ __forceinline__ uint16_t part_hi(float x, uint16_t* lo) {
-  const uint16_t h = f32_to_bf16(x);
-  *lo = f32_to_bf16(x - bf16_to_f32(h));
-  return h;
+  u32x2_t h, l;
+  uint32_t w;
+  h[0] = split2(x[0], x[1], &w);
+  l[0] = w;
+  h[1] = split2(x[2], x[3], &w);
+  l[1] = w;
+  *reinterpret_cast<u32x2_t*>(hi) = h;
+  *reinterpret_cast<u32x2_t*>(lo) = l;
 }
 
 template <int D, int NT>
@@ -425,42 +435,46 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
     }
     return;
   }
-  const uint16_t* const gq = reinterpret_cast<const uint16_t*>(a.q);
-  const uint16_t* const gk = reinterpret_cast<const uint16_t*>(a.k);
-  const uint16_t* const gv = reinterpret_cast<const uint16_t*>(a.v);
-  const uint16_t* const gg = reinterpret_cast<const uint16_t*>(a.g);
-  const uint16_t* const gbeta = reinterpret_cast<const uint16_t*>(a.beta);
-  // (row, head); entries past the tree repeat its last one, whose values are then not used
-  auto place = [&](int t) { return (row0 + min(t, T - 1)) * a.H + h; };
+  // (row, head) of the request's first row; rows are 32-bit offsets from it, and entries past
+  // the tree repeat its last one, whose values are then not used
+  const int64_t first = (row0 * a.H + h) * D;
+  const uint16_t* const gq = reinterpret_cast<const uint16_t*>(a.q) + first;
+  const uint16_t* const gk = reinterpret_cast<const uint16_t*>(a.k) + first;
+  const uint16_t* const gv = reinterpret_cast<const uint16_t*>(a.v) + first;
+  const uint16_t* const gg = reinterpret_cast<const uint16_t*>(a.g) + first;
+  const uint16_t* const gbeta = reinterpret_cast<const uint16_t*>(a.beta) + row0 * a.H + h;
+  const uint32_t HD = a.H * D;
 
   // ---- everything a wave needs is asked for here, the state last: what is asked for is
   // answered in order, and the state is needed last
   const int c0 = CPL * (16 * wv + col);
   const int parent = lane < T ? a.parent[row0 + lane] : -2;
   constexpr int GU = (N * 2 + 63) / 64;  // 16-byte units of a column tile's gates a lane brings: node u / 2
-  u16x8 graw[CT][GU];
-  u16x4 kraw[CT][NT], qraw[CT][NT];
+  u32x4_t graw[CT][GU];
+  u32x2_t kraw[CT][NT], qraw[CT][NT];
   uint16_t braw[NT];
   uint32_t vraw[KN][8];
 #pragma unroll
-  for (int i = 0; i < CT; ++i) {
-    const int c = 16 * (CT * wv + i);
+  for (int u = 0; u < GU; ++u) {
+    const uint32_t at = min((64 * u + lane) >> 1, T - 1) * HD + 16 * CT * wv + 8 * (lane & 1);
 #pragma unroll
-    for (int u = 0; u < GU; ++u)
-      graw[i][u] = *reinterpret_cast<const u16x8*>(gg + place((64 * u + lane) >> 1) * D + c + 8 * (lane & 1));
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      kraw[i][t] = *reinterpret_cast<const u16x4*>(gk + place(16 * t + col) * D + c + 4 * g);
-      qraw[i][t] = *reinterpret_cast<const u16x4*>(gq + place(16 * t + col) * D + c + 4 * g);
-    }
+    for (int i = 0; i < CT; ++i) graw[i][u] = *reinterpret_cast<const u32x4_t*>(gg + at + 16 * i);
   }
 #pragma unroll
-  for (int t = 0; t < NT; ++t) braw[t] = gbeta[place(16 * t + col)];
+  for (int t = 0; t < NT; ++t) {
+    const uint32_t row = min(16 * t + col, T - 1), at = row * HD + 16 * CT * wv + 4 * g;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      kraw[i][t] = *reinterpret_cast<const u32x2_t*>(gk + at + 16 * i);
+      qraw[i][t] = *reinterpret_cast<const u32x2_t*>(gq + at + 16 * i);
+    }
+    braw[t] = gbeta[row * (uint32_t)a.H];
+  }
 #pragma unroll
   for (int k = 0; k < KN; ++k)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint16_t* p = gv + place(32 * k + 8 * g + i) * D + c0;
+      const uint16_t* p = gv + min(32 * k + 8 * g + i, T - 1) * HD + c0;
       vraw[k][i] = CPL == 2 ? *reinterpret_cast<const uint32_t*>(p) : *p;
     }
   __builtin_amdgcn_sched_barrier(0);
@@ -487,32 +501,39 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
     way[tid] = tree.way;
     odd[tid] = 0;
   }
-  // ---- gates by columns, a wave its own column tiles
-#pragma unroll
-  for (int i = 0; i < CT; ++i)
-#pragma unroll
-    for (int u = 0; u < GU; ++u) {
-      const int s = (64 * u + lane) >> 1, c = 16 * (CT * wv + i) + 8 * (lane & 1);
-      if (s >= N) continue;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        uint16_t x = graw[i][u][e];
-        if (!(good >> s & 1) || !(bf16_to_f32(x) < __builtin_inff())) x = 0;
-        else if (bf16_to_f32(x) < -104.f) x = 0xc2d0u;  // -104
-        gb[(c + e) * LS + s] = x;
-      }
-    }
-  __syncthreads();
+  // ---- gates by columns, a wave its own column tiles.  Gates that are infinite, NaN or past
+  // 104 are rare, and looked at one by one
+  uint64_t odd_gates = 0;  // nodes with a gate that is NaN or +inf
 #pragma unroll
   for (int i = 0; i < CT; ++i)
 #pragma unroll
     for (int u = 0; u < GU; ++u) {
       const int s = (64 * u + lane) >> 1;
-      bool bad = false;
+      u32x4_t w = graw[i][u];
+      if (s >= N || !(good >> s & 1)) w = u32x4_t{0u, 0u, 0u, 0u};
+      uint32_t near = ~0u;  // bits 15 and 31: values of at most 104 (0x42d0) either way
 #pragma unroll
-      for (int e = 0; e < 8; ++e) bad |= !(bf16_to_f32(graw[i][u][e]) < __builtin_inff());
-      if (s < N && (good >> s & 1) && bad) odd[s] = 1;
+      for (int e = 0; e < 4; ++e) near &= 0xc2d0c2d0u - (w[e] & 0x7fff7fffu);
+      if (__any(~near & 0x80008000u)) {
+        bool bad = false;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const uint32_t x = w[e >> 1] >> (16 * (e & 1)) & 0xffffu;
+          const bool no = !(low_of(x) < __builtin_inff());
+          const uint32_t y = no ? 0u : low_of(x) < -104.f ? 0xc2d0u : x;
+          bad |= no;
+          w[e >> 1] = (w[e >> 1] & (e & 1 ? 0xffffu : 0xffff0000u)) | y << (16 * (e & 1));
+        }
+        for (uint64_t m = __ballot(bad); m; m &= m - 1) odd_gates |= 1ull << ((64 * u + __builtin_ctzll(m)) >> 1);
+      }
+      if (s < N) {
+        uint16_t* to = gb + (16 * (CT * wv + i) + 8 * (lane & 1)) * LS + s;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) to[e * LS] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
+      }
     }
+  __syncthreads();
+  if (odd_gates >> lane & 1) odd[lane] = 1;
   // ---- gates summed along the ways, as a product with the 0/1 matrix of ways; the factors
   bool far = false;
   f32x4 khat[CT][NT], qhat[CT][NT];
@@ -524,13 +545,15 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
 #pragma unroll
     for (int k = 0; k < KN; ++k) {
       const uint32_t bits = (uint32_t)(w >> (32 * k + 8 * g)) & 255u;
-      u16x8 x;
+      u32x4_t x;  // 0x3f80 is 1
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = bits >> e & 1 ? 0x3f80u : 0;
+      for (int e = 0; e < 4; ++e) x[e] = (bits >> (2 * e) & 1) * 0x3f80u | (bits >> (2 * e + 1) & 1) * 0x3f800000u;
       on[k] = __builtin_bit_cast(bf16x8, x);
     }
     const bool live = good >> node & 1;
-    const float beta = live ? bf16_to_f32(braw[t]) : 0.f;
+    float beta = live ? bf16_to_f32(braw[t]) : 0.f;
+    const bool odd_beta = !is_finite(beta);
+    if (odd_beta) beta = 0.f;
 #pragma unroll
     for (int i = 0; i < CT; ++i) {
       const int c = 16 * (CT * wv + i);
@@ -541,21 +564,23 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
           const bf16x8 x = 32 * k + 8 * g < N ? lds8(gb + (c + col) * LS + 32 * k + 8 * g) : none8();
           G = mma8(x, on[k], G);
         }
+      u32x2_t kw = kraw[i][t], qw = qraw[i][t];
+      if (!live) kw = qw = u32x2_t{0u, 0u};
+      const bool odd_k = (not_finite2(kw[0]) | not_finite2(kw[1])) & 0x80008000u;
+      if (odd_k || odd_beta) {
+        odd[node] = 1;
+        kw = u32x2_t{0u, 0u};
+      }
+      const f32x4 k = {low_of(kw[0]), high_of(kw[0]), low_of(kw[1]), high_of(kw[1])};
+      const f32x4 q = {low_of(qw[0]), high_of(qw[0]), low_of(qw[1]), high_of(qw[1])};
       f32x4 x;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float k = live ? bf16_to_f32(kraw[i][t][e]) : 0.f;
-        const float q = live ? bf16_to_f32(qraw[i][t][e]) : 0.f;
-        if (!is_finite(k) || !is_finite(beta)) {
-          odd[node] = 1;
-          k = 0.f;
-        }
-        const float G1 = live ? G[e] : 0.f;
-        far |= fabsf(G1) > kFarGate<uint16_t>;
-        const float up = __expf(G1);
-        khat[i][t][e] = k * up;
-        qhat[i][t][e] = q * up;
-        x[e] = (is_finite(beta) ? beta : 0.f) * k * __expf(-G1);
+      for (int e = 0; e < 4; ++e) {  // of an entry that is no node G is 0, as its gates and its way are
+        far |= fabsf(G[e]) > kFarGate<uint16_t>;
+        const float y = G[e] * 1.44269504f, up = __builtin_amdgcn_exp2f(y);
+        khat[i][t][e] = k[e] * up;
+        qhat[i][t][e] = q[e] * up;
+        x[e] = beta * k[e] * __builtin_amdgcn_exp2f(-y);
       }
       const int to = node * LC + c + 4 * g;
       put_parts(kb + to, kb + N * LC + to, khat[i][t]);
@@ -566,21 +591,31 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
   // values of the wave's columns as an operand: nodes 32 k + 8 g + i
   bf16x8 vf[KN][CPL];
 #pragma unroll
-  for (int k = 0; k < KN; ++k)
+  for (int k = 0; k < KN; ++k) {
+    const uint32_t live = 32 * k + 8 * g < N ? (uint32_t)(good >> (32 * k + 8 * g)) : 0u;
+    uint32_t bad = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      vraw[k][i] = live >> i & 1 ? vraw[k][i] : 0u;
+      bad |= not_finite2(vraw[k][i]);
+    }
+    if (bad & 0x80008000u) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (not_finite2(vraw[k][i]) & 0x80008000u) {
+          odd[32 * k + 8 * g + i] = 1;
+          vraw[k][i] = 0;
+        }
+    }
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
-      u16x8 x;
+      u32x4_t x;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int s = 32 * k + 8 * g + i;
-        x[i] = s < N && (good >> s & 1) ? (uint16_t)(vraw[k][i] >> (16 * j)) : 0;
-        if ((x[i] & 0x7f80u) == 0x7f80u) {
-          odd[s] = 1;
-          x[i] = 0;
-        }
-      }
+      for (int i = 0; i < 4; ++i)
+        x[i] = __builtin_amdgcn_perm(vraw[k][2 * i + 1], vraw[k][2 * i], j ? 0x07060302u : 0x05040100u);
       vf[k][j] = __builtin_bit_cast(bf16x8, x);
     }
+  }
   far = __syncthreads_or(far);
 
   // ---- A and Q, tile by tile of the lower triangle; in registers until every wave has
@@ -619,11 +654,14 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
 #pragma unroll
     for (int i = 0; i < CT; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < 4; e += 2) {
         const int to = (16 * (CT * wv + i) + 4 * g + e) * LS + 16 * t + col;
-        uint16_t lo;
-        kb[to] = part_hi(khat[i][t][e], &lo);
-        kb[D * LS + to] = lo;
+        uint32_t lo;
+        const uint32_t hi = split2(khat[i][t][e], khat[i][t][e + 1], &lo);
+        kb[to] = (uint16_t)hi;
+        kb[to + LS] = (uint16_t)(hi >> 16);
+        kb[D * LS + to] = (uint16_t)lo;
+        kb[D * LS + to + LS] = (uint16_t)(lo >> 16);
       }
   if (!far) {
 #pragma unroll
@@ -694,11 +732,11 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
   for (int k = 0; k < KD; ++k)
 #pragma unroll
     for (int j = 0; j < CPL; ++j) {
-      u16x8 hi, lo;
+      u32x4_t hi, lo;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint16_t l;
-        hi[i] = part_hi(st[k][i][j], &l);
+      for (int i = 0; i < 4; ++i) {
+        uint32_t l;
+        hi[i] = split2(st[k][2 * i][j], st[k][2 * i + 1][j], &l);
         lo[i] = l;
       }
       sf[k][j] = Parts{__builtin_bit_cast(bf16x8, hi), __builtin_bit_cast(bf16x8, lo)};
@@ -741,13 +779,13 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
       float o[CPL];
 #pragma unroll
       for (int j = 0; j < CPL; ++j) o[j] = !is_node ? 0.f : ok ? x[j][e] + (y[j][e] + z[j][e]) : __builtin_nanf("");
-      const int64_t at = ((row0 + node) * a.H + h) * D + c0;
+      const uint32_t at = node * HD + c0;
       if (a.out_bf16) {
-        uint16_t* to = reinterpret_cast<uint16_t*>(a.o) + at;
+        uint16_t* to = reinterpret_cast<uint16_t*>(a.o) + first + at;
         if constexpr (CPL == 2) *reinterpret_cast<uint32_t*>(to) = pack_bf16x2(o[0], o[1]);
         else *to = f32_to_bf16(o[0]);
       } else {
-        float* to = reinterpret_cast<float*>(a.o) + at;
+        float* to = reinterpret_cast<float*>(a.o) + first + at;
 #pragma unroll
         for (int j = 0; j < CPL; ++j) to[j] = o[j];
       }

@@ -20,8 +20,9 @@ kda_status check_trees(const char* what, int32_t n, int32_t tokens, int64_t head
   if (n < 0) return fail(KDA_ERR_SHAPE, "%s: n < 0", what);
   if (tokens < 1 || tokens > kMaxTree)
     return fail(KDA_ERR_SHAPE, "%s: tokens per request %d outside [1, %d]", what, tokens, kMaxTree);
-  // workgroups of up to 1024 threads, of which a launch can count 2^32
-  if ((int64_t)n * heads >= (int64_t)1 << 22 || (int64_t)n * tokens * heads > (int64_t)1 << 30)
+  // workgroups of up to 1024 threads, of which a launch can count 2^32; a request's rows are
+  // 32-bit offsets
+  if (heads > 1 << 16 || (int64_t)n * heads >= (int64_t)1 << 22 || (int64_t)n * tokens * heads > (int64_t)1 << 30)
     return fail(KDA_ERR_SHAPE, "%s: n * heads * tokens too large", what);
   return KDA_OK;
 }
