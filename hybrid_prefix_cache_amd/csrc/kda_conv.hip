@@ -264,52 +264,60 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvUpdateArgs a) {
 }
 
 // Along a tree of drafted tokens: node t's inputs are its own row of x and those of the
-// nodes before it on its way, then the window's (page_in[r]).  A thread takes a 16-byte
-// channel group of kConvTreeNodes nodes of a request; its taps stay in registers.  Rows
-// of parents are read again by their children, mostly from the caches.  Same taps and
-// summation order as conv_kernel.
-constexpr int kConvTreeNodes = 8;
+// nodes before it on its way, then the window's (page_in[r]).  A workgroup takes 64 channel
+// groups of 16 bytes of a request, with a wave for every 16 nodes: each row is asked for
+// once, before the tree is known, and goes to LDS, where a node finds its taps by number.
+// Same taps and summation order as conv_kernel.  Bound by the bytes of x and y.
+constexpr int kConvTreeNodes = 16;  // of a wave
 
-template <typename In, int W>
-__global__ __launch_bounds__(256) void conv_tree_kernel(ConvTreeArgs a) {
+template <typename In, int W, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void conv_tree_kernel(ConvTreeArgs a) {
   using CV = ConvVec<In>;
   constexpr int N = CV::N, K = kConvTreeNodes;
-  const int parts = (a.tokens + K - 1) / K, r = blockIdx.x / parts, t0 = blockIdx.x % parts * K;
-  const int64_t row0 = (int64_t)r * a.tokens, C = a.C;
-  const TreeNode tree = tree_node(a.parent + row0, a.tokens);
-  const uint64_t good = __ballot(tree.good()), node = __ballot(tree.node);
-  const int up = tree.good() ? a.parent[row0 + (threadIdx.x & 63)] : -1;  // of the lane's entry
-  const int pin = a.page_in[r];
-  const bool page = pin >= 0 && pin < a.num_pages;
-  const int c0 = (blockIdx.y * 256 + threadIdx.x) * N;
+  __shared__ u32x4_t in[W - 1 + K * WAVES][64];  // the window, then the nodes
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int cols = (a.C / N + 63) / 64, r = blockIdx.x / cols, t0 = K * wv, T = a.tokens;
+  const int64_t row0 = (int64_t)r * T, C = a.C;
+  const int c0 = (blockIdx.x % cols * 64 + lane) * N;
   const bool live = c0 < a.C;
-  const In* x = reinterpret_cast<const In*>(a.x) + row0 * C + c0;
-  const In* win = reinterpret_cast<const In*>(a.cpool + (int64_t)(page ? pin : 0) * a.cpage_bytes) + c0;
+  const int c = live ? c0 : 0;
+  const int pin = a.page_in[r], parent = lane < T ? a.parent[row0 + lane] : -2;
+  const bool page = pin >= 0 && pin < a.num_pages;
+  const In* x = reinterpret_cast<const In*>(a.x) + row0 * C + c;
+  u32x4_t rows[K], before[W - 1];
+#pragma unroll
+  for (int i = 0; i < K; ++i) rows[i] = CV::raw(x + min(t0 + i, T - 1) * C);
   float wt[W][N];
-  if (live) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+  for (int i = 0; i < N; ++i)
 #pragma unroll
-      for (int j = 0; j < W; ++j) wt[j][i] = a.w[(int64_t)(c0 + i) * W + j];
+    for (int j = 0; j < W; ++j) wt[j][i] = a.w[(int64_t)(c + i) * W + j];
+  if (wv == 0) {
+    const In* win = reinterpret_cast<const In*>(a.cpool + (int64_t)(page ? pin : 0) * a.cpage_bytes) + c;
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) before[j] = CV::raw(win + j * C);
   }
-  u32x4_t rows[K][W];
+  const TreeNode tree = tree_node_of(parent);
+  const uint64_t good = __ballot(tree.good()), node = __ballot(tree.node);
+  int tap[W];  // of the lane's entry: rows of `in`
+  int at = lane, back = 0;
+#pragma unroll
+  for (int j = W - 1; j >= 0; --j) {
+    tap[j] = at >= 0 ? W - 1 + at : W - 1 - back;
+    const int up = __shfl(tree.good() ? parent : -1, max(at, 0));
+    at = at >= 0 ? up : -1;
+    back += at < 0;
+  }
+#pragma unroll
+  for (int i = 0; i < K; ++i) in[W - 1 + t0 + i][lane] = rows[i];
+  if (wv == 0)
+#pragma unroll
+    for (int j = 0; j < W - 1; ++j) in[j][lane] = before[j];
+  if constexpr (WAVES > 1) __syncthreads();
 #pragma unroll
   for (int i = 0; i < K; ++i) {
     const int t = t0 + i;
-    if (t >= a.tokens || !(good >> t & 1) || !page) continue;
-    int at = t, back = 0;  // the node, or (at < 0) how many inputs before the tree
-#pragma unroll
-    for (int j = W - 1; j >= 0; --j) {
-      if (live) rows[i][j] = CV::raw(at >= 0 ? x + at * C : win + (int64_t)(W - 1 - back) * C);
-      if (at >= 0) at = __builtin_amdgcn_readlane(up, at);
-      if (at < 0) ++back;
-    }
-  }
-  if (!live) return;
-#pragma unroll
-  for (int i = 0; i < K; ++i) {
-    const int t = t0 + i;
-    if (t >= a.tokens) continue;
+    if (t >= T) break;
     float yv[N];
 #pragma unroll
     for (int e = 0; e < N; ++e) yv[e] = 0.f;
@@ -318,7 +326,7 @@ __global__ __launch_bounds__(256) void conv_tree_kernel(ConvTreeArgs a) {
 #pragma unroll
       for (int j = 0; j < W; ++j) {
         float xv[N];
-        CV::unpack(rows[i][j], xv);
+        CV::unpack(j == W - 1 ? rows[i] : in[__builtin_amdgcn_readlane(tap[j], t)][lane], xv);
 #pragma unroll
         for (int e = 0; e < N; ++e) yv[e] = fmaf(wt[j][e], xv[e], yv[e]);
       }
@@ -327,6 +335,7 @@ __global__ __launch_bounds__(256) void conv_tree_kernel(ConvTreeArgs a) {
       for (int e = 0; e < N; ++e) yv[e] = __builtin_nanf("");
     }
     const int64_t yo = (row0 + t) * C + c0;
+    if (!live) continue;  // no sooner: the taps are in every lane
     if (a.out_bf16) {
       u32x4_t qv;
 #pragma unroll
@@ -373,13 +382,17 @@ template <int W> __global__ __launch_bounds__(256) void conv_commit_kernel(ConvC
   for (int j = 0; j < W - 1; ++j) *reinterpret_cast<u32x4_t*>(dp + (int64_t)j * a.row_bytes) = rows[j];
 }
 
-template <typename In> static hipError_t launch_conv_tree_t(const ConvTreeArgs& a, hipStream_t st) {
+template <typename In, int WAVES> static hipError_t launch_conv_tree_w(const ConvTreeArgs& a, hipStream_t st) {
   constexpr int N = ConvVec<In>::N;
-  const dim3 grid((unsigned)(a.n * ((a.tokens + kConvTreeNodes - 1) / kConvTreeNodes)), (unsigned)((a.C / N + 255) / 256));
-  if (a.W == 2) hipLaunchKernelGGL((conv_tree_kernel<In, 2>), grid, dim3(256), 0, st, a);
-  else if (a.W == 3) hipLaunchKernelGGL((conv_tree_kernel<In, 3>), grid, dim3(256), 0, st, a);
-  else hipLaunchKernelGGL((conv_tree_kernel<In, 4>), grid, dim3(256), 0, st, a);
+  const dim3 grid((unsigned)(a.n * ((a.C / N + 63) / 64)));
+  if (a.W == 2) hipLaunchKernelGGL((conv_tree_kernel<In, 2, WAVES>), grid, dim3(64 * WAVES), 0, st, a);
+  else if (a.W == 3) hipLaunchKernelGGL((conv_tree_kernel<In, 3, WAVES>), grid, dim3(64 * WAVES), 0, st, a);
+  else hipLaunchKernelGGL((conv_tree_kernel<In, 4, WAVES>), grid, dim3(64 * WAVES), 0, st, a);
   return hipGetLastError();
+}
+template <typename In> static hipError_t launch_conv_tree_t(const ConvTreeArgs& a, hipStream_t st) {
+  if (a.tokens <= kConvTreeNodes) return launch_conv_tree_w<In, 1>(a, st);
+  return a.tokens <= 2 * kConvTreeNodes ? launch_conv_tree_w<In, 2>(a, st) : launch_conv_tree_w<In, 4>(a, st);
 }
 hipError_t launch_conv_tree(const ConvTreeArgs& a, hipStream_t st) {
   return a.in_bf16 ? launch_conv_tree_t<uint16_t>(a, st) : launch_conv_tree_t<float>(a, st);

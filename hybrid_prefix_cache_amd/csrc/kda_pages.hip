@@ -266,26 +266,35 @@ __global__ __launch_bounds__(256) void pages_remap_kernel(PagesArgs a) {
 
 // Pages src[i] to dst[i]: whole, or the blocks that hold their first tokens.  A list may be
 // long and mostly empty (a compaction's has an entry for every page of the pool), so a
-// workgroup gathers the pairs to copy from 1024 entries at a time, and the pieces of 16 KB
-// of a head's blocks go round the grid.
+// workgroup gathers the pairs to copy from 1024 entries at a time, the next 1024 on their
+// way meanwhile.  blockIdx.x is a piece of 16 KB of a head's blocks, and blockIdx.y takes
+// the pairs in turn.
 constexpr int kCopyPiece = 16384, kCopyList = 1024;
 __global__ __launch_bounds__(256) void kv_copy_pages_kernel(CopyPagesArgs a) {
-  __shared__ int list[kCopyList];
+  __shared__ int list[kCopyList][3];  // src, dst, blocks
   __shared__ int part[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t whole = (int64_t)a.block_bytes * a.blocks;
-  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece), per = pieces * a.heads;
-  int64_t done = 0;  // pieces of the entries before
-  for (int i0 = 0; i0 < a.n; i0 += kCopyList) {
-    int at = 0, pairs = 0;
-    uint32_t is = 0;
+  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece), h = blockIdx.x / pieces, piece = blockIdx.x % pieces;
+  const int64_t lo = (int64_t)piece * kCopyPiece;
+  const uint8_t* const head = a.base + h * a.head_bytes;
+  int src[4], dst[4], tokens[4];
+  auto ask = [&](int64_t i0) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int i = i0 + 4 * tid + j;
-      const int src = i < a.n ? a.src[i] : -1, dst = i < a.n ? a.dst[i] : -1;
-      is |= (src >= 0 && src < a.num_pages && dst >= 0 && dst < a.num_pages && src != dst) ? 1u << j : 0u;
+      const int64_t i = i0 + 256 * j + tid;
+      src[j] = i < a.n ? a.src[i] : -1;
+      dst[j] = i < a.n ? a.dst[i] : -1;
+      tokens[j] = a.tokens && i < a.n ? a.tokens[i] : 0;
     }
-    int y = __builtin_popcount(is);
+  };
+  ask(0);
+  int first = blockIdx.y;  // of the pairs gathered next
+  for (int64_t i0 = 0; i0 < a.n; i0 += kCopyList) {
+    int is = 0, pairs = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) is += src[j] >= 0 && src[j] < a.num_pages && dst[j] >= 0 && dst[j] < a.num_pages && src[j] != dst[j];
+    int y = is;
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) {
       const int up = __shfl_up(y, i);
@@ -294,24 +303,26 @@ __global__ __launch_bounds__(256) void kv_copy_pages_kernel(CopyPagesArgs a) {
     __syncthreads();  // the list is free
     if (lane == 63) part[wv] = y;
     __syncthreads();
+    int at = y - is;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
       at += w < wv ? part[w] : 0;
       pairs += part[w];
     }
-    at += y - __builtin_popcount(is);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (is >> j & 1) list[at++] = i0 + 4 * tid + j;
+      if (src[j] >= 0 && src[j] < a.num_pages && dst[j] >= 0 && dst[j] < a.num_pages && src[j] != dst[j]) {
+        list[at][0] = src[j];
+        list[at][1] = dst[j];
+        list[at++][2] = a.tokens ? min(max(0, (int)(((int64_t)tokens[j] + 31) / 32)), a.blocks) : a.blocks;
+      }
+    ask(i0 + kCopyList);
     __syncthreads();
-    const int64_t units = (int64_t)pairs * per;
-    for (int64_t u = (blockIdx.x + gridDim.x - done % gridDim.x) % gridDim.x; u < units; u += gridDim.x) {
-      const int i = list[u / per], rest = (int)(u % per), h = rest / pieces, piece = rest % pieces;
-      const int src = a.src[i], dst = a.dst[i];
-      const int blocks = a.tokens ? min(max(0, (a.tokens[i] + 31) / 32), a.blocks) : a.blocks;
-      const uint8_t* from = a.base + src * a.page_bytes + h * a.head_bytes;
-      uint8_t* to = a.base + dst * a.page_bytes + h * a.head_bytes;
-      const int64_t lo = (int64_t)piece * kCopyPiece, hi = min(lo + kCopyPiece, (int64_t)blocks * a.block_bytes);
+    for (; first < pairs; first += gridDim.y) {
+      const int blocks = list[first][2];
+      const uint8_t* from = head + list[first][0] * a.page_bytes;
+      uint8_t* to = const_cast<uint8_t*>(head) + list[first][1] * a.page_bytes;
+      const int64_t hi = min(lo + kCopyPiece, (int64_t)blocks * a.block_bytes);
       u32x4_t x[kCopyPiece / 4096];
 #pragma unroll
       for (int j = 0; j < kCopyPiece / 4096; ++j) {
@@ -327,7 +338,7 @@ __global__ __launch_bounds__(256) void kv_copy_pages_kernel(CopyPagesArgs a) {
         for (int b = tid; b < blocks && a.scale_bytes; b += 256)
           *reinterpret_cast<u32x2_t*>(to + whole + 8 * b) = *reinterpret_cast<const u32x2_t*>(from + whole + 8 * b);
     }
-    done += units;
+    first -= pairs;
   }
 }
 
@@ -361,10 +372,10 @@ hipError_t launch_pages_compact(const PagesArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 hipError_t launch_kv_copy_pages(const CopyPagesArgs& a, hipStream_t st) {
-  const int64_t pieces = ((int64_t)a.block_bytes * a.blocks + kCopyPiece - 1) / kCopyPiece;
-  int64_t units = (int64_t)a.n * pieces * a.heads;
-  if (units > 4096) units = 4096;
-  hipLaunchKernelGGL(kv_copy_pages_kernel, dim3((unsigned)units), dim3(256), 0, st, a);
+  const int64_t pieces = ((int64_t)a.block_bytes * a.blocks + kCopyPiece - 1) / kCopyPiece * a.heads;
+  // 2048 workgroups, eight a CU, are there at once; more would gather the list for little
+  const int64_t fill = 2048 / pieces > 0 ? 2048 / pieces : 1, turns = a.n < fill ? a.n : fill;
+  hipLaunchKernelGGL(kv_copy_pages_kernel, dim3((unsigned)pieces, (unsigned)turns), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

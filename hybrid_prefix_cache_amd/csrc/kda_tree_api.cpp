@@ -122,9 +122,9 @@ kda_status kda_short_conv_tree(const kda_conv_pool* cpool, const void* x, const 
   for (const void* p : {x, static_cast<const void*>(y), static_cast<const void*>(w)})
     if (!aligned(p, 16)) return fail(KDA_ERR_SHAPE, "%s: x, y, w must be 16-byte aligned", what);
   if (x == y) return fail(KDA_ERR_SHAPE, "%s: y may not alias x", what);
-  // a workgroup takes eight nodes and 256 groups of 16 bytes of channels
-  const int64_t groups = (cpool->channels / (cpool->dtype == KDA_BF16 ? 8 : 4) + 255) / 256;
-  if ((int64_t)n * ((tokens + 7) / 8) * groups >= (int64_t)1 << 24)
+  // a workgroup takes 64 groups of 16 bytes of channels
+  const int64_t groups = (cpool->channels / (cpool->dtype == KDA_BF16 ? 8 : 4) + 63) / 64;
+  if ((int64_t)n * groups >= (int64_t)1 << 24)
     return fail(KDA_ERR_SHAPE, "%s: n * tokens * channels too large", what);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   s = validated(what, cpool->num_pages, n, page_in, nullptr, st);

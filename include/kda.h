@@ -610,7 +610,7 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
  *            parent[t] is -1 (it follows the last cached token; a tree may have several
  *            such roots) or an earlier entry s < t that is a node (it follows node s).
  *            Below -1 there is no node (-2 is usual, for requests that drafted fewer):
- *            its input rows are not read and its output rows are 0.  Device-side: a
+ *            its input rows do not count and its output rows are 0.  Device-side: a
  *            parent that is not before its child, or no node, makes the child and all
  *            that follow it bad: NaN in their output rows, and nothing is stored of them.
  *            With KDA_VALIDATE=1 the attention, append and commit calls check the trees
