@@ -35,23 +35,52 @@ __device__ __forceinline__ int scan_exclusive(int x, int* sh, int* total) {
   return before + y - x;
 }
 
+// A round of a search through the pages by one workgroup: a wave looks at kChunks times 64
+// pages that follow each other, a lane at one of each 64, so that loads are whole lines and
+// a place is a count of bits.
+constexpr int kChunks = 8, kRound = kChunks * kScan;
+__device__ __forceinline__ int64_t search_page(int64_t p0, int chunk) {
+  return p0 + (threadIdx.x >> 6) * (64 * kChunks) + 64 * chunk + (threadIdx.x & 63);
+}
+// Sum of the waves' x (the same in a wave's lanes) before this wave, and of all.  sh: 16 words.
+__device__ __forceinline__ int waves_before(int x, int* sh, int* total) {
+  const int wv = threadIdx.x >> 6;
+  __syncthreads();  // sh is free
+  if ((threadIdx.x & 63) == 0) sh[wv] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kScan / 64; ++i) {
+    before += i < wv ? sh[i] : 0;
+    all += sh[i];
+  }
+  *total = all;
+  return before;
+}
+
 // The first `want` free pages, ascending, to out; how many there are (at most `want`
-// counts).  Each thread looks at four pages a round.
+// counts).
 __device__ __forceinline__ int find_free(const int32_t* refs, int num_pages, int want, int32_t* out, int* sh) {
+  const uint64_t under = (1ull << (threadIdx.x & 63)) - 1;
   int found = 0;
-  for (int p0 = 0; p0 < num_pages && found < want; p0 += 4 * kScan) {
-    const int p = p0 + 4 * threadIdx.x;
-    uint32_t is = 0;
+  for (int64_t p0 = 0; p0 < num_pages && found < want; p0 += kRound) {
+    int is[kChunks];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) is |= (p + i < num_pages && refs[p + i] <= 0) ? 1u << i : 0u;
-    int all;
-    int at = found + scan_exclusive(__builtin_popcount(is), sh, &all);
+    for (int i = 0; i < kChunks; ++i) is[i] = refs[min(search_page(p0, i), (int64_t)num_pages - 1)];
+    uint64_t m[kChunks];
+    int mine = 0, all;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (is >> i & 1) {
-        if (at < want) out[at] = p + i;
-        ++at;
-      }
+    for (int i = 0; i < kChunks; ++i) {
+      m[i] = __ballot(is[i] <= 0 && search_page(p0, i) < num_pages);
+      mine += __popcll(m[i]);
+    }
+    int at = found + waves_before(mine, sh, &all);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const int to = at + __popcll(m[i] & under);
+      if ((m[i] & (under + 1)) && to < want) out[to] = (int)search_page(p0, i);
+      at += __popcll(m[i]);
+    }
     found += all;
   }
   return min(found, want);
@@ -67,52 +96,84 @@ __device__ __forceinline__ Range overlapped(int lo, int hi, int page_tokens, int
   return Range{lo / page_tokens, (int)min((int64_t)max_pages, ((int64_t)hi + page_tokens - 1) / page_tokens)};
 }
 
+// A call of reserve, fork or compact is several steps, each of which needs all of the one
+// before.  A step goes over its items from `first` on, `count` apart.  Where there is little
+// to do one workgroup of kScan threads takes all steps in one launch; otherwise they are
+// launches of their own, and only the scans are one workgroup's.
+struct Items {
+  int64_t first, count;
+};
+__device__ __forceinline__ Items own_threads() { return Items{threadIdx.x, kScan}; }
+__device__ __forceinline__ Items own_waves() { return Items{threadIdx.x >> 6, kScan / 64}; }
+__device__ __forceinline__ Items all_threads() { return Items{(int64_t)blockIdx.x * 256 + threadIdx.x, (int64_t)gridDim.x * 256}; }
+__device__ __forceinline__ Items all_waves() { return Items{blockIdx.x * 4 + (threadIdx.x >> 6), (int64_t)gridDim.x * 4}; }
+
+// Ranks of the x(i) things of items 0..n-1, written by put(i, x, rank); how many there are.
+template <typename X, typename Put> __device__ __forceinline__ int rank_all(int n, int* sh, X x, Put put) {
+  int before = 0;
+  for (int64_t i0 = 0; i0 < n; i0 += kScan) {
+    const int64_t i = i0 + threadIdx.x;
+    const int mine = i < n ? x((int)i) : 0;
+    int all;
+    const int at = before + scan_exclusive(mine, sh, &all);
+    if (i < n) put((int)i, mine, at);
+    before += all;
+  }
+  return before;
+}
+
 // reserve: entries that hold no page, row by row (a wave each) ...
-__global__ __launch_bounds__(256) void pages_need_kernel(PagesArgs a) {
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (row >= a.rows) return;
-  const Range e = overlapped(a.first[row], a.last[row], a.page_tokens, a.max_pages);
-  const int32_t* t = a.table + (int64_t)row * a.max_pages;
-  int need = 0;
-  for (int j = e.begin; j < e.end; j += 64)
-    need += __popcll(__ballot(j + lane < e.end && t[j + lane] < 0));
-  if (lane == 0) a.w.need[row] = need;
+__device__ __forceinline__ void reserve_need(const PagesArgs& a, Items it) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t row = it.first; row < a.rows; row += it.count) {
+    const Range e = overlapped(a.first[row], a.last[row], a.page_tokens, a.max_pages);
+    const int32_t* t = a.table + row * a.max_pages;
+    int need = 0;
+    for (int j = e.begin; j < e.end; j += 64) need += __popcll(__ballot(j + lane < e.end && t[j + lane] < 0));
+    if (lane == 0) a.w.need[row] = need;
+  }
 }
 // ... their ranks among all, and as many free pages ...
-__global__ __launch_bounds__(kScan) void pages_find_kernel(PagesArgs a) {
-  __shared__ int sh[kScan / 64];
-  int want = 0;
-  for (int r0 = 0; r0 < a.rows; r0 += kScan) {
-    const int r = r0 + threadIdx.x, x = r < a.rows ? a.w.need[r] : 0;
-    int all;
-    const int at = want + scan_exclusive(x, sh, &all);
-    if (r < a.rows) a.w.need[r] = at;
-    want += all;
-  }
+__device__ __forceinline__ void reserve_find(const PagesArgs& a, int* sh) {
+  const int want = rank_all(a.rows, sh, [&](int r) { return a.w.need[r]; }, [&](int r, int, int at) { a.w.need[r] = at; });
   const int found = find_free(a.refs, a.num_pages, min(want, a.num_pages), a.w.free, sh);
   if (threadIdx.x == 0) a.w.total[0] = found;
 }
 // ... which go to them in that order.
-__global__ __launch_bounds__(256) void pages_take_kernel(PagesArgs a) {
-  const int row = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (row >= a.rows) return;
-  const Range e = overlapped(a.first[row], a.last[row], a.page_tokens, a.max_pages);
-  int32_t* t = a.table + (int64_t)row * a.max_pages;
-  const int found = a.w.total[0];
-  int at = a.w.need[row], missing = 0;
-  for (int j = e.begin; j < e.end; j += 64) {
-    const bool none = j + lane < e.end && t[j + lane] < 0;
-    const uint64_t m = __ballot(none);
-    const int mine = at + __popcll(m & ((1ull << lane) - 1));
-    if (none && mine < found) {
-      const int page = a.w.free[mine];
-      t[j + lane] = page;
-      a.refs[page] = 1;
+__device__ __forceinline__ void reserve_take(const PagesArgs& a, Items it) {
+  const int lane = threadIdx.x & 63, found = a.w.total[0];
+  for (int64_t row = it.first; row < a.rows; row += it.count) {
+    const Range e = overlapped(a.first[row], a.last[row], a.page_tokens, a.max_pages);
+    int32_t* t = a.table + row * a.max_pages;
+    int at = a.w.need[row], missing = 0;
+    for (int j = e.begin; j < e.end; j += 64) {
+      const bool none = j + lane < e.end && t[j + lane] < 0;
+      const uint64_t m = __ballot(none);
+      const int mine = at + __popcll(m & ((1ull << lane) - 1));
+      if (none && mine < found) {
+        const int page = a.w.free[mine];
+        t[j + lane] = page;
+        a.refs[page] = 1;
+      }
+      at += __popcll(m);
+      missing += __popcll(__ballot(none && mine >= found));
     }
-    at += __popcll(m);
-    missing += __popcll(__ballot(none && mine >= found));
+    if (lane == 0) a.status[row] = missing;
   }
-  if (lane == 0) a.status[row] = missing;
+}
+__global__ __launch_bounds__(256) void pages_need_kernel(PagesArgs a) { reserve_need(a, all_waves()); }
+__global__ __launch_bounds__(kScan) void pages_find_kernel(PagesArgs a) {
+  __shared__ int sh[kScan / 64];
+  reserve_find(a, sh);
+}
+__global__ __launch_bounds__(256) void pages_take_kernel(PagesArgs a) { reserve_take(a, all_waves()); }
+__global__ __launch_bounds__(kScan) void pages_reserve_kernel(PagesArgs a) {
+  __shared__ int sh[kScan / 64];
+  reserve_need(a, own_waves());
+  __syncthreads();
+  reserve_find(a, sh);
+  __syncthreads();
+  reserve_take(a, own_waves());
 }
 
 // free: an entry whose tokens all lie in [first, last) lets go of its page.
@@ -129,100 +190,128 @@ __global__ __launch_bounds__(256) void pages_free_kernel(PagesArgs a) {
   }
 }
 
-// fork: which forks are made, and their tail pages (one workgroup; the forks in rounds of
-// kScan).  need[i]: the rank of fork i's tail page, -1 for none, -2 where it is not made.
-__global__ __launch_bounds__(256) void pages_fork_check_kernel(PagesArgs a) {
-  const int i = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-  if (i >= a.n) return;
-  const int s = a.src[i], d = a.dst[i], tok = a.tokens[i];
-  int need = -2, status = 2;
-  if (tok < 0) {
-    status = 0;
-  } else if (s >= 0 && s < a.rows && d >= 0 && d < a.rows && s != d && tok <= (int64_t)a.max_pages * a.page_tokens) {
-    bool some = false;
-    const int32_t* t = a.table + (int64_t)d * a.max_pages;
-    for (int j = lane; j < a.max_pages; j += 64) some |= t[j] >= 0;
-    if (!__any(some)) {
+// fork: which forks are made, and which have a tail page (a wave each): need[i] is 0 with a
+// tail page, -1 without one, -2 where the fork is not made ...
+__device__ __forceinline__ void fork_check(const PagesArgs& a, Items it) {
+  const int lane = threadIdx.x & 63;
+  for (int64_t i = it.first; i < a.n; i += it.count) {
+    const int s = a.src[i], d = a.dst[i], tok = a.tokens[i];
+    int need = -2, status = 2;
+    if (tok < 0) {
       status = 0;
-      need = -1;
-      if (tok % a.page_tokens) {
-        const int tail = a.table[(int64_t)s * a.max_pages + tok / a.page_tokens];
-        if (tail >= 0 && tail < a.num_pages) need = 0;
+    } else if (s >= 0 && s < a.rows && d >= 0 && d < a.rows && s != d && tok <= (int64_t)a.max_pages * a.page_tokens) {
+      bool some = false;
+      const int32_t* t = a.table + (int64_t)d * a.max_pages;
+      for (int j = lane; j < a.max_pages; j += 64) some |= t[j] >= 0;
+      if (!__any(some)) {
+        status = 0;
+        need = -1;
+        if (tok % a.page_tokens) {
+          const int tail = a.table[(int64_t)s * a.max_pages + tok / a.page_tokens];
+          if (tail >= 0 && tail < a.num_pages) need = 0;
+        }
       }
     }
-  }
-  if (lane == 0) {
-    a.w.need[i] = need;
-    a.status[i] = status;
+    if (lane == 0) {
+      a.w.need[i] = need;
+      a.status[i] = status;
+    }
   }
 }
-__global__ __launch_bounds__(kScan) void pages_fork_find_kernel(PagesArgs a) {
-  __shared__ int sh[kScan / 64];
-  int want = 0;
-  for (int i0 = 0; i0 < a.n; i0 += kScan) {
-    const int i = i0 + threadIdx.x, tail = i < a.n && a.w.need[i] == 0;
-    int all;
-    const int at = want + scan_exclusive(tail, sh, &all);
-    if (tail) a.w.need[i] = at;
-    want += all;
-  }
+// ... the tail pages' ranks, and free pages for them ...
+__device__ __forceinline__ void fork_find(const PagesArgs& a, int* sh) {
+  const int want = rank_all(a.n, sh, [&](int i) { return a.w.need[i] == 0 ? 1 : 0; },
+                            [&](int i, int tail, int at) { if (tail) a.w.need[i] = at; });
   const int found = find_free(a.refs, a.num_pages, min(want, a.num_pages), a.w.free, sh);
   if (threadIdx.x == 0) a.w.total[0] = found;
 }
-__global__ __launch_bounds__(256) void pages_fork_kernel(PagesArgs a) {
-  const int i = blockIdx.x, rank = a.w.need[i], found = a.w.total[0];
-  // the list of copies ends where the tails do
-  if (threadIdx.x == 0 && i >= found) {
-    a.copy_src[i] = a.copy_dst[i] = -1;
-    a.copy_tokens[i] = 0;
+// ... the rows (a wave each).  The list of copies ends where the tails do.
+__device__ __forceinline__ void fork_rows(const PagesArgs& a, Items it) {
+  const int lane = threadIdx.x & 63, found = a.w.total[0];
+  for (int64_t i = it.first; i < a.n; i += it.count) {
+    const int rank = a.w.need[i];
+    if (lane == 0 && i >= found) {
+      a.copy_src[i] = a.copy_dst[i] = -1;
+      a.copy_tokens[i] = 0;
+    }
+    if (rank == -2) continue;
+    if (rank >= found) {  // no page for the tail
+      if (lane == 0) a.status[i] = 1;
+      continue;
+    }
+    const int tok = a.tokens[i], full = tok / a.page_tokens;
+    const int32_t* s = a.table + (int64_t)a.src[i] * a.max_pages;
+    int32_t* d = a.table + (int64_t)a.dst[i] * a.max_pages;
+    for (int j = lane; j < full; j += 64) {
+      const int page = s[j];
+      d[j] = page;
+      if (page >= 0 && page < a.num_pages) atomicAdd(a.refs + page, 1);
+    }
+    if (lane == 0 && rank >= 0) {
+      const int page = a.w.free[rank];
+      d[full] = page;
+      a.refs[page] = 1;
+      a.copy_src[rank] = s[full];
+      a.copy_dst[rank] = page;
+      a.copy_tokens[rank] = tok % a.page_tokens;
+    }
   }
-  if (rank == -2) return;
-  if (rank >= found) {  // no page for the tail
-    if (threadIdx.x == 0) a.status[i] = 1;
-    return;
-  }
-  const int tok = a.tokens[i], full = tok / a.page_tokens;
-  const int32_t* s = a.table + (int64_t)a.src[i] * a.max_pages;
-  int32_t* d = a.table + (int64_t)a.dst[i] * a.max_pages;
-  for (int j = threadIdx.x; j < full; j += 256) {
-    const int page = s[j];
-    d[j] = page;
-    if (page >= 0 && page < a.num_pages) atomicAdd(a.refs + page, 1);
-  }
-  if (threadIdx.x == 0 && rank >= 0) {
-    const int page = a.w.free[rank];
-    d[full] = page;
-    a.refs[page] = 1;
-    a.copy_src[rank] = s[full];
-    a.copy_dst[rank] = page;
-    a.copy_tokens[rank] = tok % a.page_tokens;
-  }
+}
+__global__ __launch_bounds__(256) void pages_fork_check_kernel(PagesArgs a) { fork_check(a, all_waves()); }
+__global__ __launch_bounds__(kScan) void pages_fork_find_kernel(PagesArgs a) {
+  __shared__ int sh[kScan / 64];
+  fork_find(a, sh);
+}
+__global__ __launch_bounds__(256) void pages_fork_rows_kernel(PagesArgs a) { fork_rows(a, all_waves()); }
+__global__ __launch_bounds__(kScan) void pages_fork_kernel(PagesArgs a) {
+  __shared__ int sh[kScan / 64];
+  fork_check(a, own_waves());
+  __syncthreads();
+  fork_find(a, sh);
+  __syncthreads();
+  fork_rows(a, own_waves());
 }
 
 // compact: how many table entries hold each page ...
-__global__ __launch_bounds__(256) void pages_clear_kernel(PagesArgs a) {
-  const int p = blockIdx.x * 256 + threadIdx.x;
-  if (p < a.num_pages) a.w.held[p] = 0;
+__device__ __forceinline__ void compact_clear(const PagesArgs& a, Items it) {
+  for (int64_t p = it.first; p < a.num_pages; p += it.count) a.w.held[p] = 0;
 }
-__global__ __launch_bounds__(256) void pages_held_kernel(PagesArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)a.rows * a.max_pages) return;
-  const int page = a.table[i];
-  if (page >= 0 && page < a.num_pages) atomicAdd(a.w.held + page, 1);
+__device__ __forceinline__ void compact_count(const PagesArgs& a, Items it) {
+  for (int64_t i = it.first; i < (int64_t)a.rows * a.max_pages; i += it.count) {
+    const int page = a.table[i];
+    if (page >= 0 && page < a.num_pages) atomicAdd(a.w.held + page, 1);
+  }
 }
-// ... the free pages and the pages that only tables hold, both ascending ...
-__global__ __launch_bounds__(kScan) void pages_sort_kernel(PagesArgs a) {
-  __shared__ int sh[kScan / 64];
+// ... the free pages and the pages that only tables hold, both ascending (one workgroup) ...
+__device__ __forceinline__ void compact_sort(const PagesArgs& a, int* sh) {
+  const uint64_t under = (1ull << (threadIdx.x & 63)) - 1;
   int nfree = 0, nmove = 0;
-  for (int p0 = 0; p0 < a.num_pages; p0 += kScan) {
-    const int p = p0 + threadIdx.x;
-    const int refs = p < a.num_pages ? a.refs[p] : 1, held = p < a.num_pages ? a.w.held[p] : 0;
-    const bool is_free = refs <= 0, moves = refs > 0 && refs == held;
-    // both counts in one word: a round has 1024 of each at most
-    int all;
-    const int at = scan_exclusive((is_free ? 1 : 0) | (moves ? 1 << 16 : 0), sh, &all);
-    if (is_free) a.w.free[nfree + (at & 0xffff)] = p;
-    if (moves) a.w.move[nmove + (at >> 16)] = p;
+  for (int64_t p0 = 0; p0 < a.num_pages; p0 += kRound) {
+    int refs[kChunks], held[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {  // the counts were added up behind the vector cache, so they are read there
+      const int64_t p = min(search_page(p0, i), (int64_t)a.num_pages - 1);
+      refs[i] = a.refs[p];
+      held[i] = __hip_atomic_load(a.w.held + p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    uint64_t is_free[kChunks], moves[kChunks];
+    int mine = 0, all;  // both counts in one word: a round has 8192 of each at most
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      const bool in = search_page(p0, i) < a.num_pages;
+      is_free[i] = __ballot(in && refs[i] <= 0);
+      moves[i] = __ballot(in && refs[i] > 0 && refs[i] == held[i]);
+      mine += __popcll(is_free[i]) + (__popcll(moves[i]) << 16);
+    }
+    const int before = waves_before(mine, sh, &all);
+    int to_free = nfree + (before & 0xffff), to_move = nmove + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      if (is_free[i] & (under + 1)) a.w.free[to_free + __popcll(is_free[i] & under)] = (int)search_page(p0, i);
+      if (moves[i] & (under + 1)) a.w.move[to_move + __popcll(moves[i] & under)] = (int)search_page(p0, i);
+      to_free += __popcll(is_free[i]);
+      to_move += __popcll(moves[i]);
+    }
     nfree += all & 0xffff;
     nmove += all >> 16;
   }
@@ -231,53 +320,114 @@ __global__ __launch_bounds__(kScan) void pages_sort_kernel(PagesArgs a) {
     a.w.total[1] = nmove;
   }
 }
-// ... of which the i-th highest goes to the i-th lowest free page while that is lower.
-// held then says where each page went.
-__global__ __launch_bounds__(256) void pages_move_kernel(PagesArgs a) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.num_pages) return;
-  int src = -1, dst = -1;
-  if (i < a.w.total[0] && i < a.w.total[1]) {
-    const int s = a.w.move[a.w.total[1] - 1 - i], d = a.w.free[i];
-    if (d < s) {
-      src = s;
-      dst = d;
-      a.refs[d] = a.refs[s];
-      a.refs[s] = 0;
+// ... of which the i-th highest goes to the i-th lowest free page while that is lower.  held
+// is made to say where each page is from now on: here that it stays, then those that moved.
+__device__ __forceinline__ void compact_move(const PagesArgs& a, Items it) {
+  const int nfree = a.w.total[0], nmove = a.w.total[1];
+  for (int64_t i = it.first; i < a.num_pages; i += it.count) {
+    int src = -1, dst = -1;
+    if (i < nfree && i < nmove) {
+      const int s = a.w.move[nmove - 1 - i], d = a.w.free[i];
+      if (d < s) {
+        src = s;
+        dst = d;
+        a.refs[d] = a.refs[s];
+        a.refs[s] = 0;
+      }
     }
+    a.copy_src[i] = src;
+    a.copy_dst[i] = dst;
+    a.w.held[i] = (int)i;
   }
-  a.copy_src[i] = src;
-  a.copy_dst[i] = dst;
 }
-__global__ __launch_bounds__(256) void pages_place_kernel(PagesArgs a) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i < a.num_pages) a.w.held[i] = i;
+__device__ __forceinline__ void compact_moved(const PagesArgs& a, Items it) {
+  for (int64_t i = it.first; i < a.num_pages; i += it.count)
+    if (a.copy_src[i] >= 0) a.w.held[a.copy_src[i]] = a.copy_dst[i];
 }
-__global__ __launch_bounds__(256) void pages_moved_kernel(PagesArgs a) {
-  const int i = blockIdx.x * 256 + threadIdx.x;
-  if (i < a.num_pages && a.copy_src[i] >= 0) a.w.held[a.copy_src[i]] = a.copy_dst[i];
+__device__ __forceinline__ void compact_remap(const PagesArgs& a, Items it) {
+  for (int64_t i = it.first; i < (int64_t)a.rows * a.max_pages; i += it.count) {
+    const int page = a.table[i];
+    if (page >= 0 && page < a.num_pages) a.table[i] = a.w.held[page];
+  }
 }
-__global__ __launch_bounds__(256) void pages_remap_kernel(PagesArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= (int64_t)a.rows * a.max_pages) return;
-  const int page = a.table[i];
-  if (page >= 0 && page < a.num_pages) a.table[i] = a.w.held[page];
+__global__ __launch_bounds__(256) void pages_clear_kernel(PagesArgs a) { compact_clear(a, all_threads()); }
+__global__ __launch_bounds__(256) void pages_count_kernel(PagesArgs a) { compact_count(a, all_threads()); }
+__global__ __launch_bounds__(kScan) void pages_sort_kernel(PagesArgs a) {
+  __shared__ int sh[kScan / 64];
+  compact_sort(a, sh);
+}
+__global__ __launch_bounds__(256) void pages_move_kernel(PagesArgs a) { compact_move(a, all_threads()); }
+__global__ __launch_bounds__(256) void pages_moved_kernel(PagesArgs a) { compact_moved(a, all_threads()); }
+__global__ __launch_bounds__(256) void pages_remap_kernel(PagesArgs a) { compact_remap(a, all_threads()); }
+__global__ __launch_bounds__(kScan) void pages_compact_kernel(PagesArgs a) {
+  __shared__ int sh[kScan / 64];
+  compact_clear(a, own_threads());
+  __syncthreads();
+  compact_count(a, own_threads());
+  __syncthreads();
+  compact_sort(a, sh);
+  __syncthreads();
+  compact_move(a, own_threads());
+  __syncthreads();
+  compact_moved(a, own_threads());
+  __syncthreads();
+  compact_remap(a, own_threads());
 }
 
-// Pages src[i] to dst[i]: whole, or the blocks that hold their first tokens.  A list may be
-// long and mostly empty (a compaction's has an entry for every page of the pool), so a
-// workgroup gathers the pairs to copy from 1024 entries at a time, the next 1024 on their
-// way meanwhile.  blockIdx.x is a piece of 16 KB of a head's blocks, and blockIdx.y takes
-// the pairs in turn.
+// Pages src[i] to dst[i]: whole, or the blocks that hold their first tokens.  A workgroup
+// takes a piece of 16 KB of a head's blocks.  A list may be long and mostly empty (a
+// compaction's has an entry for every page of the pool): then a workgroup gathers the pairs
+// to copy from 1024 entries at a time, the next 1024 on their way meanwhile, and takes its
+// piece of them in turn.  Bound by memory: 32 MB copied take 19 us in pages, 14 us in one
+// piece.
 constexpr int kCopyPiece = 16384, kCopyList = 1024;
-__global__ __launch_bounds__(256) void kv_copy_pages_kernel(CopyPagesArgs a) {
+__device__ __forceinline__ bool is_copy(const CopyPagesArgs& a, int src, int dst) {
+  return src >= 0 && src < a.num_pages && dst >= 0 && dst < a.num_pages && src != dst;
+}
+__device__ __forceinline__ int copy_blocks(const CopyPagesArgs& a, int tokens) {
+  return a.tokens ? min(max(0, (int)(((int64_t)tokens + 31) / 32)), a.blocks) : a.blocks;
+}
+__device__ __forceinline__ void copy_piece(const CopyPagesArgs& a, int64_t whole, int h, int piece, int src, int dst, int blocks) {
+  const int64_t lo = (int64_t)piece * kCopyPiece, hi = min(lo + kCopyPiece, (int64_t)blocks * a.block_bytes);
+  const uint8_t* from = a.base + src * a.page_bytes + h * a.head_bytes;
+  uint8_t* to = a.base + dst * a.page_bytes + h * a.head_bytes;
+  const int tid = threadIdx.x;
+  u32x4_t x[kCopyPiece / 4096];
+#pragma unroll
+  for (int j = 0; j < kCopyPiece / 4096; ++j) {
+    const int64_t p = lo + 4096 * j + 16 * tid;
+    if (p < hi) x[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from + p));
+  }
+#pragma unroll
+  for (int j = 0; j < kCopyPiece / 4096; ++j) {
+    const int64_t p = lo + 4096 * j + 16 * tid;
+    if (p < hi) __builtin_nontemporal_store(x[j], reinterpret_cast<u32x4_t*>(to + p));
+  }
+  if (piece == 0)
+    for (int b = tid; b < blocks && a.scale_bytes; b += 256)
+      *reinterpret_cast<u32x2_t*>(to + whole + 8 * b) = *reinterpret_cast<const u32x2_t*>(from + whole + 8 * b);
+}
+// The workgroups of an XCD (every eighth) take units that follow each other, so that a page
+// is copied, and its addresses translated, by one or two of them (64 tail pages of 1 MB, half
+// full: 21 -> 19 us).
+__device__ __forceinline__ int copy_unit() {
+  const int all = gridDim.x, x = blockIdx.x % 8;
+  return x * (all / 8) + min(x, all % 8) + blockIdx.x / 8;
+}
+__global__ __launch_bounds__(256, 8) void kv_copy_pages_kernel(CopyPagesArgs a) {
+  const int64_t whole = (int64_t)a.block_bytes * a.blocks;
+  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece), unit = copy_unit(), i = unit / (pieces * a.heads);
+  const int rest = unit % (pieces * a.heads), h = rest / pieces, piece = rest % pieces;
+  const int src = a.src[i], dst = a.dst[i], tokens = a.tokens ? a.tokens[i] : 0;
+  if (is_copy(a, src, dst)) copy_piece(a, whole, h, piece, src, dst, copy_blocks(a, tokens));
+}
+__global__ __launch_bounds__(256) void kv_copy_list_kernel(CopyPagesArgs a) {
   __shared__ int list[kCopyList][3];  // src, dst, blocks
   __shared__ int part[4];
   const int tid = threadIdx.x, lane = tid & 63, wv = tid >> 6;
   const int64_t whole = (int64_t)a.block_bytes * a.blocks;
-  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece), h = blockIdx.x / pieces, piece = blockIdx.x % pieces;
-  const int64_t lo = (int64_t)piece * kCopyPiece;
-  const uint8_t* const head = a.base + h * a.head_bytes;
+  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece), per = pieces * a.heads;
+  const int rest = blockIdx.x % per, h = rest / pieces, piece = rest % pieces, turns = gridDim.x / per;
   int src[4], dst[4], tokens[4];
   auto ask = [&](int64_t i0) {
 #pragma unroll
@@ -289,11 +439,11 @@ __global__ __launch_bounds__(256) void kv_copy_pages_kernel(CopyPagesArgs a) {
     }
   };
   ask(0);
-  int first = blockIdx.y;  // of the pairs gathered next
+  int first = blockIdx.x / per;  // of the pairs gathered next
   for (int64_t i0 = 0; i0 < a.n; i0 += kCopyList) {
     int is = 0, pairs = 0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) is += src[j] >= 0 && src[j] < a.num_pages && dst[j] >= 0 && dst[j] < a.num_pages && src[j] != dst[j];
+    for (int j = 0; j < 4; ++j) is += is_copy(a, src[j], dst[j]);
     int y = is;
 #pragma unroll
     for (int i = 1; i < 64; i <<= 1) {
@@ -311,40 +461,32 @@ __global__ __launch_bounds__(256) void kv_copy_pages_kernel(CopyPagesArgs a) {
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (src[j] >= 0 && src[j] < a.num_pages && dst[j] >= 0 && dst[j] < a.num_pages && src[j] != dst[j]) {
+      if (is_copy(a, src[j], dst[j])) {
         list[at][0] = src[j];
         list[at][1] = dst[j];
-        list[at++][2] = a.tokens ? min(max(0, (int)(((int64_t)tokens[j] + 31) / 32)), a.blocks) : a.blocks;
+        list[at++][2] = copy_blocks(a, tokens[j]);
       }
     ask(i0 + kCopyList);
     __syncthreads();
-    for (; first < pairs; first += gridDim.y) {
-      const int blocks = list[first][2];
-      const uint8_t* from = head + list[first][0] * a.page_bytes;
-      uint8_t* to = const_cast<uint8_t*>(head) + list[first][1] * a.page_bytes;
-      const int64_t hi = min(lo + kCopyPiece, (int64_t)blocks * a.block_bytes);
-      u32x4_t x[kCopyPiece / 4096];
-#pragma unroll
-      for (int j = 0; j < kCopyPiece / 4096; ++j) {
-        const int64_t p = lo + 4096 * j + 16 * tid;
-        if (p < hi) x[j] = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(from + p));
-      }
-#pragma unroll
-      for (int j = 0; j < kCopyPiece / 4096; ++j) {
-        const int64_t p = lo + 4096 * j + 16 * tid;
-        if (p < hi) __builtin_nontemporal_store(x[j], reinterpret_cast<u32x4_t*>(to + p));
-      }
-      if (piece == 0)
-        for (int b = tid; b < blocks && a.scale_bytes; b += 256)
-          *reinterpret_cast<u32x2_t*>(to + whole + 8 * b) = *reinterpret_cast<const u32x2_t*>(from + whole + 8 * b);
-    }
+    for (; first < pairs; first += turns) copy_piece(a, whole, h, piece, list[first][0], list[first][1], list[first][2]);
     first -= pairs;
   }
 }
 
 static dim3 over(int64_t n, int per) { return dim3((unsigned)((n + per - 1) / per)); }
 
+// One launch where that is quicker.  A compaction (one launch, then six; us): 4096 entries and
+// 4000 pages 8.2, 12.8; 8192 and 8000 12.5, 13.2; 16384 and 16000 24, 16.
+constexpr int64_t kFewEntries = 8192, kFewPages = 8192;
+// Of reserve and fork, by rows of the table times the 64-entry pieces of one (one launch, then
+// three): 8 3.1, 5.9; 64 4.6, 6.2; 128 6.4, 6.0.
+static bool few_rows(int64_t rows, int max_pages) { return rows * ((max_pages + 63) / 64) <= 64; }
+
 hipError_t launch_pages_reserve(const PagesArgs& a, hipStream_t st) {
+  if (few_rows(a.rows, a.max_pages)) {
+    hipLaunchKernelGGL(pages_reserve_kernel, dim3(1), dim3(kScan), 0, st, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(pages_need_kernel, over(a.rows, 4), dim3(256), 0, st, a);
   hipLaunchKernelGGL(pages_find_kernel, dim3(1), dim3(kScan), 0, st, a);
   hipLaunchKernelGGL(pages_take_kernel, over(a.rows, 4), dim3(256), 0, st, a);
@@ -355,27 +497,38 @@ hipError_t launch_pages_free(const PagesArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 hipError_t launch_pages_fork(const PagesArgs& a, hipStream_t st) {
+  if (few_rows(a.n, a.max_pages)) {
+    hipLaunchKernelGGL(pages_fork_kernel, dim3(1), dim3(kScan), 0, st, a);
+    return hipGetLastError();
+  }
   hipLaunchKernelGGL(pages_fork_check_kernel, over(a.n, 4), dim3(256), 0, st, a);
   hipLaunchKernelGGL(pages_fork_find_kernel, dim3(1), dim3(kScan), 0, st, a);
-  hipLaunchKernelGGL(pages_fork_kernel, dim3((unsigned)a.n), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(pages_fork_rows_kernel, over(a.n, 4), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 hipError_t launch_pages_compact(const PagesArgs& a, hipStream_t st) {
-  const dim3 pages = over(a.num_pages, 256), entries = over((int64_t)a.rows * a.max_pages, 256);
+  const int64_t entries = (int64_t)a.rows * a.max_pages;
+  if (entries <= kFewEntries && a.num_pages <= kFewPages) {
+    hipLaunchKernelGGL(pages_compact_kernel, dim3(1), dim3(kScan), 0, st, a);
+    return hipGetLastError();
+  }
+  const dim3 pages = over(a.num_pages, 256), all = over(entries, 256);
   hipLaunchKernelGGL(pages_clear_kernel, pages, dim3(256), 0, st, a);
-  hipLaunchKernelGGL(pages_held_kernel, entries, dim3(256), 0, st, a);
+  hipLaunchKernelGGL(pages_count_kernel, all, dim3(256), 0, st, a);
   hipLaunchKernelGGL(pages_sort_kernel, dim3(1), dim3(kScan), 0, st, a);
   hipLaunchKernelGGL(pages_move_kernel, pages, dim3(256), 0, st, a);
-  hipLaunchKernelGGL(pages_place_kernel, pages, dim3(256), 0, st, a);
   hipLaunchKernelGGL(pages_moved_kernel, pages, dim3(256), 0, st, a);
-  hipLaunchKernelGGL(pages_remap_kernel, entries, dim3(256), 0, st, a);
+  hipLaunchKernelGGL(pages_remap_kernel, all, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 hipError_t launch_kv_copy_pages(const CopyPagesArgs& a, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.block_bytes * a.blocks + kCopyPiece - 1) / kCopyPiece * a.heads;
-  // 2048 workgroups, eight a CU, are there at once; more would gather the list for little
-  const int64_t fill = 2048 / pieces > 0 ? 2048 / pieces : 1, turns = a.n < fill ? a.n : fill;
-  hipLaunchKernelGGL(kv_copy_pages_kernel, dim3((unsigned)pieces, (unsigned)turns), dim3(256), 0, st, a);
+  // A workgroup for each piece of each entry, up to four times as many as the CUs hold; past
+  // that most of them would find nothing to copy.
+  const bool each = a.n * pieces <= 8192;
+  const dim3 grid((unsigned)(pieces * (each ? a.n : pieces < 2048 ? 2048 / pieces : 1)));
+  if (each) hipLaunchKernelGGL(kv_copy_pages_kernel, grid, dim3(256), 0, st, a);
+  else hipLaunchKernelGGL(kv_copy_list_kernel, grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 
