@@ -169,78 +169,33 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
     return;
   }
   const int c0 = CPL * (16 * wv + col);
-  const TreeNode tree = tree_node(a.parent + row0, T);
-  const uint64_t good = __ballot(tree.good());
-  if (tid < 64) {
-    way[tid] = tree.way;
-    odd[tid] = 0;
-  }
-  __syncthreads();
   auto in = [&](const void* p, int64_t at) { return load_as_f(reinterpret_cast<const In*>(p) + at); };
-  auto place = [&](int t) { return (row0 + t) * a.H + h; };  // (row, head)
+  // (row, head); entries past the tree repeat its last one, whose values are then not used
+  auto place = [&](int t) { return (row0 + min(t, T - 1)) * a.H + h; };
 
-  // ---- gates summed along the ways, as a product with the 0/1 matrix of ways; then the
-  // factors.  A wave takes columns 16 ct .. of all nodes.
-  bool far = false;
-  for (int ct = wv; ct < D / 16; ct += WAVES) {
-    const int c = 16 * ct + col;
-    f32x4 G[NT];
+  // ---- everything a wave needs is asked for here, the state last: what is asked for is
+  // answered in order, and the state is needed last.  A wave takes columns 16 ct .. of all
+  // nodes' gates, keys and queries, and c0 .. of their values and of the state.
+  constexpr int CT = D / 16 / WAVES;
+  const int parent = lane < T ? a.parent[row0 + lane] : -2;
+  float gate[CT][4 * NT], key[CT][4 * NT], query[CT][4 * NT], bt[4 * NT], vt[4 * NT][CPL];
 #pragma unroll
-    for (int i = 0; i < NT; ++i) G[i] = zero4();
+  for (int i = 0; i < 4 * NT; ++i)
 #pragma unroll
-    for (int ks = 0; ks < 4 * NT; ++ks) {
-      const int s = 4 * ks + g;
-      float x = 0.f;
-      if (good >> s & 1) {
-        x = in(a.g, place(s) * D + c);
-        if (!(x < __builtin_inff())) {
-          odd[s] = 1;
-          x = 0.f;
-        }
-        x = fmaxf(x, -104.f);
-      }
+    for (int ct = 0; ct < CT; ++ct) gate[ct][i] = in(a.g, place(4 * i + g) * D + 16 * (wv + WAVES * ct) + col);
 #pragma unroll
-      for (int i = ks / 4; i < NT; ++i) G[i] = mma1(way[16 * i + col] >> s & 1 ? 1.f : 0.f, x, G[i]);
+  for (int i = 0; i < 4 * NT; ++i) {  // row 16 kb + 4 g + i
+    const int64_t at = place(16 * (i >> 2) + 4 * g + (i & 3));
+#pragma unroll
+    for (int ct = 0; ct < CT; ++ct) {
+      key[ct][i] = in(a.k, at * D + 16 * (wv + WAVES * ct) + col);
+      query[ct][i] = in(a.q, at * D + 16 * (wv + WAVES * ct) + col);
     }
+    bt[i] = in(a.beta, at);
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * i + 4 * g + e;
-        float k = 0.f, q = 0.f, beta = 0.f, x = 0.f;
-        if (good >> t & 1) {
-          k = in(a.k, place(t) * D + c);
-          q = in(a.q, place(t) * D + c);
-          beta = in(a.beta, place(t));
-          x = G[i][e];
-          if (!is_finite(k) || !is_finite(beta)) {
-            odd[t] = 1;
-            k = beta = 0.f;
-          }
-        }
-        far |= fabsf(x) > kFarGate<In>;
-        const float up = __expf(x);
-        kh[t * LD + c] = k * up;
-        qh[t * LD + c] = q * up;
-        buf[t * LD + c] = beta * k * __expf(-x);
-      }
+    for (int j = 0; j < CPL; ++j) vt[i][j] = in(a.v, at * D + c0 + j);
   }
-  // values of the wave's columns, of row 16 kb + 4 g + i
-  float vt[4 * NT][CPL];
-#pragma unroll
-  for (int i = 0; i < 4 * NT; ++i) {
-    const int t = 16 * (i >> 2) + 4 * g + (i & 3);
-#pragma unroll
-    for (int j = 0; j < CPL; ++j) {
-      vt[i][j] = good >> t & 1 ? in(a.v, place(t) * D + c0 + j) : 0.f;
-      if (!is_finite(vt[i][j])) {
-        odd[t] = 1;
-        vt[i][j] = 0.f;
-      }
-    }
-  }
-  // ---- the wave's columns of the state, asked for here, behind all else that is asked for: row
-  // 16 kb + 4 g + i
+  __builtin_amdgcn_sched_barrier(0);
   const float* s0 = reinterpret_cast<const float*>(a.pool + pin * a.page_bytes) + (int64_t)h * D * D + c0;
   float st[D / 4][CPL];
 #pragma unroll
@@ -256,6 +211,68 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
         st[4 * kb + i][0] = *p;
       }
     }
+  __builtin_amdgcn_sched_barrier(0);
+
+  const TreeNode tree = tree_node_of(parent);
+  const uint64_t good = __ballot(tree.good());
+  if (tid < 64) {
+    way[tid] = tree.way;
+    odd[tid] = 0;
+  }
+  __syncthreads();
+
+  // ---- gates summed along the ways, as a product with the 0/1 matrix of ways; then the
+  // factors
+  bool far = false;
+#pragma unroll
+  for (int ct = 0; ct < CT; ++ct) {
+    const int c = 16 * (wv + WAVES * ct) + col;
+    f32x4 G[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) G[i] = zero4();
+#pragma unroll
+    for (int ks = 0; ks < 4 * NT; ++ks) {
+      const int s = 4 * ks + g;
+      float x = good >> s & 1 ? gate[ct][ks] : 0.f;
+      if (!(x < __builtin_inff())) {
+        odd[s] = 1;
+        x = 0.f;
+      }
+      x = fmaxf(x, -104.f);
+#pragma unroll
+      for (int i = ks / 4; i < NT; ++i) G[i] = mma1(way[16 * i + col] >> s & 1 ? 1.f : 0.f, x, G[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * i + 4 * g + e;
+        const bool live = good >> t & 1;
+        float k = live ? key[ct][4 * i + e] : 0.f, beta = live ? bt[4 * i + e] : 0.f;
+        const float q = live ? query[ct][4 * i + e] : 0.f, x = live ? G[i][e] : 0.f;
+        if (!is_finite(k) || !is_finite(beta)) {
+          odd[t] = 1;
+          k = beta = 0.f;
+        }
+        far |= fabsf(x) > kFarGate<In>;
+        const float up = __expf(x);
+        kh[t * LD + c] = k * up;
+        qh[t * LD + c] = q * up;
+        buf[t * LD + c] = beta * k * __expf(-x);
+      }
+  }
+#pragma unroll
+  for (int i = 0; i < 4 * NT; ++i) {
+    const int t = 16 * (i >> 2) + 4 * g + (i & 3);
+#pragma unroll
+    for (int j = 0; j < CPL; ++j) {
+      if (!(good >> t & 1)) vt[i][j] = 0.f;
+      if (!is_finite(vt[i][j])) {
+        odd[t] = 1;
+        vt[i][j] = 0.f;
+      }
+    }
+  }
 
   far = __syncthreads_or(far);
 
