@@ -17,8 +17,10 @@
 // asked for itself.
 //
 // Only the device knows the requests' lengths, and a call takes as long as its longest
-// CU: workgroups take the requests longest first, by groups of 64 requests, and where all
-// fit the card at once, the CU with the longest gets the shortest beside it.
+// CU: workgroups take the requests longest first, by groups of 64 requests, and where two
+// fit a CU and all the card at once, the CU with the longest gets the shortest beside it.
+// (One a CU, shortest last: 24 requests of 61 nodes and up to 6000 tokens, 384 tiles: 144
+// us; shortest first: 152.)
 #include "kda_attn_rows.h"
 
 namespace kda {
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(64 * GR * GT) void attn_tree_kernel(AttnArgs a) {
   const int each = a.c.H * a.b.units_per, total = a.b.n * each;
   int b = blockIdx.x / a.splits;
   const int sp = blockIdx.x % a.splits;
-  if (a.splits == 1 && b >= kCUs && total <= 2 * kCUs) b = total - 1 - (b - kCUs);
+  if (GR == 2 && a.splits == 1 && b >= kCUs && total <= 2 * kCUs) b = total - 1 - (b - kCUs);
   const int place_r = b / each, groups = (a.b.n + 63) / 64;
   const int req = uni(a.b.n == 1 ? 0 : kth_longest(a, place_r % groups, groups, place_r / groups));
   const int h = b % each / a.b.units_per, row0 = b % a.b.units_per * ROWS;
