@@ -173,6 +173,27 @@ def test_copies_past_4_gib_and_many():
         assert torch.equal(a, buf[pages - 700:, h * used: h * used + body].flip(0))
 
 
+@pytest.mark.parametrize("n,every", [(1, 1), (1500, 3), (9000, 29), (70001, 90), (12000, 13000)])
+def test_copies_of_a_list_with_gaps(n, every):
+    """Pairs spread over lists of one gathering and of many; the last entry of a list is one of them."""
+    H, d, pt, pages = 1, 64, 64, 1700
+    page = 256 + K.kda_kv_head_bytes(d, pt, K.KDA_INT8)
+    buf = torch.randint(0, 255, (pages, page), dtype=torch.uint8, device="cuda")
+    pool = K.make_kv_pool(buf, page, pages, H, d, pt, K.KDA_INT8)
+    rng = np.random.default_rng(n)
+    src, dst, tokens = np.full(n, -1), rng.integers(-5, pages + 5, n), rng.integers(-3, pt + 70, n)
+    at = np.arange(n - 1, -1, -every)
+    order = rng.permutation(pages)
+    src[at], dst[at] = order[rng.integers(0, 800, len(at))], order[800: 800 + len(at)]
+    want, part = buf.clone(), 2 * 32 * d
+    for i in at:
+        blocks = max(0, min(pt // 32, -(-int(tokens[i]) // 32)))
+        for lo, size in ((0, part), (pt // 32 * part, 8)):
+            want[dst[i], lo: lo + blocks * size] = buf[src[i], lo: lo + blocks * size]
+    K.kda_kv_copy_pages(pool, ints(src), ints(dst), tokens=ints(tokens))
+    assert torch.equal(buf, want)
+
+
 @pytest.mark.parametrize("cache", ["int8", "bf16"])
 def test_samples_forked_from_a_running_request(cache):
     """Fork, copy, reserve, append: the samples hold the source's tokens and their own, the source what it held."""

@@ -146,6 +146,25 @@ def test_split_caches(cache, tokens, hq):
         check_rows(got, x, r, "bf16", 0, 0, (cache, tokens))
 
 
+@pytest.mark.parametrize("cache,dtype", [("int8", "bf16"), ("bf16", "bf16"), ("int8", "f32")])
+@pytest.mark.parametrize("n,tokens,hq", [(65, 17, 2), (131, 9, 4), (150, 34, 2), (70, 12, 16)])
+def test_many_requests_longest_first(cache, dtype, n, tokens, hq):
+    """More requests than a wave orders at once, most of them alike in length, some without part."""
+    rng = np.random.default_rng(n)
+    lens = [int(x) for x in rng.choice([0, 1, 31, 32, 40, 200], n)]
+    d = Draft(lens, [tree(("random", "comb", "roots", "holes")[i % 4], tokens, i) for i in range(n)], 1, hq, 64, 64, cache, dtype,
+              seed=n)
+    out = [i for i in range(n) if i % 11 == 5]
+    d.append()
+    d.pos[torch.tensor(out, device="cuda")] = -1
+    o = d.attend("f32")
+    for r in range(n):
+        if r in out:
+            assert (host(o)[r * tokens: (r + 1) * tokens] == 0).all()
+        else:
+            check_rows(o, d, r, "f32", 0, 0, (cache, n))
+
+
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("tokens,hq", [(5, 2), (24, 8)])
 def test_other_branches_do_not_reach_a_row(bad, tokens, hq):
