@@ -267,7 +267,9 @@ __global__ __launch_bounds__(256) void conv_update_kernel(ConvUpdateArgs a) {
 // nodes before it on its way, then the window's (page_in[r]).  A workgroup takes 64 channel
 // groups of 16 bytes of a request, with a wave for every 16 nodes: each row is asked for
 // once, before the tree is known, and goes to LDS, where a node finds its taps by number.
-// Same taps and summation order as conv_kernel.  Bound by the bytes of x and y.
+// Same taps and summation order as conv_kernel.  Bound by memory and the way to the first
+// row: 64 trees of 16 nodes, 12288 channels, bf16, take 15 us (54 MB, 3.6 TB/s); with rows
+// looked up in memory, four for a node, 24.5.
 constexpr int kConvTreeNodes = 16;  // of a wave
 
 template <typename In, int W, int WAVES>

@@ -378,8 +378,8 @@ __global__ __launch_bounds__(kScan) void pages_compact_kernel(PagesArgs a) {
 // takes a piece of 16 KB of a head's blocks.  A list may be long and mostly empty (a
 // compaction's has an entry for every page of the pool): then a workgroup gathers the pairs
 // to copy from 1024 entries at a time, the next 1024 on their way meanwhile, and takes its
-// piece of them in turn.  Bound by memory: 32 MB copied take 19 us in pages, 14 us in one
-// piece.
+// piece of them in turn.  Bound by memory: 38 MB of 64 tail pages take 19 us (4.0 TB/s both
+// ways); a library copy of 32 MB in one piece takes 14.
 constexpr int kCopyPiece = 16384, kCopyList = 1024;
 __device__ __forceinline__ bool is_copy(const CopyPagesArgs& a, int src, int dst) {
   return src >= 0 && src < a.num_pages && dst >= 0 && dst < a.num_pages && src != dst;

@@ -10,7 +10,12 @@
 //     W = Q (I + A)^-1,    O = (Qhat - W Khat) S0 + W V.
 // So the entering state is read once, for up to 64 nodes, and nothing but O is written;
 // all products run on matrix instructions, and everything before the last line is done
-// while the state is on its way to the registers.
+// while the state is on its way to the registers.  A workgroup takes a head of a request.
+//
+// Small trees are bound by memory: 64 trees of 16 nodes, 32 heads of 128, bf16, take 35 us
+// (177 MB, 5.0 TB/s).  Large ones by the chain of steps in a workgroup, of which 126 KB of
+// LDS let a CU hold one: 24 trees of 63 nodes take 62 us (112 MB).  One tree of 5 nodes, 8
+// heads of 64, fp32, takes 7.2 us.
 //
 // exp(G_t - G_s) is the product of exp(G_t) and exp(-G_s) where no |G| passes kFarGate;
 // else the sums A and Q are taken pair by pair.  A gate below -104 counts as -104, whose
@@ -822,6 +827,7 @@ template <int D> struct CommitShape {
 // The state after the accepted path of each request: the entering one read once, the
 // path's tokens applied in the decode step's arithmetic (and to its bits), the last one
 // written once.  A workgroup per (request, head), the thread layout of the decode step.
+// Bound by memory: 64 requests of 32 heads of 128 take 50 us (270 MB, 5.4 TB/s).
 template <int D, typename In>
 __global__ __launch_bounds__((CommitShape<D>::NT), 4) void state_commit_kernel(StateCommitArgs a) {
   using SH = CommitShape<D>;
