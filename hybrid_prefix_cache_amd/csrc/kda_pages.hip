@@ -176,13 +176,14 @@ __global__ __launch_bounds__(kScan) void pages_reserve_kernel(PagesArgs a) {
   reserve_take(a, own_waves());
 }
 
-// free: an entry whose tokens all lie in [first, last) lets go of its page.
+// free: an entry whose tokens all lie in [first, last) lets go of its page (a wave a row).
 __global__ __launch_bounds__(256) void pages_free_kernel(PagesArgs a) {
-  const int row = blockIdx.x;
+  const int row = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (row >= a.rows) return;
   const int64_t lo = max(a.first[row], 0), hi = a.last[row], pt = a.page_tokens;
   const int begin = (int)min((lo + pt - 1) / pt, (int64_t)a.max_pages), end = (int)min(max(hi, (int64_t)0) / pt, (int64_t)a.max_pages);
   int32_t* t = a.table + (int64_t)row * a.max_pages;
-  for (int j = begin + threadIdx.x; j < end; j += 256) {
+  for (int j = begin + (threadIdx.x & 63); j < end; j += 64) {
     const int page = t[j];
     if (page < 0) continue;
     t[j] = -1;
@@ -493,7 +494,7 @@ hipError_t launch_pages_reserve(const PagesArgs& a, hipStream_t st) {
   return hipGetLastError();
 }
 hipError_t launch_pages_free(const PagesArgs& a, hipStream_t st) {
-  hipLaunchKernelGGL(pages_free_kernel, dim3((unsigned)a.rows), dim3(256), 0, st, a);
+  hipLaunchKernelGGL(pages_free_kernel, over(a.rows, 4), dim3(256), 0, st, a);
   return hipGetLastError();
 }
 hipError_t launch_pages_fork(const PagesArgs& a, hipStream_t st) {

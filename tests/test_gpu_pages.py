@@ -106,6 +106,29 @@ def test_reserve_free_fork_compact(pages, rows, width, pt, seed):
         b.compact()
 
 
+def test_as_many_rows_as_a_map_may_have():
+    rows, pages = 1 << 24, 1000
+    refs, table = torch.zeros(pages, dtype=torch.int32, device="cuda"), torch.full((rows, 1), -1, dtype=torch.int32, device="cuda")
+    m = K.make_page_map(refs, table, 1)
+    work = torch.empty(K.kda_pages_workspace_bytes(m), dtype=torch.uint8, device="cuda")
+    first, last, status = (torch.zeros(rows, dtype=torch.int32, device="cuda") for _ in range(3))
+    some = torch.arange(5, rows, 17000, device="cuda")  # 987 rows
+    last[some] = 1
+    K.kda_pages_reserve(m, first, last, status, workspace=work)
+    assert torch.equal(table[some, 0], torch.arange(len(some), dtype=torch.int32, device="cuda")) and not status.any()
+    assert int((table >= 0).sum()) == len(some) == int(refs.sum())
+    last[some[: len(some) // 2]] = 0
+    K.kda_pages_free(m, first, last)
+    kept = some[: len(some) // 2]
+    assert int((table >= 0).sum()) == len(kept) == int(refs.sum()) and (table[kept, 0] >= 0).all()
+    copies = torch.empty((2, pages), dtype=torch.int32, device="cuda")
+    last.fill_(2)
+    K.kda_pages_free(m, first, torch.where(torch.arange(rows, device="cuda") == kept[0], last, 0).int())
+    K.kda_pages_compact(m, copies[0], copies[1], workspace=work)
+    assert copies[:, 0].tolist() == [len(kept) - 1, 0] and (copies[:, 1:] == -1).all()
+    assert table[kept[-1]].item() == 0 and int(refs.sum()) == len(kept) - 1
+
+
 def test_reserve_when_pages_run_out():
     b = Book([0, 1, 0, 2, 0], [[1, -1, -1, -1], [-1, 3, -1, -1], [3, -1, -1, -1]], 8)
     b.reserve([0, 4, 8], [24, 9, 33])  # two, one, and three of which none is left
