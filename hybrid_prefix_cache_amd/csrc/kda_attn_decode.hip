@@ -98,6 +98,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   const int req = item / a.c.H, h = item % a.c.H;
   const int M = a.b.tokens * a.G;
   const int64_t p0 = a.b.pos[req], p1 = p0 + a.b.tokens - 1;
+  const int parent = TREE && lane < a.b.tokens ? a.parent[(int64_t)req * a.b.tokens + lane] : -2;
   const bool off = p0 < 0, over = p1 >= (int64_t)a.c.max_pages * a.c.page_tokens;
   if (off || over) {
     if (sp == 0)
@@ -114,13 +115,37 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
   const Whole whole = whole_of(TREE ? p0 - 1 : p0, p1, a.window, a.sinks);
   const Chunk ch = chunk_of(reach.count(), a.splits, a.min_blocks, sp);
   if (ch.begin >= ch.end) return;
+  // ---- this wave's blocks: tiles first, first + 4, ...; lane i looks up the page of the i-th of each 64
+  const int first = ch.begin + wv, count = first < ch.end ? (ch.end - first + 3) / 4 : 0;
+  const uint8_t* head0 = a.c.base + h * a.c.head_bytes;
+  const int per = a.c.page_tokens / kKvBlock;
+  int pg = 0, in = 0;
+  auto look_up = [&](int base) {
+    const int t = first + 4 * (base + lane);
+    if (t < ch.end) {
+      const int blk = reach.block(t);
+      const int j = blk / per;
+      in = blk - j * per;
+      pg = a.c.table[(int64_t)req * a.c.max_pages + j];
+      if (pg < 0 || pg >= a.c.num_pages) pg = -1;
+    }
+  };
+  TileRegs<D, EB> cur, nxt;
+  int cur_pg = 0, nxt_pg = 0;
+  auto fetch = [&](int i, TileRegs<D, EB>& t, int& page) {
+    page = __builtin_amdgcn_readlane(pg, i & 63);
+    const int inner = __builtin_amdgcn_readlane(in, i & 63);
+    load_tile<D, EB>(a.c, head0, max(page, 0), inner, lane, t);  // a bad page: page 0's bytes, never used
+  };
   TreeNode tree;
   uint64_t sight = 0, nodes = 0, bad = 0, see_way[MT];  // of the lane's entry; of all; of the lane's rows
-  if constexpr (TREE) {
-    tree = tree_node(a.parent + (int64_t)req * a.b.tokens, a.b.tokens);
+  if constexpr (TREE) {  // while the first block's page, then the block, are on their way
+    if (count > 0) look_up(0);
+    tree = tree_node_of(parent);
     sight = tree_sight(tree, p0, a.b.tokens, a.window, a.sinks);
     nodes = __ballot(tree.node);
     bad = __ballot(tree.bad);
+    if (count > 0) fetch(0, cur, cur_pg);
   }
 
   // ---- queries: lane (g, col) holds row col's channels of k-group g
@@ -182,29 +207,7 @@ __global__ __launch_bounds__(256) void attn_decode_kernel(AttnArgs a) {
     for (int dt = 0; dt < DT; ++dt) acc[mt][dt] = zero4();
   }
 
-  // ---- this wave's blocks: tiles first, first + 4, ...; lane i looks up the page of the i-th of each 64
-  const int first = ch.begin + wv, count = first < ch.end ? (ch.end - first + 3) / 4 : 0;
-  const uint8_t* head0 = a.c.base + h * a.c.head_bytes;
-  const int per = a.c.page_tokens / kKvBlock;
-  int pg = 0, in = 0;
-  auto look_up = [&](int base) {
-    const int t = first + 4 * (base + lane);
-    if (t < ch.end) {
-      const int blk = reach.block(t);
-      const int j = blk / per;
-      in = blk - j * per;
-      pg = a.c.table[(int64_t)req * a.c.max_pages + j];
-      if (pg < 0 || pg >= a.c.num_pages) pg = -1;
-    }
-  };
-  TileRegs<D, EB> cur, nxt;
-  int cur_pg = 0, nxt_pg = 0;
-  auto fetch = [&](int i, TileRegs<D, EB>& t, int& page) {
-    page = __builtin_amdgcn_readlane(pg, i & 63);
-    const int inner = __builtin_amdgcn_readlane(in, i & 63);
-    load_tile<D, EB>(a.c, head0, max(page, 0), inner, lane, t);  // a bad page: page 0's bytes, never used
-  };
-  if (count > 0) {
+  if (!TREE && count > 0) {
     look_up(0);
     fetch(0, cur, cur_pg);
   }
