@@ -408,17 +408,15 @@ __device__ __forceinline__ void copy_piece(const CopyPagesArgs& a, int64_t whole
     for (int b = tid; b < blocks && a.scale_bytes; b += 256)
       *reinterpret_cast<u32x2_t*>(to + whole + 8 * b) = *reinterpret_cast<const u32x2_t*>(from + whole + 8 * b);
 }
-// The workgroups of an XCD (every eighth) take units that follow each other, so that a page
-// is copied, and its addresses translated, by one or two of them (64 tail pages of 1 MB, half
-// full: 21 -> 19 us).
-__device__ __forceinline__ int copy_unit() {
-  const int all = gridDim.x, x = blockIdx.x % 8;
-  return x * (all / 8) + min(x, all % 8) + blockIdx.x / 8;
-}
+// Eight entries at a time, one for each XCD (whose workgroups are every eighth): a page is
+// copied, and its addresses translated, by one of them (64 tail pages of 1 MB, half full: 21
+// -> 19 us).
 __global__ __launch_bounds__(256, 8) void kv_copy_pages_kernel(CopyPagesArgs a) {
   const int64_t whole = (int64_t)a.block_bytes * a.blocks;
-  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece), unit = copy_unit(), i = unit / (pieces * a.heads);
-  const int rest = unit % (pieces * a.heads), h = rest / pieces, piece = rest % pieces;
+  const int pieces = (int)((whole + kCopyPiece - 1) / kCopyPiece), per = pieces * a.heads, x = a.n < 64 ? 1 : 8;
+  const int unit = blockIdx.x / x, i = unit / per * x + blockIdx.x % x;
+  if (i >= a.n) return;
+  const int rest = unit % per, h = rest / pieces, piece = rest % pieces;
   const int src = a.src[i], dst = a.dst[i], tokens = a.tokens ? a.tokens[i] : 0;
   if (is_copy(a, src, dst)) copy_piece(a, whole, h, piece, src, dst, copy_blocks(a, tokens));
 }
@@ -524,10 +522,11 @@ hipError_t launch_pages_compact(const PagesArgs& a, hipStream_t st) {
 }
 hipError_t launch_kv_copy_pages(const CopyPagesArgs& a, hipStream_t st) {
   const int64_t pieces = ((int64_t)a.block_bytes * a.blocks + kCopyPiece - 1) / kCopyPiece * a.heads;
-  // A workgroup for each piece of each entry, up to four times as many as the CUs hold; past
-  // that most of them would find nothing to copy.
-  const bool each = a.n * pieces <= 8192;
-  const dim3 grid((unsigned)(pieces * (each ? a.n : pieces < 2048 ? 2048 / pieces : 1)));
+  // A workgroup for each piece of each entry, or the list gathered (pages of 128 KB, a tenth
+  // of the entries pairs; us): 8000 pieces 7.0, 7.8; 16000 11.3, 14.1; 32000 25.4, 26.5; 64000
+  // 58.6, 54.8.  With no pairs 5.2, 5.2; 8.7, 6.9; 15.9, 10.3; 30, 18.
+  const bool each = a.n * pieces <= 32768;
+  const dim3 grid((unsigned)(pieces * (each ? (a.n < 64 ? a.n : (a.n + 7) / 8 * 8) : pieces < 2048 ? 2048 / pieces : 1)));
   if (each) hipLaunchKernelGGL(kv_copy_pages_kernel, grid, dim3(256), 0, st, a);
   else hipLaunchKernelGGL(kv_copy_list_kernel, grid, dim3(256), 0, st, a);
   return hipGetLastError();
