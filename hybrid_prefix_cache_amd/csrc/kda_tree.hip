@@ -13,9 +13,9 @@
 // while the state is on its way to the registers.  A workgroup takes a head of a request.
 //
 // Small trees are bound by memory: 64 trees of 16 nodes, 32 heads of 128, bf16, take 35 us
-// (177 MB, 5.0 TB/s).  Large ones by the chain of steps in a workgroup, of which 126 KB of
-// LDS let a CU hold one: 24 trees of 63 nodes take 62 us (112 MB).  One tree of 5 nodes, 8
-// heads of 64, fp32, takes 7.2 us.
+// (177 MB, 5.0 TB/s).  Large ones by the chain of steps in a workgroup, of which a CU holds
+// two: 24 trees of 63 nodes take 48 us (112 MB).  One tree of 5 nodes, 8 heads of 64, fp32,
+// takes 7.2 us.
 //
 // exp(G_t - G_s) is the product of exp(G_t) and exp(-G_s) where no |G| passes kFarGate;
 // else the sums A and Q are taken pair by pair.  A gate below -104 counts as -104, whose
@@ -401,9 +401,17 @@ template <int D, int NT> struct TreeShape16 {
   static constexpr int LN = N + 4;               // of rows of nodes (fp32)
   static constexpr int ROWS = 2 * N * LC;        // two parts by rows
   static constexpr int COLS = 2 * D * LS;        // by columns
-  static constexpr int KB = ROWS > COLS ? ROWS : COLS;            // Khat by rows, then by columns
-  static constexpr int XB = ROWS > 4 * N * LN ? ROWS : 4 * N * LN;  // beta k exp(-G), then A and W (fp32)
-  static constexpr int GB = D * LS > 2 * N * LS ? D * LS : 2 * N * LS;  // gates by columns, then W
+  // THIN: Khat's place is the gates' before and Qhat's between and after, and W's parts take
+  // A's place, so that a CU holds two workgroups, of 74 KB, instead of one of 126; four more
+  // barriers, and the state is asked for where registers are free (24 trees of 63 nodes: 62 ->
+  // 48 us).
+  static constexpr bool THIN = D == 128 && NT > 2;
+  static constexpr int KB = ROWS > COLS ? ROWS : COLS;  // Khat by rows, then by columns
+  static constexpr int PARTS = 2 * N * LS;              // of W
+  static constexpr int AM = THIN && PARTS > 2 * N * LN ? PARTS : 2 * N * LN;        // A (fp32)
+  static constexpr int XB = ROWS > AM + 2 * N * LN ? ROWS : AM + 2 * N * LN;        // beta k exp(-G), then A and W (fp32)
+  static constexpr int GB = THIN ? 8 : D * LS > PARTS ? D * LS : PARTS;             // gates by columns, then W
+  static constexpr int QB = THIN ? 8 : ROWS;
 };
 
 struct Parts {
@@ -435,15 +443,19 @@ __device__ __forceinline__ void put_parts(uint16_t* hi, uint16_t* lo, const f32x
 }
 
 template <int D, int NT>
-__global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kernel(TreeArgs a) {
+__global__ __launch_bounds__((TreeShape16<D, NT>::THREADS), (TreeShape16<D, NT>::THIN ? 4 : 1)) void tree_bf16_kernel(TreeArgs a) {
   using SH = TreeShape16<D, NT>;
   constexpr int N = SH::N, LC = SH::LC, LS = SH::LS, LN = SH::LN, CPL = SH::CPL, CT = SH::CT, WAVES = SH::WAVES;
   constexpr int KD = D / 32, KN = (N + 31) / 32;  // matrix steps over channels, over nodes
-  __shared__ __align__(16) uint16_t kb[SH::KB], qb[SH::ROWS], xb[SH::XB], gb[SH::GB];
+  constexpr bool THIN = SH::THIN;
+  __shared__ __align__(16) uint16_t kb[SH::KB], qb_[SH::QB], xb[SH::XB], gb_[SH::GB];
   __shared__ uint64_t way[64];
   __shared__ int odd[64];  // a node has a value that is not finite
   float* const am = reinterpret_cast<float*>(xb);
-  float* const wm = am + N * LN;
+  float* const wm = reinterpret_cast<float*>(xb + SH::AM);
+  uint16_t* const qb = THIN ? kb : qb_;      // Qhat, then Qhat - W Khat
+  uint16_t* const gates = THIN ? kb : gb_;
+  uint16_t* const wp = THIN ? xb : gb_;      // W's parts
   const int tid = threadIdx.x, lane = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int g = lane >> 4, col = lane & 15;
   const int r = blockIdx.x / a.H, h = blockIdx.x % a.H, T = a.tokens;
@@ -467,8 +479,8 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
   const uint16_t* const gbeta = reinterpret_cast<const uint16_t*>(a.beta) + row0 * a.H + h;
   const uint32_t HD = a.H * D;
 
-  // ---- everything a wave needs is asked for here, the state last: what is asked for is
-  // answered in order, and the state is needed last
+  // ---- everything a wave needs is asked for here (THIN: but the state), the state last: what
+  // is asked for is answered in order, and the state is needed last
   const int c0 = CPL * (16 * wv + col);
   const int parent = lane < T ? a.parent[row0 + lane] : -2;
   constexpr int GU = (N * 2 + 63) / 64;  // 16-byte units of a column tile's gates a lane brings: node u / 2
@@ -502,19 +514,22 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
   __builtin_amdgcn_sched_barrier(0);
   const float* s0 = reinterpret_cast<const float*>(a.pool + pin * a.page_bytes) + (int64_t)h * D * D + c0;
   float st[KD][8][CPL];  // rows 32 k + 8 g + i
+  auto ask_state = [&] {
 #pragma unroll
-  for (int k = 0; k < KD; ++k)
+    for (int k = 0; k < KD; ++k)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float* p = s0 + (32 * k + 8 * g + i) * D;
-      if constexpr (CPL == 2) {
-        const float2 x = *reinterpret_cast<const float2*>(p);
-        st[k][i][0] = x.x;
-        st[k][i][1] = x.y;
-      } else {
-        st[k][i][0] = *p;
+      for (int i = 0; i < 8; ++i) {
+        const float* p = s0 + (32 * k + 8 * g + i) * D;
+        if constexpr (CPL == 2) {
+          const float2 x = *reinterpret_cast<const float2*>(p);
+          st[k][i][0] = x.x;
+          st[k][i][1] = x.y;
+        } else {
+          st[k][i][0] = *p;
+        }
       }
-    }
+  };
+  if constexpr (!THIN) ask_state();
   __builtin_amdgcn_sched_barrier(0);
 
   const TreeNode tree = tree_node_of(parent);
@@ -549,67 +564,13 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
         for (uint64_t m = __ballot(bad); m; m &= m - 1) odd_gates |= 1ull << ((64 * u + __builtin_ctzll(m)) >> 1);
       }
       if (s < N) {
-        uint16_t* to = gb + (16 * (CT * wv + i) + 8 * (lane & 1)) * LS + s;
+        uint16_t* to = gates + (16 * (CT * wv + i) + 8 * (lane & 1)) * LS + s;
 #pragma unroll
         for (int e = 0; e < 8; ++e) to[e * LS] = (uint16_t)(w[e >> 1] >> (16 * (e & 1)));
       }
     }
   __syncthreads();
   if (odd_gates >> lane & 1) odd[lane] = 1;
-  // ---- gates summed along the ways, as a product with the 0/1 matrix of ways; the factors
-  bool far = false;
-  f32x4 khat[CT][NT], qhat[CT][NT];
-#pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    const int node = 16 * t + col;
-    const uint64_t w = way[node];
-    bf16x8 on[KN];
-#pragma unroll
-    for (int k = 0; k < KN; ++k) {
-      const uint32_t bits = (uint32_t)(w >> (32 * k + 8 * g)) & 255u;
-      u32x4_t x;  // 0x3f80 is 1
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x[e] = (bits >> (2 * e) & 1) * 0x3f80u | (bits >> (2 * e + 1) & 1) * 0x3f800000u;
-      on[k] = __builtin_bit_cast(bf16x8, x);
-    }
-    const bool live = good >> node & 1;
-    float beta = live ? bf16_to_f32(braw[t]) : 0.f;
-    const bool odd_beta = !is_finite(beta);
-    if (odd_beta) beta = 0.f;
-#pragma unroll
-    for (int i = 0; i < CT; ++i) {
-      const int c = 16 * (CT * wv + i);
-      f32x4 G = zero4();
-#pragma unroll
-      for (int k = 0; k < KN; ++k)
-        if (32 * k <= 16 * t) {
-          const bf16x8 x = 32 * k + 8 * g < N ? lds8(gb + (c + col) * LS + 32 * k + 8 * g) : none8();
-          G = mma8(x, on[k], G);
-        }
-      u32x2_t kw = kraw[i][t], qw = qraw[i][t];
-      if (!live) kw = qw = u32x2_t{0u, 0u};
-      const bool odd_k = (not_finite2(kw[0]) | not_finite2(kw[1])) & 0x80008000u;
-      if (odd_k || odd_beta) {
-        odd[node] = 1;
-        kw = u32x2_t{0u, 0u};
-      }
-      const f32x4 k = {low_of(kw[0]), high_of(kw[0]), low_of(kw[1]), high_of(kw[1])};
-      const f32x4 q = {low_of(qw[0]), high_of(qw[0]), low_of(qw[1]), high_of(qw[1])};
-      f32x4 x;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {  // of an entry that is no node G is 0, as its gates and its way are
-        far |= fabsf(G[e]) > kFarGate<uint16_t>;
-        const float y = G[e] * 1.44269504f, up = __builtin_amdgcn_exp2f(y);
-        khat[i][t][e] = k[e] * up;
-        qhat[i][t][e] = q[e] * up;
-        x[e] = beta * k[e] * __builtin_amdgcn_exp2f(-y);
-      }
-      const int to = node * LC + c + 4 * g;
-      put_parts(kb + to, kb + N * LC + to, khat[i][t]);
-      put_parts(qb + to, qb + N * LC + to, qhat[i][t]);
-      put_parts(xb + to, xb + N * LC + to, x);
-    }
-  }
   // values of the wave's columns as an operand: nodes 32 k + 8 g + i
   bf16x8 vf[KN][CPL];
 #pragma unroll
@@ -638,35 +599,109 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
       vf[k][j] = __builtin_bit_cast(bf16x8, x);
     }
   }
+  // ---- gates summed along the ways, as a product with the 0/1 matrix of ways ...
+  bool far = false;
+  f32x4 khat[CT][NT], qhat[CT][NT], G[CT][NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const uint64_t w = way[16 * t + col];
+    bf16x8 on[KN];
+#pragma unroll
+    for (int k = 0; k < KN; ++k) {
+      const uint32_t bits = (uint32_t)(w >> (32 * k + 8 * g)) & 255u;
+      u32x4_t x;  // 0x3f80 is 1
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = (bits >> (2 * e) & 1) * 0x3f80u | (bits >> (2 * e + 1) & 1) * 0x3f800000u;
+      on[k] = __builtin_bit_cast(bf16x8, x);
+    }
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      G[i][t] = zero4();
+#pragma unroll
+      for (int k = 0; k < KN; ++k)
+        if (32 * k <= 16 * t) {
+          const bf16x8 x = 32 * k + 8 * g < N ? lds8(gates + (16 * (CT * wv + i) + col) * LS + 32 * k + 8 * g) : none8();
+          G[i][t] = mma8(x, on[k], G[i][t]);
+        }
+    }
+  }
+  if constexpr (THIN) __syncthreads();
+  // ... and the factors
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    const int node = 16 * t + col;
+    const bool live = good >> node & 1;
+    float beta = live ? bf16_to_f32(braw[t]) : 0.f;
+    const bool odd_beta = !is_finite(beta);
+    if (odd_beta) beta = 0.f;
+#pragma unroll
+    for (int i = 0; i < CT; ++i) {
+      u32x2_t kw = kraw[i][t], qw = qraw[i][t];
+      if (!live) kw = qw = u32x2_t{0u, 0u};
+      const bool odd_k = (not_finite2(kw[0]) | not_finite2(kw[1])) & 0x80008000u;
+      if (odd_k || odd_beta) {
+        odd[node] = 1;
+        kw = u32x2_t{0u, 0u};
+      }
+      const f32x4 k = {low_of(kw[0]), high_of(kw[0]), low_of(kw[1]), high_of(kw[1])};
+      const f32x4 q = {low_of(qw[0]), high_of(qw[0]), low_of(qw[1]), high_of(qw[1])};
+      f32x4 x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {  // of an entry that is no node G is 0, as its gates and its way are
+        far |= fabsf(G[i][t][e]) > kFarGate<uint16_t>;
+        const float y = G[i][t][e] * 1.44269504f, up = __builtin_amdgcn_exp2f(y);
+        khat[i][t][e] = k[e] * up;
+        qhat[i][t][e] = q[e] * up;
+        x[e] = beta * k[e] * __builtin_amdgcn_exp2f(-y);
+      }
+      const int to = node * LC + 16 * (CT * wv + i) + 4 * g;
+      put_parts(kb + to, kb + N * LC + to, khat[i][t]);
+      if constexpr (!THIN) put_parts(qb + to, qb + N * LC + to, qhat[i][t]);
+      put_parts(xb + to, xb + N * LC + to, x);
+    }
+  }
   far = __syncthreads_or(far);
 
   // ---- A and Q, tile by tile of the lower triangle; in registers until every wave has
   // read what they replace
-  constexpr int UNITS = NT * (NT + 1), MINE = (UNITS + WAVES - 1) / WAVES;  // a tile of A or of Q
-  f32x4 got[MINE];
+  constexpr int TILES = NT * (NT + 1) / 2, UNITS = THIN ? TILES : 2 * TILES, MINE = (UNITS + WAVES - 1) / WAVES;
+  f32x4 got[THIN ? 2 : 1][MINE];  // unit u: of tile u / 2 A, then Q; THIN: of tile u, first all of A, then all of Q
   auto tile_of = [](int u, int* ti, int* tj) {
-    const int tile = u >> 1;
+    const int tile = THIN ? u : u >> 1;
     *ti = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0;
     *tj = tile - *ti * (*ti + 1) / 2;
   };
-  if (!far) {
+#pragma unroll
+  for (int turn = 0; turn < (THIN ? 2 : 1); ++turn) {
+    if (turn) {  // Qhat to Khat's place
+      __syncthreads();
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int i = 0; i < CT; ++i) {
+          const int to = (16 * t + col) * LC + 16 * (CT * wv + i) + 4 * g;
+          put_parts(qb + to, qb + N * LC + to, qhat[i][t]);
+        }
+      __syncthreads();
+    }
+    if (far) continue;
 #pragma unroll
     for (int m = 0; m < MINE; ++m) {
       const int u = m * WAVES + wv;
       if (u >= UNITS) continue;
       int ti, tj;
       tile_of(u, &ti, &tj);
-      const uint16_t* A = (u & 1 ? qb : kb) + (16 * ti + col) * LC + 8 * g;
+      const uint16_t* A = (THIN || !(u & 1) ? kb : qb) + (16 * ti + col) * LC + 8 * g;
       const uint16_t* B = xb + (16 * tj + col) * LC + 8 * g;
       f32x4 x = zero4(), y = zero4(), z = zero4();
-#pragma unroll
+#pragma unroll (THIN ? 2 : KD)
       for (int k = 0; k < KD; ++k) {
         const bf16x8 ah = lds8(A + 32 * k), al = lds8(A + N * LC + 32 * k), bh = lds8(B + 32 * k), bl = lds8(B + N * LC + 32 * k);
         x = mma8(ah, bh, x);
         y = mma8(al, bh, y);
         z = mma8(ah, bl, z);
       }
-      got[m] = x + (y + z);
+      got[turn][m] = x + (y + z);
     }
   }
   __syncthreads();
@@ -685,6 +720,7 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
         kb[D * LS + to] = (uint16_t)lo;
         kb[D * LS + to + LS] = (uint16_t)(lo >> 16);
       }
+  if constexpr (THIN) ask_state();  // Khat's registers are free, and another workgroup is there meanwhile
   if (!far) {
 #pragma unroll
     for (int m = 0; m < MINE; ++m) {
@@ -692,11 +728,15 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
       if (u >= UNITS) continue;
       int ti, tj;
       tile_of(u, &ti, &tj);
-      float* to = u & 1 ? wm : am;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * ti + 4 * g + e, s = 16 * tj + col;
-        to[t * LN + s] = (way[t] >> s & 1) && ((u & 1) || s != t) ? got[m][e] : 0.f;
+      for (int turn = 0; turn < (THIN ? 2 : 1); ++turn) {
+        const bool second = THIN ? turn : u & 1;
+        float* to = second ? wm : am;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int t = 16 * ti + 4 * g + e, s = 16 * tj + col;
+          to[t * LN + s] = (way[t] >> s & 1) && (second || s != t) ? got[turn][m][e] : 0.f;
+        }
       }
     }
   } else {
@@ -706,10 +746,11 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
   invert_diagonal<NT>(am, LN, wv, lane);
   __syncthreads();
   // ---- W = Q (I + A)^-1, and its parts
+  if (wv < NT) solve_row<LN>(am, wm, wv, g, col);
+  if constexpr (THIN) __syncthreads();
   if (wv < NT) {
-    solve_row<LN>(am, wm, wv, g, col);
     const float* w = wm + 16 * wv * LN;
-    uint16_t* to = gb + 16 * wv * LS;
+    uint16_t* to = wp + 16 * wv * LS;
     for (int i = lane; i < 16 * 4 * (wv + 1); i += 64) {
       const int t = i / (4 * (wv + 1)), s = i % (4 * (wv + 1)) * 4;
       put_parts(to + t * LS + s, to + N * LS + t * LS + s, lds4(w + t * LN + s));
@@ -724,7 +765,7 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
 #pragma unroll
     for (int k = 0; k < KN; ++k) {
       const bool on = 32 * k + 8 * g < 16 * (t + 1);
-      const uint16_t* p = gb + (16 * t + col) * LS + 32 * k + 8 * g;
+      const uint16_t* p = wp + (16 * t + col) * LS + 32 * k + 8 * g;
       wh[k] = on ? lds8(p) : none8();
       wl[k] = on ? lds8(p + N * LS) : none8();
     }
@@ -742,9 +783,20 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
           x = mma8(kl, wh[k], x);
           x = mma8(kh, wl[k], x);
         }
+      qhat[i][t] = qhat[i][t] - x;
       const int to = (16 * t + col) * LC + c + 4 * g;
-      put_parts(qb + to, qb + N * LC + to, qhat[i][t] - x);
+      if constexpr (!THIN) put_parts(qb + to, qb + N * LC + to, qhat[i][t]);
     }
+  }
+  if constexpr (THIN) {
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t)
+#pragma unroll
+      for (int i = 0; i < CT; ++i) {
+        const int to = (16 * t + col) * LC + 16 * (CT * wv + i) + 4 * g;
+        put_parts(qb + to, qb + N * LC + to, qhat[i][t]);
+      }
   }
   __syncthreads();
 
@@ -774,7 +826,7 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS)) void tree_bf16_kerne
     for (int k = 0; k < KN; ++k)
       if (32 * k <= 16 * t) {
         const bool on = 32 * k + 8 * g < 16 * (t + 1);
-        const uint16_t* p = gb + (16 * t + col) * LS + 32 * k + 8 * g;
+        const uint16_t* p = wp + (16 * t + col) * LS + 32 * k + 8 * g;
         const bf16x8 wh = on ? lds8(p) : none8(), wl = on ? lds8(p + N * LS) : none8();
 #pragma unroll
         for (int j = 0; j < CPL; ++j) {
