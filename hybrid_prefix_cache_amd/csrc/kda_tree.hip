@@ -404,7 +404,7 @@ template <int D, int NT> struct TreeShape16 {
   // THIN: Khat's place is the gates' before and Qhat's between and after, and W's parts take
   // A's place, so that a CU holds two workgroups, of 74 KB, instead of one of 126; four more
   // barriers, and the state is asked for where registers are free (24 trees of 63 nodes: 62 ->
-  // 48 us).
+  // 48 us).  Up to 32 nodes it gains nothing (48 trees of 32, with the commit: 97 us, 95 without).
   static constexpr bool THIN = D == 128 && NT > 2;
   static constexpr int KB = ROWS > COLS ? ROWS : COLS;  // Khat by rows, then by columns
   static constexpr int PARTS = 2 * N * LS;              // of W
