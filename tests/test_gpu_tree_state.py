@@ -130,6 +130,30 @@ def test_values_that_are_not_finite_are_their_descendants_alone(name, bad, token
     assert torch.equal(got[tokens:], clean[tokens:])
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 128), ("bf16", 64)])
+@pytest.mark.parametrize("tokens", [16, 20, 48, 64])
+@pytest.mark.parametrize("gate", [0.05, 40.0])
+def test_values_that_are_not_finite_beside_gates_that_forget(dtype, d, tokens, gate):
+    """The same where A and Q are summed pair by pair, in every size of the kernels, in a tree with holes."""
+    row = tree("holes", tokens, 2)
+    ways = T.ways(row)
+    x = States([row, tree("comb", tokens)], 2, d, dtype, seed=tokens, gate=gate)
+    clean = x.run("f32")
+    nodes = [t for t, way in enumerate(ways) if way]
+    spoilt = nodes[1::5]
+    for i, t in enumerate(spoilt):
+        y = x.x[("k", "v", "beta")[i % 3]]
+        (y[t, 1:] if y.dim() == 2 else y[t, 1:, 3 * i % d]).fill_((float("nan"), float("inf"), -float("inf"))[i // 3 % 3])
+    got = x.run("f32")
+    assert torch.equal(got[:, 0].nan_to_num(7.0), clean[:, 0].nan_to_num(7.0))
+    for t, way in enumerate(ways):
+        if way and set(way) & set(spoilt):
+            assert torch.isnan(got[t, 1]).all(), t
+        else:
+            assert torch.equal(got[t, 1].nan_to_num(7.0), clean[t, 1].nan_to_num(7.0)), t
+    assert torch.equal(got[tokens:], clean[tokens:])
+
+
 def test_rows_of_no_node_are_not_read():
     row = tree("holes", 20, 3)
     x = States([row], 2, 64, "f32", seed=6)
