@@ -17,8 +17,8 @@
 // two: 24 trees of 63 nodes take 48 us (112 MB).  One tree of 5 nodes, 8 heads of 64, fp32,
 // takes 7.2 us.
 //
-// exp(G_t - G_s) is the product of exp(G_t) and exp(-G_s) where no |G| passes kFarGate;
-// else the sums A and Q are taken pair by pair.  A gate below -104 counts as -104, whose
+// exp(G_t - G_s) is the product of exp(G_t) and exp(-G_s) where no |G| passes kFarGate (and
+// no beta k exp(-G) fp32's range); else the sums A and Q are taken pair by pair.  A gate below -104 counts as -104, whose
 // exponential is 0 in fp32 too.
 #include "kda_device.h"
 #include "kda_launch.h"
@@ -49,14 +49,21 @@ __device__ __forceinline__ f32x4 mma1(float a, float b, f32x4 c) { return __buil
 
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) < __builtin_inff(); }
 
+// What other nodes' zeros are multiplied with has to be finite: x, or 0 where it is not (finite
+// inputs may pass fp32's range too), and its node's mark.
+__device__ __forceinline__ float kept(float x, int* odd) {
+  if (is_finite(x)) return x;
+  *odd = 1;
+  return 0.f;
+}
+
 // A and Q pair by pair, up the way of each of the wave's nodes, the gates between summed as
-// it goes; a lane takes channels lane, lane + 64.  Rare, and slow: 64 nodes in a chain take
+// it goes, but for nodes behind a spoilt one; a lane takes channels lane, lane + 64.  Rare, and slow: 64 nodes in a chain take
 // 64 * 65 / 2 such steps.
 template <int D, typename In>
-__device__ __forceinline__ void tree_pairs(const TreeArgs& a, const uint64_t* way, const int* odd, uint64_t good, int64_t row0,
-                                           int h, int N, int LN, int waves, float* am, float* wm) {
+__device__ __forceinline__ void tree_pairs(const TreeArgs& a, const uint64_t* way, int* odd, uint64_t spoilt, uint64_t good,
+                                           int64_t row0, int h, int N, int LN, int waves, float* am, float* wm) {
   const int lane = threadIdx.x & 63;
-  const uint64_t spoilt = __ballot(odd[lane] != 0);
   auto in = [&](const void* p, int64_t at) { return load_as_f(reinterpret_cast<const In*>(p) + at); };
   auto place = [&](int t) { return (row0 + t) * a.H + h; };
   for (int t = threadIdx.x >> 6; t < N; t += waves) {
@@ -86,7 +93,7 @@ __device__ __forceinline__ void tree_pairs(const TreeArgs& a, const uint64_t* wa
       }
       const float beta = in(a.beta, place(s));
       if (lane == 0) {
-        if (s != t) am[t * LN + s] = beta * sa;
+        if (s != t) am[t * LN + s] = kept(beta * sa, odd + t);
         wm[t * LN + s] = beta * sq;
       }
     }
@@ -94,7 +101,7 @@ __device__ __forceinline__ void tree_pairs(const TreeArgs& a, const uint64_t* wa
 }
 
 // The diagonal tiles of I + A, inverted in place: lane c of a wave takes column c.
-template <int NT> __device__ __forceinline__ void invert_diagonal(float* am, int LN, int wv, int lane) {
+template <int NT> __device__ __forceinline__ void invert_diagonal(float* am, int LN, int* odd, int wv, int lane) {
   if (wv >= NT || lane >= 16) return;
   float* d = am + 16 * wv * LN + 16 * wv;
   float x[16];
@@ -106,7 +113,7 @@ template <int NT> __device__ __forceinline__ void invert_diagonal(float* am, int
     float y = i == lane ? 1.f : 0.f;
 #pragma unroll
     for (int j = 0; j < i; ++j) y = __builtin_fmaf(-row[j >> 2][j & 3], x[j], y);
-    x[i] = y;  // 0 above the diagonal
+    x[i] = kept(y, odd + 16 * wv + i);  // 0 above the diagonal
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) d[i * LN + lane] = x[i];
@@ -261,9 +268,11 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
         }
         far |= fabsf(x) > kFarGate<In>;
         const float up = __expf(x);
-        kh[t * LD + c] = k * up;
+        const float down = beta * k * __expf(-x);
+        far |= !is_finite(down);
+        kh[t * LD + c] = kept(k * up, odd + t);
         qh[t * LD + c] = q * up;
-        buf[t * LD + c] = beta * k * __expf(-x);
+        buf[t * LD + c] = down;
       }
   }
 #pragma unroll
@@ -280,6 +289,7 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
   }
 
   far = __syncthreads_or(far);
+  const uint64_t marked = __ballot(odd[lane] != 0);  // so far: A's nodes may mark more
 
   // ---- A and Q, tile by tile of the lower triangle; in registers until every wave has
   // read what they replace
@@ -315,16 +325,16 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
       for (int e = 0; e < 4; ++e) {
         const int t = 16 * ti + 4 * g + e, s = 16 * tj + col;
         const bool on = way[t] >> s & 1;
-        am[t * LN + s] = on && s != t ? at[m][e] : 0.f;
+        am[t * LN + s] = kept(on && s != t ? at[m][e] : 0.f, odd + t);
         wm[t * LN + s] = on ? qt[m][e] : 0.f;
       }
     }
   } else {
-    tree_pairs<D, In>(a, way, odd, good, row0, h, N, LN, WAVES, am, wm);
+    tree_pairs<D, In>(a, way, odd, marked, good, row0, h, N, LN, WAVES, am, wm);
   }
   __syncthreads();
 
-  invert_diagonal<NT>(am, LN, wv, lane);
+  invert_diagonal<NT>(am, LN, odd, wv, lane);
   __syncthreads();
   if (wv < NT) solve_row<LN>(am, wm, wv, g, col);
   __syncthreads();
@@ -430,8 +440,8 @@ __device__ __forceinline__ uint32_t split2(float x, float y, uint32_t* lo) {
 }
 // Bits 15 and 31 are set where the word's bf16 values are infinite or NaN.
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) { return (w & 0x7f807f80u) + 0x00800080u; }
-// Four values as parts, to two places 8 bytes long.
-__device__ __forceinline__ void put_parts(uint16_t* hi, uint16_t* lo, const f32x4& x) {
+// Four values as parts, to two places 8 bytes long; whether the upper ones are finite.
+__device__ __forceinline__ bool put_parts(uint16_t* hi, uint16_t* lo, const f32x4& x) {
   u32x2_t h, l;
   uint32_t w;
   h[0] = split2(x[0], x[1], &w);
@@ -440,6 +450,7 @@ __device__ __forceinline__ void put_parts(uint16_t* hi, uint16_t* lo, const f32x
   l[1] = w;
   *reinterpret_cast<u32x2_t*>(hi) = h;
   *reinterpret_cast<u32x2_t*>(lo) = l;
+  return !((not_finite2(h[0]) | not_finite2(h[1])) & 0x80008000u);
 }
 
 template <int D, int NT>
@@ -655,12 +666,17 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS), (TreeShape16<D, NT>:
         x[e] = beta * k[e] * __builtin_amdgcn_exp2f(-y);
       }
       const int to = node * LC + 16 * (CT * wv + i) + 4 * g;
-      put_parts(kb + to, kb + N * LC + to, khat[i][t]);
+      if (!put_parts(kb + to, kb + N * LC + to, khat[i][t])) {  // as kept()
+        odd[node] = 1;
+        khat[i][t] = zero4();
+        put_parts(kb + to, kb + N * LC + to, khat[i][t]);
+      }
       if constexpr (!THIN) put_parts(qb + to, qb + N * LC + to, qhat[i][t]);
-      put_parts(xb + to, xb + N * LC + to, x);
+      far |= !put_parts(xb + to, xb + N * LC + to, x);
     }
   }
   far = __syncthreads_or(far);
+  const uint64_t marked = __ballot(odd[lane] != 0);  // so far: A's nodes may mark more
 
   // ---- A and Q, tile by tile of the lower triangle; in registers until every wave has
   // read what they replace
@@ -735,15 +751,16 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS), (TreeShape16<D, NT>:
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int t = 16 * ti + 4 * g + e, s = 16 * tj + col;
-          to[t * LN + s] = (way[t] >> s & 1) && (second || s != t) ? got[turn][m][e] : 0.f;
+          const float y = (way[t] >> s & 1) && (second || s != t) ? got[turn][m][e] : 0.f;
+          to[t * LN + s] = second ? y : kept(y, odd + t);
         }
       }
     }
   } else {
-    tree_pairs<D, uint16_t>(a, way, odd, good, row0, h, N, LN, WAVES, am, wm);
+    tree_pairs<D, uint16_t>(a, way, odd, marked, good, row0, h, N, LN, WAVES, am, wm);
   }
   __syncthreads();
-  invert_diagonal<NT>(am, LN, wv, lane);
+  invert_diagonal<NT>(am, LN, odd, wv, lane);
   __syncthreads();
   // ---- W = Q (I + A)^-1, and its parts
   if (wv < NT) solve_row<LN>(am, wm, wv, g, col);

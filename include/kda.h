@@ -641,7 +641,9 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
  * chain's to rounding, not to the bit.  g >= -104 counts, below it as -104 (whose
  * exponential is 0 in fp32).  A node with a k, v or beta that is infinite or NaN, or a g
  * that is NaN or +inf, is NaN in every channel, and so are the nodes that follow it;
- * other nodes are not touched by it.
+ * other nodes are not touched by it.  The same holds where finite inputs pass fp32's range:
+ * k exp(the gates summed on the node's way), for gates above 0, or the products of its key
+ * with those before it.
  * Device-side: a request whose page index is outside [0, num_pages) gets NaN rows.
  */
 kda_status kda_decode_tree(const kda_pool* pool, const void* q, const void* k, const void* v,
