@@ -156,10 +156,11 @@ kda_status ship_seqs(const std::vector<KvSeq>& seqs, void* ws, KvBatch* b, hipSt
 }
 
 // KDA_VALIDATE=1: the pages a call needs, read back and checked.  `write`: the
-// pages that receive tokens have to be distinct between requests.
+// pages that receive tokens have to be distinct between requests; those among them
+// that hold slots past a request's len, up to start + slots, need not exist.
 kda_status check_pages(const kda_kv_pool* p, const int32_t* table, int32_t max_pages,
                        const std::vector<KvSeq>& seqs, int32_t window, int32_t sinks, bool write, bool reads,
-                       hipStream_t st) {
+                       hipStream_t st, int32_t slots = 0) {
   std::vector<int32_t> t(seqs.size() * (size_t)max_pages);
   if (t.empty()) return KDA_OK;
   hipError_t e = hipMemcpyAsync(t.data(), table, t.size() * 4, hipMemcpyDeviceToHost, st);
@@ -168,19 +169,21 @@ kda_status check_pages(const kda_kv_pool* p, const int32_t* table, int32_t max_p
   std::unordered_set<int32_t> written;
   for (size_t i = 0; i < seqs.size(); ++i) {
     const KvSeq& s = seqs[i];
-    if (s.start < 0 || s.len == 0) continue;
-    const int64_t end = (int64_t)s.start + s.len;
+    if (s.start < 0 || (s.len == 0 && slots == 0)) continue;
+    const int64_t end = (int64_t)s.start + s.len, all = std::max(end, (int64_t)s.start + slots);
     if (end > (int64_t)max_pages * p->page_tokens)
       return fail(KDA_ERR_PAGE_RANGE, "request %zu: %lld tokens pass its table row", i, (long long)end);
-    for (int64_t j = 0; j * p->page_tokens < end; ++j) {
+    for (int64_t j = 0; j < max_pages && j * p->page_tokens < all; ++j) {
       const int64_t a = j * p->page_tokens, b = a + p->page_tokens;
-      const bool wr = write && b > s.start;
+      const bool needed = s.len > 0 && a < end, wr = write && b > s.start;
       // the first row's window reaches furthest back
       const bool rd = reads && (!window || a < sinks || b > (int64_t)s.start - window + 1);
       if (!wr && !rd) continue;
       const int32_t pg = t[i * max_pages + j];
-      if (pg < 0 || pg >= p->num_pages)
+      if (pg < 0 || pg >= p->num_pages) {
+        if (!needed) continue;
         return fail(KDA_ERR_PAGE_RANGE, "page_table[%zu][%lld] = %d", i, (long long)j, pg);
+      }
       if (wr && !written.insert(pg).second)
         return fail(KDA_ERR_PAGE_ALIAS, "page %d receives tokens of two requests", pg);
     }
@@ -543,7 +546,8 @@ kda_status append_step(const char* what, const kda_kv_pool* pool, const kda_rope
   if (validating()) {
     std::vector<KvSeq> seqs;
     s = tree ? tree_seqs(pos, parent, n, tokens, &seqs, st) : step_seqs(pos, n, tokens, &seqs, st);
-    if (s == KDA_OK) s = check_pages(pool, page_table, max_pages, seqs, 0, 0, true, false, st);
+    // every slot of a tree is written, zeros behind its last node too
+    if (s == KDA_OK) s = check_pages(pool, page_table, max_pages, seqs, 0, 0, true, false, st, tree ? tokens : 0);
     if (s != KDA_OK) return s;
   }
   KvAppendArgs a = append_args(pool, rope, q, k, v, q_ld, k_ld, v_ld, q_out, num_q_heads, page_table, max_pages, rows);

@@ -683,7 +683,9 @@ kda_status kda_short_conv_commit(const kda_conv_pool* cpool, const void* x, int3
  * kda_kv_append_step for trees: entry t goes to cache slot pos[r] + t, rotated (with
  * its q row) by its position, pos[r] + depth.  Entries that are no nodes, bad ones and
  * nodes at positions past rope->num_pos store zeros in their slots (q_out: 0, NaN,
- * NaN).  The slots from pos[r] on hold the draft until kda_kv_commit.  In a KDA_INT8
+ * NaN), so that all pages with slots pos[r] .. pos[r] + tokens - 1 are written and may not
+ * be another request's; those past the last node need not exist.  The slots from pos[r]
+ * on hold the draft until kda_kv_commit.  In a KDA_INT8
  * cache all nodes count for the scale of the block that they share with older tokens,
  * as in kda_kv_append, whether they are accepted or not.
  */
