@@ -652,23 +652,12 @@ kda_status kda_kv_commit(const kda_kv_pool* pool, int32_t n, int32_t tokens, con
     if ((int64_t)n * pool->num_heads * 2 > kMaxGroups) return fail(KDA_ERR_SHAPE, "too much work for one call");
     hipStream_t st = reinterpret_cast<hipStream_t>(stream);
     if (validating()) {
-      std::vector<int32_t> c((size_t)n), p((size_t)n * tokens);
-      hipError_t e = hipMemcpyAsync(c.data(), count, c.size() * 4, hipMemcpyDeviceToHost, st);
-      if (e == hipSuccess) e = hipMemcpyAsync(p.data(), path, p.size() * 4, hipMemcpyDeviceToHost, st);
-      if (e == hipSuccess) e = hipStreamSynchronize(st);
-      if (e != hipSuccess) return hip_fail(e, "path read-back");
+      std::vector<int32_t> c, p;
+      s = check_paths("kda_kv_commit", path, count, n, tokens, &p, &c, st);
       std::vector<KvSeq> seqs;
-      s = step_seqs(pos, n, tokens, &seqs, st);
+      if (s == KDA_OK) s = step_seqs(pos, n, tokens, &seqs, st);
       if (s != KDA_OK) return s;
-      for (int32_t i = 0; i < n; ++i) {
-        if (c[i] < 0 || c[i] > tokens) return fail(KDA_ERR_SEQ, "request %d: count %d outside [0, tokens]", i, c[i]);
-        for (int32_t j = 0, before = -1; j < c[i]; ++j) {
-          const int32_t t = p[(size_t)i * tokens + j];
-          if (t <= before || t >= tokens) return fail(KDA_ERR_SEQ, "request %d: path[%d] = %d", i, j, t);
-          before = t;
-        }
-        seqs[i].len = c[i] ? p[(size_t)i * tokens + c[i] - 1] + 1 : 0;
-      }
+      for (int32_t i = 0; i < n; ++i) seqs[i].len = c[i] ? p[(size_t)i * tokens + c[i] - 1] + 1 : 0;
       s = check_pages(pool, page_table, max_pages, seqs, 0, 0, true, false, st);
       if (s != KDA_OK) return s;
     }

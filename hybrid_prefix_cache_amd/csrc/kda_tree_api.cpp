@@ -48,17 +48,44 @@ kda_status check_pages(const char* what, int32_t num_pages, int32_t n, const int
   return KDA_OK;
 }
 
-kda_status validated(const char* what, int32_t num_pages, int32_t n, const int32_t* page_in, const int32_t* page_out,
-                     hipStream_t st) {
+kda_status validated(const char* what, int32_t num_pages, int32_t n, const int32_t* page_in, hipStream_t st) {
   if (!validating()) return KDA_OK;
   try {
-    return check_pages(what, num_pages, n, page_in, page_out, st);
+    return check_pages(what, num_pages, n, page_in, nullptr, st);
+  } catch (...) {
+    return fail(KDA_ERR_WORKSPACE, "out of host memory");
+  }
+}
+kda_status validated_commit(const char* what, int32_t num_pages, int32_t n, int32_t tokens, const int32_t* path,
+                            const int32_t* count, const int32_t* page_in, const int32_t* page_out, hipStream_t st) {
+  if (!validating()) return KDA_OK;
+  try {
+    std::vector<int32_t> p, c;
+    const kda_status s = check_paths(what, path, count, n, tokens, &p, &c, st);
+    return s == KDA_OK ? check_pages(what, num_pages, n, page_in, page_out, st) : s;
   } catch (...) {
     return fail(KDA_ERR_WORKSPACE, "out of host memory");
   }
 }
 
 }  // namespace
+
+kda_status kda::check_paths(const char* what, const int32_t* path, const int32_t* count, int32_t n, int32_t tokens,
+                            std::vector<int32_t>* p, std::vector<int32_t>* c, hipStream_t st) {
+  p->resize((size_t)n * tokens);
+  c->resize((size_t)n);
+  hipError_t e = hipMemcpyAsync(c->data(), count, c->size() * 4, hipMemcpyDeviceToHost, st);
+  if (e == hipSuccess) e = hipMemcpyAsync(p->data(), path, p->size() * 4, hipMemcpyDeviceToHost, st);
+  if (e == hipSuccess) e = hipStreamSynchronize(st);
+  if (e != hipSuccess) return hip_fail(e, "path read-back");
+  for (int32_t r = 0; r < n; ++r) {
+    const int32_t m = (*c)[r], *row = p->data() + (size_t)r * tokens;
+    if (m < 0 || m > tokens) return fail(KDA_ERR_SEQ, "%s: request %d: count %d outside [0, tokens]", what, r, m);
+    for (int32_t i = 0, before = -1; i < m; before = row[i++])
+      if (row[i] <= before || row[i] >= tokens) return fail(KDA_ERR_SEQ, "%s: request %d: path[%d] = %d", what, r, i, row[i]);
+  }
+  return KDA_OK;
+}
 
 extern "C" {
 
@@ -77,7 +104,7 @@ kda_status kda_decode_tree(const kda_pool* pool, const void* q, const void* k, c
   for (const void* p : {q, k, v, g, static_cast<const void*>(o)})
     if (!aligned(p, 16)) return fail(KDA_ERR_SHAPE, "%s: q, k, v, g and o must be 16-byte aligned", what);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  s = validated(what, pool->num_pages, n, page_in, nullptr, st);
+  s = validated(what, pool->num_pages, n, page_in, st);
   if (s != KDA_OK) return s;
   const TreeArgs a{q, k, v, g, beta, o, parent, page_in, static_cast<const uint8_t*>(pool->base), pool->page_bytes,
                    pool->num_pages, pool->num_heads, out_dtype == KDA_BF16, n, tokens};
@@ -100,7 +127,7 @@ kda_status kda_decode_commit(const kda_pool* pool, const void* k, const void* v,
   for (const void* p : {k, v, g})
     if (!aligned(p, 16)) return fail(KDA_ERR_SHAPE, "%s: k, v and g must be 16-byte aligned", what);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  s = validated(what, pool->num_pages, n, page_in, page_out, st);
+  s = validated_commit(what, pool->num_pages, n, tokens, path, count, page_in, page_out, st);
   if (s != KDA_OK) return s;
   const StateCommitArgs a{k, v, g, beta, path, count, page_in, page_out, static_cast<uint8_t*>(pool->base),
                           pool->page_bytes, pool->num_pages, pool->num_heads, n, tokens};
@@ -127,7 +154,7 @@ kda_status kda_short_conv_tree(const kda_conv_pool* cpool, const void* x, const 
   if ((int64_t)n * groups >= (int64_t)1 << 24)
     return fail(KDA_ERR_SHAPE, "%s: n * tokens * channels too large", what);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  s = validated(what, cpool->num_pages, n, page_in, nullptr, st);
+  s = validated(what, cpool->num_pages, n, page_in, st);
   if (s != KDA_OK) return s;
   const ConvTreeArgs a{x, w, y, parent, page_in, static_cast<const uint8_t*>(cpool->base), cpool->page_bytes,
                        cpool->num_pages, n, tokens, cpool->channels, cpool->width, cpool->dtype == KDA_BF16,
@@ -151,7 +178,7 @@ kda_status kda_short_conv_commit(const kda_conv_pool* cpool, const void* x, int3
   const int64_t groups = (cpool->channels / (cpool->dtype == KDA_BF16 ? 8 : 4) + 255) / 256;
   if (n * groups >= (int64_t)1 << 24) return fail(KDA_ERR_SHAPE, "%s: n * channels too large", what);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
-  s = validated(what, cpool->num_pages, n, page_in, page_out, st);
+  s = validated_commit(what, cpool->num_pages, n, tokens, path, count, page_in, page_out, st);
   if (s != KDA_OK) return s;
   const ConvCommitArgs a{x, path, count, page_in, page_out, static_cast<uint8_t*>(cpool->base), cpool->page_bytes,
                          cpool->num_pages, n, tokens, cpool->channels * (cpool->dtype == KDA_BF16 ? 2 : 4), cpool->width};

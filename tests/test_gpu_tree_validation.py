@@ -4,6 +4,7 @@ import torch
 
 import hybrid_prefix_cache_amd as K
 from test_gpu_tree_attn import Draft, ints
+from test_gpu_tree_state import Conv, States
 from tree_util import tree
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +36,23 @@ def test_append_writes_the_slots_behind_the_last_node(validate, row, pos):
     call(table)
     call(table[:, :2].contiguous())
     call(x.f.table)
+
+
+@pytest.mark.parametrize("path,count", [([2, 1, 0, 0, 0], 2), ([1, 1, 0, 0, 0], 2), ([0, 5, 0, 0, 0], 2), ([-1, 1, 0, 0, 0], 1),
+                                        ([0, 1, 2, 3, 4], 6), ([0, 0, 0, 0, 0], -1)])
+def test_commits_refuse_bad_paths(validate, path, count):
+    """In every layer kind, the bad path a later request's."""
+    trees = [tree("binary", 5)] * 2
+    path, count = ints([[0, 1, 3, -9, -9], path]), ints([3, count])
+    x, c = States(trees, 1, 64, "bf16"), Conv(trees, 64, 4, "bf16")
+    before, a, pages = (x.pb.buf.clone(), c.buf.clone()), x.x, ints([0, 1])
+    d = Draft([40, 60], trees, 1, 2, 64, 32, "int8", "bf16")
+    calls = (lambda p, m: K.kda_decode_commit(x.pb.pool, a["k"], a["v"], a["g"], a["beta"], p, m, pages, pages),
+             lambda p, m: K.kda_short_conv_commit(c.pool, c.x, p, m, pages, pages),
+             lambda p, m: K.kda_kv_commit(d.f.kb.pool, p, m, d.pos, d.f.table))
+    for call in calls:
+        refused(K.KDA_ERR_SEQ, lambda: call(path, count))
+    torch.cuda.synchronize()
+    assert torch.equal(before[0], x.pb.buf) and torch.equal(before[1], c.buf)
+    for call in calls:  # what is behind a path's end is not read
+        call(ints([[0, 1, 3, -9, -9], [4, 2, 9, 9, 9]]), ints([3, 1]))
