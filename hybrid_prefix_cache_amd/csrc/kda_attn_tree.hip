@@ -457,10 +457,11 @@ template <int D> __global__ __launch_bounds__(128 * kFewGroups) void attn_tree_f
 }
 
 template <int D, int EB, int NP, int FEW, int MANY> static void launch_rows(const AttnArgs& a, hipStream_t st) {
-  const dim3 grid((unsigned)((int64_t)a.units * a.c.H * a.splits));
-  if (a.tile_rows != kFewRows) hipLaunchKernelGGL((attn_tree_kernel<D, EB, NP, MANY, 4, 2>), grid, dim3(512), 0, st, a);
-  else if constexpr (EB == 1 && NP == 1) hipLaunchKernelGGL((attn_tree_few_kernel<D>), grid, dim3(128 * kFewGroups), 0, st, a);
-  else hipLaunchKernelGGL((attn_tree_kernel<D, EB, NP, FEW, 2, 2>), grid, dim3(256), 0, st, a);
+  static_assert(128 * kFewGroups == 512, "attn_tree_threads");
+  const dim3 grid((unsigned)((int64_t)a.units * a.c.H * a.splits)), block(attn_tree_threads(NP == 1, EB == 1, a.tile_rows));
+  if (a.tile_rows != kFewRows) hipLaunchKernelGGL((attn_tree_kernel<D, EB, NP, MANY, 4, 2>), grid, block, 0, st, a);
+  else if constexpr (EB == 1 && NP == 1) hipLaunchKernelGGL((attn_tree_few_kernel<D>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((attn_tree_kernel<D, EB, NP, FEW, 2, 2>), grid, block, 0, st, a);
 }
 // parts of a weight: as in the tiled kernel
 template <int D> static void launch_tree_d(bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st) {

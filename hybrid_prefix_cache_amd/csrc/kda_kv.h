@@ -105,6 +105,10 @@ constexpr int kFewRows = 64;     // rows of a sequence and head that are few to 
 // tiles in one wave cost the second workgroup of a CU: 24 requests of 35 rows over
 // 5000 tokens took 57 us there, 39 us in 128-row tiles; 64 of 20 rows 80 against 102.
 constexpr int kDecodeRows = 32;
+// Threads of a workgroup of launch_attn_tree's kernels.
+inline int attn_tree_threads(bool in_bf16, bool int8, int tile_rows) {
+  return tile_rows == kFewRows && !(in_bf16 && int8) ? 256 : 512;
+}
 
 hipError_t launch_attn_decode(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);
 hipError_t launch_attn_tiled(int D, bool in_bf16, bool int8, const AttnArgs& a, hipStream_t st);

@@ -506,7 +506,8 @@ kda_status attend_step(const char* what, const kda_kv_pool* pool, const void* q,
   if (s != KDA_OK) return s;
   const AttnPlan pl = tree ? plan_tree(pool, num_q_heads, n, tokens, max_pages, window, sinks)
                            : plan_decode(pool, num_q_heads, n, tokens, max_pages, window, sinks);
-  if (pl.units * pool->num_heads * pl.splits > kMaxGroups || rows * num_q_heads > kMaxTokens)
+  const bool wide = tree && !pl.decode && attn_tree_threads(in_dtype == KDA_BF16, pool->dtype == KDA_INT8, pl.tile_rows) > 256;
+  if (pl.units * pool->num_heads * pl.splits > (wide ? kMaxGroups / 2 : kMaxGroups) || rows * num_q_heads > kMaxTokens)
     return fail(KDA_ERR_SHAPE, "too much work for one call");
   s = check_workspace(workspace, workspace_bytes, std::max<size_t>(256, pl.bytes));
   if (s != KDA_OK) return s;

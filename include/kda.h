@@ -703,6 +703,9 @@ kda_status kda_kv_append_tree(const kda_kv_pool* pool, const kda_rope* rope, con
  * hold does not reach it, as that section says of tokens a row does not see.  Rows of a
  * request whose pos[r] + tokens passes max_pages * page_tokens are NaN; pos[r] < 0: 0.
  * Weights are rounded as in kda_attn_decode.  workspace: kda_attn_tree_workspace_bytes.
+ * Past 32 rows a request and key/value head a workgroup takes 64 of them (128 past 64), and
+ * a call is refused if it needs 2^23 or more (2^24 up to 64 rows, with fp32 q or a KDA_BF16
+ * cache).
  */
 size_t kda_attn_tree_workspace_bytes(const kda_kv_pool* pool, int32_t num_q_heads, int32_t n,
                                      int32_t tokens, int32_t max_pages, int32_t window,
