@@ -488,6 +488,33 @@ kda_status tree_seqs(const int32_t* pos, const int32_t* parent, int32_t n, int32
   return KDA_OK;
 }
 
+// The pages of accepted paths, read back and checked: those with the slots that receive
+// their rows, distinct between requests, and those the rows come from.
+kda_status check_commit_pages(const kda_kv_pool* p, const int32_t* table, int32_t max_pages, const int32_t* pos,
+                              const std::vector<int32_t>& path, const std::vector<int32_t>& count, int32_t n,
+                              int32_t tokens, hipStream_t st) {
+  std::vector<KvSeq> seqs;
+  kda_status s = step_seqs(pos, n, tokens, &seqs, st);
+  if (s != KDA_OK) return s;
+  for (int32_t i = 0; i < n; ++i) seqs[i].len = count[i];
+  s = check_pages(p, table, max_pages, seqs, 0, 0, true, false, st);
+  if (s != KDA_OK) return s;
+  std::vector<int32_t> t((size_t)n * max_pages);
+  hipError_t e = hipMemcpyAsync(t.data(), table, t.size() * 4, hipMemcpyDeviceToHost, st);
+  if (e == hipSuccess) e = hipStreamSynchronize(st);
+  if (e != hipSuccess) return hip_fail(e, "page table read-back");
+  for (int32_t i = 0; i < n; ++i) {
+    for (int32_t k = 0; k < count[i] && seqs[i].start >= 0; ++k) {
+      const int64_t j = ((int64_t)seqs[i].start + path[(size_t)i * tokens + k]) / p->page_tokens;
+      if (j >= max_pages) return fail(KDA_ERR_PAGE_RANGE, "request %d: its path passes its table row", i);
+      const int32_t pg = t[(size_t)i * max_pages + j];
+      if (pg < 0 || pg >= p->num_pages)
+        return fail(KDA_ERR_PAGE_RANGE, "page_table[%d][%lld] = %d", i, (long long)j, pg);
+    }
+  }
+  return KDA_OK;
+}
+
 // The attention step over n requests of `tokens` rows each; parent: the rows are a tree.
 kda_status attend_step(const char* what, const kda_kv_pool* pool, const void* q, kda_dtype in_dtype, int64_t q_ld,
                        void* o, kda_dtype out_dtype, int32_t num_q_heads, float scale, int32_t window, int32_t sinks,
@@ -655,11 +682,7 @@ kda_status kda_kv_commit(const kda_kv_pool* pool, int32_t n, int32_t tokens, con
     if (validating()) {
       std::vector<int32_t> c, p;
       s = check_paths("kda_kv_commit", path, count, n, tokens, &p, &c, st);
-      std::vector<KvSeq> seqs;
-      if (s == KDA_OK) s = step_seqs(pos, n, tokens, &seqs, st);
-      if (s != KDA_OK) return s;
-      for (int32_t i = 0; i < n; ++i) seqs[i].len = c[i] ? p[(size_t)i * tokens + c[i] - 1] + 1 : 0;
-      s = check_pages(pool, page_table, max_pages, seqs, 0, 0, true, false, st);
+      if (s == KDA_OK) s = check_commit_pages(pool, page_table, max_pages, pos, p, c, n, tokens, st);
       if (s != KDA_OK) return s;
     }
     const KvCommitArgs a{cache_of(pool, page_table, max_pages), pos, path, count, n, tokens};

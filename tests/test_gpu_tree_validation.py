@@ -56,3 +56,32 @@ def test_commits_refuse_bad_paths(validate, path, count):
     assert torch.equal(before[0], x.pb.buf) and torch.equal(before[1], c.buf)
     for call in calls:  # what is behind a path's end is not read
         call(ints([[0, 1, 3, -9, -9], [4, 2, 9, 9, 9]]), ints([3, 1]))
+
+
+@pytest.mark.parametrize("cache", ["int8", "bf16"])
+def test_commit_needs_the_pages_of_its_path_alone(validate, cache):
+    """Slots 30, 70 of pages of 32 tokens: the page between is not touched, and need not be there; the other
+    two are needed, and the one that receives the rows is no other request's."""
+    row = [-1] + [-2] * 39 + [0]
+    x = Draft([30, 10], [row] * 2, 2, 2, 64, 32, cache, "bf16")
+    x.append()
+    path, count = ints([[0, 40] + [-1] * 39, [0, 40] + [-1] * 39]), ints([2, 0])
+    call = lambda t: K.kda_kv_commit(x.f.kb.pool, path, count, x.pos, t)
+    table = x.f.table.clone()
+    for j in (0, 2):
+        table[0, j] = -1
+        refused(K.KDA_ERR_PAGE_RANGE, lambda: call(table))
+        table[0, j] = x.f.table[0, j]
+    refused(K.KDA_ERR_PAGE_RANGE, lambda: call(table[:, :2].contiguous()))
+    count[1] = 2
+    table[1, 0] = table[0, 0]
+    refused(K.KDA_ERR_PAGE_ALIAS, lambda: call(table))
+    count[1] = 0
+    start = x.f.kb.buf.clone()
+    call(x.f.table)
+    want = x.f.kb.buf.clone()
+    assert not torch.equal(start, want)
+    x.f.kb.buf.copy_(start)
+    table[0, 1] = -1
+    call(table)
+    assert torch.equal(x.f.kb.buf, want)
