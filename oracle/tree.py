@@ -189,3 +189,50 @@ class Pages:
         for s, d in moves:
             self.refs[d], self.refs[s] = self.refs[s], 0
         return moves
+
+
+def closed_form(q, k, v, g, beta, row, S0, parts):
+    """One request's o [T, H, d] by the closed form in the roundings that a kernel has: every
+    product and sum in fp32, one after the other; parts: the operands in two bf16 parts, products
+    of upper with lower ones, but not of two lower ones (0: in fp32; 1: without lower parts).
+    exp(G_t - G_s) as the product of exp(G_t) and exp(-G_s) up to |G| of 60 (fp32: 16), past it
+    pair by pair in fp32."""
+    f, log2e = np.float32, np.float32(1.44269504)
+
+    def split(x):
+        if not parts:
+            return [x]
+        hi = A.bf16(x).astype(f)
+        return [hi, A.bf16(x - hi).astype(f)] if parts == 2 else [hi]
+
+    def dot(a, b):  # a [m, n], b [n, j] in parts
+        s = np.zeros((a[0].shape[0], b[0].shape[1]), f)
+        for x, y in [(a[0], b[0]), *[(x, b[0]) for x in a[1:]], *[(a[0], y) for y in b[1:]]]:
+            for i in range(x.shape[1]):
+                s = s + x[:, i: i + 1] * y[i: i + 1]
+        return s
+
+    T, H, d = q.shape
+    o, w = np.zeros((T, H, d)), ways(row)
+    on = np.array([[s in (x or ()) for s in range(T)] for x in w])
+    for h in range(H):
+        qh, kh, vh, gh, bh = (np.where(on.any(1).reshape(-1, *[1] * (x.ndim - 2)), x[:, h], 0).astype(f) for x in (q, k, v, g, beta))
+        G = np.array([np.maximum(gh[x], f(-104)).sum(0, dtype=f) if x else np.zeros(d, f) for x in w])
+        Kh, Qh = kh * np.exp2(G * log2e), qh * np.exp2(G * log2e)
+        if np.abs(G).max() <= (60 if parts else 16):
+            x = [y.T for y in split(bh[:, None] * kh * np.exp2(-G * log2e))]
+            Am, Qm = dot(split(Kh), x), dot(split(Qh), x)
+        else:
+            Am, Qm = np.zeros((T, T), f), np.zeros((T, T), f)
+            for s in range(T):
+                x = kh[s] * np.exp2(np.where(on[:, s: s + 1], G - G[s], f(0)) * log2e)
+                for to, y in ((Am, kh), (Qm, qh)):
+                    to[:, s] = bh[s] * np.add.accumulate(y * x, axis=1, dtype=f)[:, -1]
+        Am, Qm = np.where(on & ~np.eye(T, dtype=bool), Am, f(0)), np.where(on, Qm, f(0))
+        W = Qm.copy()
+        for j in range(T - 2, -1, -1):
+            for i in range(j + 1, T):
+                W[:, j] -= W[:, i] * Am[i, j]
+        R = Qh - dot(split(W), split(Kh))
+        o[:, h] = dot(split(R), split(S0[h].astype(f))) + dot(split(W), [vh])
+    return o
