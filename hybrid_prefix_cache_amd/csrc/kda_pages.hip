@@ -477,9 +477,10 @@ static dim3 over(int64_t n, int per) { return dim3((unsigned)((n + per - 1) / pe
 // One launch where that is quicker.  A compaction (one launch, then six; us): 4096 entries and
 // 4000 pages 8.2, 12.8; 8192 and 8000 12.5, 13.2; 16384 and 16000 24, 16.
 constexpr int64_t kFewEntries = 8192, kFewPages = 8192;
-// Of reserve and fork, by rows of the table times the 64-entry pieces of one (one launch, then
-// three): 8 3.1, 5.9; 64 4.6, 6.2; 128 6.4, 6.0.
-static bool few_rows(int64_t rows, int max_pages) { return rows * ((max_pages + 63) / 64) <= 64; }
+// Of reserve and fork calls that give each row a page, of 10 000 pages (one launch, then three; us):
+// rows of 64 entries reserved 16 7.4, 9.8; 32 8.7, 9.8; 48 10.7, 10.3; 64 11.8, 9.6; forked 16 8.4,
+// 10.6; 32 11.0, 10.7; 64 17.7, 10.8.  Of 1024 entries 4 forks 16.7, 18.1; of 256 16 forks 12.5, 12.8.
+static bool few_rows(int64_t rows, int max_pages) { return rows <= 32 && rows * ((max_pages + 63) / 64) <= 64; }
 
 hipError_t launch_pages_reserve(const PagesArgs& a, hipStream_t st) {
   if (few_rows(a.rows, a.max_pages)) {
