@@ -105,15 +105,26 @@ template <int NT> __device__ __forceinline__ void invert_diagonal(float* am, int
   if (wv >= NT || lane >= 16) return;
   float* d = am + 16 * wv * LN + 16 * wv;
   float x[16];
+  bool ok = true;
+  auto column = [&](auto finish) {
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    f32x4 row[4];
+    for (int i = 0; i < 16; ++i) {
+      f32x4 row[4];
 #pragma unroll
-    for (int j = 0; j < (i + 3) / 4; ++j) row[j] = lds4(d + i * LN + 4 * j);
-    float y = i == lane ? 1.f : 0.f;
+      for (int j = 0; j < (i + 3) / 4; ++j) row[j] = lds4(d + i * LN + 4 * j);
+      float y = i == lane ? 1.f : 0.f;
 #pragma unroll
-    for (int j = 0; j < i; ++j) y = __builtin_fmaf(-row[j >> 2][j & 3], x[j], y);
-    x[i] = kept(y, odd + 16 * wv + i);  // 0 above the diagonal
+      for (int j = 0; j < i; ++j) y = __builtin_fmaf(-row[j >> 2][j & 3], x[j], y);
+      x[i] = finish(y, i);  // 0 above the diagonal
+    }
+  };
+  column([&](float y, int) {
+    ok &= is_finite(y);
+    return y;
+  });
+  if (!ok) {
+    asm volatile("" ::: "memory");  // rows are read again, not kept in registers for this
+    column([&](float y, int i) { return kept(y, odd + 16 * wv + i); });
   }
 #pragma unroll
   for (int i = 0; i < 16; ++i) d[i * LN + lane] = x[i];
@@ -262,15 +273,15 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
         const bool live = good >> t & 1;
         float k = live ? key[ct][4 * i + e] : 0.f, beta = live ? bt[4 * i + e] : 0.f;
         const float q = live ? query[ct][4 * i + e] : 0.f, x = live ? G[i][e] : 0.f;
-        if (!is_finite(k) || !is_finite(beta)) {
-          odd[t] = 1;
-          k = beta = 0.f;
-        }
-        far |= fabsf(x) > kFarGate<In>;
         const float up = __expf(x);
+        float kup = k * up;
+        if (!is_finite(kup) || !is_finite(beta)) {  // as kept(); k among them
+          odd[t] = 1;
+          k = beta = kup = 0.f;
+        }
         const float down = beta * k * __expf(-x);
-        far |= !is_finite(down);
-        kh[t * LD + c] = kept(k * up, odd + t);
+        far |= !(fabsf(x) <= kFarGate<In> && is_finite(down));
+        kh[t * LD + c] = kup;
         qh[t * LD + c] = q * up;
         buf[t * LD + c] = down;
       }
@@ -321,13 +332,19 @@ __global__ __launch_bounds__((TreeShape<D, NT>::THREADS)) void tree_kernel(TreeA
       const int tile = m * WAVES + wv;
       if (tile >= TILES) continue;
       const int ti = tile >= 6 ? 3 : tile >= 3 ? 2 : tile >= 1 ? 1 : 0, tj = tile - ti * (ti + 1) / 2;
+      bool ok = true;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int t = 16 * ti + 4 * g + e, s = 16 * tj + col;
         const bool on = way[t] >> s & 1;
-        am[t * LN + s] = kept(on && s != t ? at[m][e] : 0.f, odd + t);
+        at[m][e] = on && s != t ? at[m][e] : 0.f;
+        ok &= is_finite(at[m][e]);
+        am[t * LN + s] = at[m][e];
         wm[t * LN + s] = on ? qt[m][e] : 0.f;
       }
+      if (!ok)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) am[(16 * ti + 4 * g + e) * LN + 16 * tj + col] = kept(at[m][e], odd + 16 * ti + 4 * g + e);
     }
   } else {
     tree_pairs<D, In>(a, way, odd, marked, good, row0, h, N, LN, WAVES, am, wm);
@@ -649,11 +666,6 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS), (TreeShape16<D, NT>:
     for (int i = 0; i < CT; ++i) {
       u32x2_t kw = kraw[i][t], qw = qraw[i][t];
       if (!live) kw = qw = u32x2_t{0u, 0u};
-      const bool odd_k = (not_finite2(kw[0]) | not_finite2(kw[1])) & 0x80008000u;
-      if (odd_k || odd_beta) {
-        odd[node] = 1;
-        kw = u32x2_t{0u, 0u};
-      }
       const f32x4 k = {low_of(kw[0]), high_of(kw[0]), low_of(kw[1]), high_of(kw[1])};
       const f32x4 q = {low_of(qw[0]), high_of(qw[0]), low_of(qw[1]), high_of(qw[1])};
       f32x4 x;
@@ -666,9 +678,9 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS), (TreeShape16<D, NT>:
         x[e] = beta * k[e] * __builtin_amdgcn_exp2f(-y);
       }
       const int to = node * LC + 16 * (CT * wv + i) + 4 * g;
-      if (!put_parts(kb + to, kb + N * LC + to, khat[i][t])) {  // as kept()
+      if (!put_parts(kb + to, kb + N * LC + to, khat[i][t]) || odd_beta) {  // as kept(); k among them
         odd[node] = 1;
-        khat[i][t] = zero4();
+        khat[i][t] = x = zero4();
         put_parts(kb + to, kb + N * LC + to, khat[i][t]);
       }
       if constexpr (!THIN) put_parts(qb + to, qb + N * LC + to, qhat[i][t]);
@@ -748,12 +760,20 @@ __global__ __launch_bounds__((TreeShape16<D, NT>::THREADS), (TreeShape16<D, NT>:
       for (int turn = 0; turn < (THIN ? 2 : 1); ++turn) {
         const bool second = THIN ? turn : u & 1;
         float* to = second ? wm : am;
+        bool ok = true;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int t = 16 * ti + 4 * g + e, s = 16 * tj + col;
           const float y = (way[t] >> s & 1) && (second || s != t) ? got[turn][m][e] : 0.f;
-          to[t * LN + s] = second ? y : kept(y, odd + t);
+          ok &= is_finite(y);
+          to[t * LN + s] = y;
         }
+        if (!second && !ok)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float* y = am + (16 * ti + 4 * g + e) * LN + 16 * tj + col;
+            *y = kept(*y, odd + 16 * ti + 4 * g + e);
+          }
       }
     }
   } else {
