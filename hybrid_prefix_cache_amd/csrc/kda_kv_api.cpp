@@ -369,12 +369,8 @@ AttnPlan plan_decode(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens
   return pl;
 }
 
-// Trees.  Past the decode kernel's rows a tile's blocks are shared only where the tiles leave
-// half of the card's workgroups without one: a CU holds two of 64 rows over a bf16 cache, and
-// one of the kernels of eight waves (for their registers).  64 rows, 8 heads, 8, 16 and 32
-// requests of 4000 tokens, int8: 34, 49 and 66 us; counted as two a CU 46, 60 and 92.  Lengths
-// do not count: one request far longer than the others holds a call up (64 of 2054 tokens 87 us;
-// 63 of 500 and one of 100 000 1174).
+// Trees.  Past the decode kernel's rows a tile's blocks are shared only where the tiles
+// leave half of the card's workgroups without one.
 AttnPlan plan_tree(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens, int32_t max_pages, int32_t window,
                    int32_t sinks) {  // the same for every type of q: the workspace is asked for without it
   AttnPlan pl = plan_decode(p, Hq, n, tokens, max_pages, window, sinks);
@@ -382,7 +378,7 @@ AttnPlan plan_tree(const kda_kv_pool* p, int32_t Hq, int32_t n, int32_t tokens, 
   const int64_t rows = (int64_t)tokens * (Hq / p->num_heads);
   pl.tile_rows = rows <= kFewRows ? kFewRows : kTileRows;
   pl.units = (int64_t)n * ((rows + pl.tile_rows - 1) / pl.tile_rows);
-  const int64_t slots = rows <= kFewRows && p->dtype == KDA_BF16 ? 2 * kCUs : kCUs, tiles = std::max<int64_t>(1, pl.units * p->num_heads);
+  const int64_t slots = rows <= kFewRows ? 2 * kCUs : kCUs, tiles = std::max<int64_t>(1, pl.units * p->num_heads);
   const int64_t blocks = reach_blocks((int64_t)max_pages * p->page_tokens, tokens, window, sinks);
   pl.min_blocks = 16;
   pl.splits = std::max<int64_t>(1, std::min(slots / tiles, blocks / pl.min_blocks));
