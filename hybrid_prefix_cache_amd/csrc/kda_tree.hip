@@ -14,7 +14,7 @@
 //
 // Small trees are bound by memory: 64 trees of 16 nodes, 32 heads of 128, bf16, take 35 us
 // (177 MB, 5.0 TB/s).  Large ones by the chain of steps in a workgroup, of which a CU holds
-// two: 24 trees of 63 nodes take 48 us (112 MB).  One tree of 5 nodes, 8 heads of 64, fp32,
+// two: 24 trees of 63 nodes take 45 us (112 MB; fp32 90).  One tree of 5 nodes, 8 heads of 64, fp32,
 // takes 7.2 us.
 //
 // exp(G_t - G_s) is the product of exp(G_t) and exp(-G_s) where no |G| passes kFarGate (and
@@ -58,8 +58,12 @@ __device__ __forceinline__ float kept(float x, int* odd) {
 }
 
 // A and Q pair by pair, up the way of each of the wave's nodes, the gates between summed as
-// it goes, but for nodes behind a spoilt one; a lane takes channels lane, lane + 64.  Rare, and slow: 64 nodes in a chain take
-// 64 * 65 / 2 such steps.
+// it goes, but for nodes behind a spoilt one; a lane takes channels lane, lane + 64.  All of a
+// head goes this way once the gates of one channel sum past kFarGate on one way (gates of -2:
+// ways of 31 nodes with bf16 inputs, of 9 with fp32; of -20: of 4, of 1), and it is slow: a chain
+// of 64 is 64 * 65 / 2 such steps.  32 heads of 128, 24 chains of 63 nodes: bf16 366 us (46 where
+// no sum passes), fp32 528 (91); binary trees of 63 98 (45), 151 (90); 64 chains of 16 105 (35),
+// 113 (46).
 template <int D, typename In>
 __device__ __forceinline__ void tree_pairs(const TreeArgs& a, const uint64_t* way, int* odd, uint64_t spoilt, uint64_t good,
                                            int64_t row0, int h, int N, int LN, int waves, float* am, float* wm) {
@@ -430,8 +434,8 @@ template <int D, int NT> struct TreeShape16 {
   static constexpr int COLS = 2 * D * LS;        // by columns
   // THIN: Khat's place is the gates' before and Qhat's between and after, and W's parts take
   // A's place, so that a CU holds two workgroups, of 74 KB, instead of one of 126; four more
-  // barriers, and the state is asked for where registers are free (24 trees of 63 nodes: 62 ->
-  // 48 us).  Up to 32 nodes it gains nothing (48 trees of 32, with the commit: 97 us, 95 without).
+  // barriers, and the state is asked for where registers are free (24 trees of 63 nodes: 62 us
+  // without, 45).  Up to 32 nodes it gains nothing (48 trees of 32, with the commit: 97 us, 95 without).
   static constexpr bool THIN = D == 128 && NT > 2;
   static constexpr int KB = ROWS > COLS ? ROWS : COLS;  // Khat by rows, then by columns
   static constexpr int PARTS = 2 * N * LS;              // of W

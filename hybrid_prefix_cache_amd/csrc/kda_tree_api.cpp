@@ -152,7 +152,7 @@ kda_status kda_short_conv_tree(const kda_conv_pool* cpool, const void* x, const 
   // a workgroup takes 64 groups of 16 bytes of channels
   const int64_t groups = (cpool->channels / (cpool->dtype == KDA_BF16 ? 8 : 4) + 63) / 64;
   if ((int64_t)n * groups >= (int64_t)1 << 24)
-    return fail(KDA_ERR_SHAPE, "%s: n * tokens * channels too large", what);
+    return fail(KDA_ERR_SHAPE, "%s: n * channels too large", what);
   hipStream_t st = reinterpret_cast<hipStream_t>(stream);
   s = validated(what, cpool->num_pages, n, page_in, st);
   if (s != KDA_OK) return s;

@@ -639,7 +639,8 @@ kda_status kda_attn_decode(const kda_kv_pool* pool, const void* q, kda_dtype in_
  * fp32 (products on fp32 matrix instructions; for bf16 inputs those with the state and the
  * gated rows in two bf16 parts each, good to 2^-15 of the terms), so rows equal a
  * chain's to rounding, not to the bit.  g >= -104 counts, below it as -104 (whose
- * exponential is 0 in fp32).  A node with a k, v or beta that is infinite or NaN, or a g
+ * exponential is 0 in fp32).  Slower, by up to 8 times for long chains, in a head of which
+ * the gates of a channel sum past 60 on a way (fp32 inputs: 16).  A node with a k, v or beta that is infinite or NaN, or a g
  * that is NaN or +inf, is NaN in every channel, and so are the nodes that follow it;
  * other nodes are not touched by it.  The same holds where finite inputs pass fp32's range:
  * k exp(the gates summed on the node's way), for gates above 0, or the products of its key
@@ -753,7 +754,7 @@ typedef struct {
   int32_t* refs;
   int32_t* table;
   int32_t num_pages;    /* 1 .. 2^24 */
-  int32_t rows;         /* rows * max_pages at most 2^30 */
+  int32_t rows;         /* 1 .. 2^24, rows * max_pages at most 2^30 */
   int32_t max_pages;
   int32_t page_tokens;  /* max_pages * page_tokens at most 2^30 */
 } kda_page_map;
